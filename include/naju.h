@@ -314,6 +314,45 @@ naju_status_t naju_scan_fwd_noalloc(const naju_dims_t *dims, const void *h, cons
                                     const float *x0, void *y, float *x_final, float *ckpt,
                                     uint32_t *flags, void *stream);
 
+/*
+ * ---- Around the mixer layer: tokens in, losses and tokens out ----
+ * The entry points below serve the two ends of a language model built from
+ * mixer layers and its decode step.  The conventions above hold, with sizes as
+ * plain arguments: contiguous row-major tensors unless a row stride is given,
+ * `io` the type of activations, arguments checked before anything is enqueued.
+ * Token ids are int32.
+ */
+
+/*
+ * Token embedding: out[t] = scale * W[ids[t]], and zeros where ids[t] lies
+ * outside [0, vocab) (padding).  No workspace.
+ *   ids  [tokens] int32;  W [vocab][d_model] io;  out [tokens][d_model] io (written)
+ * tokens <= 2^28, vocab <= 2^30, d_model <= 2^20.
+ */
+naju_status_t naju_embed_fwd(int64_t tokens, int64_t vocab, int64_t d_model, int32_t io,
+                             const int32_t *ids, const void *W, float scale, void *out,
+                             void *stream);
+
+/*
+ * Gradient of the embedding with respect to W:
+ *     dW[v] = scale * sum over t with ids[t] == v of dout[t]
+ * summed in fp32 in the order of t within runs, without floating-point
+ * atomics: equal inputs give equal bits.  Ids outside [0, vocab) contribute
+ * nothing.
+ *   dout  [tokens][d_model] io
+ *   accumulate  0: dW is written, rows of tokens that do not occur with zeros;
+ *               nonzero: the sums are added to dW and the other rows are not
+ *               touched (an output layer that shares W has its gradient there)
+ *   dW    [vocab][d_model] fp32
+ *   ws    naju_embed_bwd_workspace_bytes() bytes, 256-byte aligned (no initial
+ *         contents needed; not used when tokens == 0)
+ */
+size_t naju_embed_bwd_workspace_bytes(int64_t tokens, int64_t vocab, int64_t d_model);
+naju_status_t naju_embed_bwd(int64_t tokens, int64_t vocab, int64_t d_model, int32_t io,
+                             const int32_t *ids, const void *dout, float scale,
+                             int32_t accumulate, float *dW, void *ws, size_t ws_bytes,
+                             void *stream);
+
 /* Thread-local description of the last non-OK status ("" if none). */
 const char *naju_last_error(void);
 

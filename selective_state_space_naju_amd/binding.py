@@ -28,7 +28,8 @@ EXPORTS = ("naju_workspace_bytes", "naju_ckpt_bytes", "naju_workspace_init",
            "naju_workspace_check", "naju_scan_fwd", "naju_scan_bwd", "naju_block_fwd",
            "naju_block_bwd", "naju_scan_step", "naju_block_step", "naju_mixer_workspace_bytes",
            "naju_mixer_fwd", "naju_mixer_bwd_workspace_bytes", "naju_mixer_bwd",
-           "naju_scan_fwd_noalloc", "naju_last_error", "naju_version")
+           "naju_scan_fwd_noalloc", "naju_embed_fwd", "naju_embed_bwd_workspace_bytes",
+           "naju_embed_bwd", "naju_last_error", "naju_version")
 
 
 class NajuError(RuntimeError):
@@ -91,6 +92,13 @@ def lib() -> ctypes.CDLL:
         L.naju_mixer_bwd.restype = st
         L.naju_scan_fwd_noalloc.argtypes = [dp] + [vp] * 12
         L.naju_scan_fwd_noalloc.restype = st
+        i64, i32, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+        L.naju_embed_fwd.argtypes = [i64, i64, i64, i32, vp, vp, f32, vp, vp]
+        L.naju_embed_fwd.restype = st
+        L.naju_embed_bwd_workspace_bytes.argtypes = [i64, i64, i64]
+        L.naju_embed_bwd_workspace_bytes.restype = sz
+        L.naju_embed_bwd.argtypes = [i64, i64, i64, i32, vp, vp, f32, i32, vp, vp, sz, vp]
+        L.naju_embed_bwd.restype = st
         L.naju_last_error.argtypes = []
         L.naju_last_error.restype = ctypes.c_char_p
         L.naju_version.argtypes = []
@@ -451,3 +459,48 @@ def mixer_bwd(xn, W_u, W_z, conv_w, W_a, a_bias, W_b, b_bias, W_B, W_C, D, W_out
                                fwd_ws.nbytes if fwd_ws is not None else 0, ws.ptr, ws.nbytes,
                                stream_handle(dev)))
     return g
+
+
+# ------------------------------------------------- around the mixer layer
+def _cached_workspace(kind, sizes, nbytes, dev) -> Workspace:
+    """Cached workspace per (device, stream, kind, sizes); nbytes() is asked once."""
+    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream, kind) + sizes
+    ws = _ws_cache.get(key)
+    if ws is None:
+        ws = _ws_cache[key] = Workspace(nbytes(), dev)
+    return ws
+
+
+def embed_fwd(ids, W, scale=1.0):
+    """out = naju_embed_fwd(ids, W, scale): scale * W[ids], zeros where an id lies outside
+    the vocabulary.  ids: int32 of any shape; W [vocab, d_model]; out ids.shape + (d_model,)."""
+    V, d = W.shape
+    dt, dev = W.dtype, W.device
+    io = _io_of(W)
+    _req(W, "W", (V, d), dt, dev)
+    _req(ids, "ids", ids.shape, torch.int32, dev)
+    out = torch.empty(tuple(ids.shape) + (d,), dtype=dt, device=dev)
+    check(lib().naju_embed_fwd(ids.numel(), V, d, io, _p(ids), _p(W), float(scale), _p(out),
+                               stream_handle(dev)))
+    return out
+
+
+def embed_bwd(ids, dout, vocab, scale=1.0, *, dW=None, ws=None):
+    """dW = naju_embed_bwd(ids, dout, vocab, scale), fp32 [vocab, d_model].  With dW given the
+    gradient is added to it (rows of tokens that do not occur are not touched)."""
+    d = dout.shape[-1]
+    dt, dev = dout.dtype, dout.device
+    io = _io_of(dout)
+    _req(ids, "ids", ids.shape, torch.int32, dev)
+    _req(dout, "dout", tuple(ids.shape) + (d,), dt, dev)
+    _opt(dW, "dW", (vocab, d), torch.float32, dev)
+    accumulate = dW is not None
+    if dW is None:
+        dW = torch.empty((vocab, d), dtype=torch.float32, device=dev)
+    T = ids.numel()
+    ws = ws or _cached_workspace(
+        "embed_bwd", (T, vocab, d),
+        lambda: lib().naju_embed_bwd_workspace_bytes(T, vocab, d), dev)
+    check(lib().naju_embed_bwd(T, vocab, d, io, _p(ids), _p(dout), float(scale),
+                               int(accumulate), _p(dW), ws.ptr, ws.nbytes, stream_handle(dev)))
+    return dW

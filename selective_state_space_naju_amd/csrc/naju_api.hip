@@ -11,13 +11,14 @@
 
 #include "../../include/naju.h"
 #include "naju_device.h"
+#include "naju_host.h"
 #include "naju_launch.h"
 
 namespace naju {
 
 static thread_local char g_err[512] = "";
 
-static naju_status_t fail(naju_status_t st, const char *fmt, ...)
+naju_status_t fail(naju_status_t st, const char *fmt, ...)
 {
     va_list ap;
     va_start(ap, fmt);
@@ -26,7 +27,7 @@ static naju_status_t fail(naju_status_t st, const char *fmt, ...)
     return st;
 }
 
-static naju_status_t hip_status(hipError_t e, const char *what)
+naju_status_t hip_status(hipError_t e, const char *what)
 {
     if (e == hipSuccess) return NAJU_OK;
     return fail(NAJU_EHIP, "%s: %s", what, hipGetErrorString(e));
@@ -104,25 +105,30 @@ static naju_status_t check_dims(const naju_dims_t *d, bool block)
 
 static bool empty(const naju_dims_t *d) { return d->batch == 0 || d->d_inner == 0; }
 
-static naju_status_t need(const void *p, const char *name, size_t align)
+naju_status_t need(const void *p, const char *name, size_t align)
 {
     if (!p) return fail(NAJU_EINVAL, "%s is NULL", name);
     if (((uintptr_t)p) % align) return fail(NAJU_EINVAL, "%s is not %zu-byte aligned", name, align);
     return NAJU_OK;
 }
 
-static naju_status_t opt(const void *p, const char *name, size_t align)
+naju_status_t opt(const void *p, const char *name, size_t align)
 {
     if (p && ((uintptr_t)p) % align)
         return fail(NAJU_EINVAL, "%s is not %zu-byte aligned", name, align);
     return NAJU_OK;
 }
 
-#define TRY(x)                                                                                 \
-    do {                                                                                       \
-        naju_status_t _s = (x);                                                                \
-        if (_s != NAJU_OK) return _s;                                                          \
-    } while (0)
+naju_status_t need_ws(const void *ws, size_t bytes, size_t need_b)
+{
+    if (!ws) return fail(NAJU_EWORKSPACE, "workspace is NULL (needs %zu bytes)", need_b);
+    if (((uintptr_t)ws) % 256) return fail(NAJU_EINVAL, "workspace is not 256-byte aligned");
+    if (bytes < need_b)
+        return fail(NAJU_EWORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need_b);
+    return NAJU_OK;
+}
+
+#define TRY NAJU_TRY
 
 static size_t ws_bytes_for(naju_op_t op, const naju_dims_t *d)
 {
@@ -134,12 +140,7 @@ static size_t ws_bytes_for(naju_op_t op, const naju_dims_t *d)
 
 static naju_status_t check_ws(naju_op_t op, const naju_dims_t *d, const void *ws, size_t bytes)
 {
-    const size_t need_b = ws_bytes_for(op, d);
-    if (!ws) return fail(NAJU_EWORKSPACE, "workspace is NULL (needs %zu bytes)", need_b);
-    if (((uintptr_t)ws) % 256) return fail(NAJU_EINVAL, "workspace is not 256-byte aligned");
-    if (bytes < need_b)
-        return fail(NAJU_EWORKSPACE, "workspace has %zu bytes, needs %zu", bytes, need_b);
-    return NAJU_OK;
+    return need_ws(ws, bytes, ws_bytes_for(op, d));
 }
 
 // The forward's argument checks other than the workspace's.
@@ -369,10 +370,7 @@ static naju_status_t mixer_common(const naju_dims_t *d, int64_t dm, const void *
     TRY(need(W_out, "W_out", 16));
     const size_t need_b = grads ? mixer_bwd_ws_bytes(d->batch, d->seqlen, d->d_inner, d->d_state)
                                 : mixer_ws_bytes(d->batch, d->seqlen, d->d_inner, d->d_state);
-    if (!ws) return fail(NAJU_EWORKSPACE, "workspace is NULL (needs %zu bytes)", need_b);
-    if (((uintptr_t)ws) % 256) return fail(NAJU_EINVAL, "workspace is not 256-byte aligned");
-    if (ws_bytes < need_b)
-        return fail(NAJU_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need_b);
+    TRY(need_ws(ws, ws_bytes, need_b));
     if (grads) {
         const MixerGrads &q = *grads;
         TRY(need(q.d_out, "d_out", 16));

@@ -1,0 +1,203 @@
+"""GPU parity of the token embedding and its gradient against the fp64 definition.
+
+Tolerances, derived before the first run.  Forward: one fp32 product, then one
+rounding to the io type: 2^-24 relative for fp32 output (the fp32 product's own
+rounding), 2^-8 for bf16 (half a spacing, 2^-9, plus the fp32 rounding that can
+move a tie).  Gradient: the sum of n rows is formed in fp32 in an order the sort
+fixes, at most n - 1 additions and one product: |err| <= n 2^-23 sum |terms|,
+with n the number of occurrences of the token.  Ids are exact: a row of a token
+that does not occur is exactly zero.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import dev, f32_dev, host, to_dev
+from oracle import lm
+from selective_state_space_naju_amd import binding as nb
+from selective_state_space_naju_amd import inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def need_gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a ROCm device")
+    nb.lib()
+
+
+def ids_dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).to(dev())
+
+
+def draw_ids(rng, T, V, kind):
+    if kind == "uniform":
+        return rng.integers(0, V, T)
+    if kind == "zipf":  # log-uniform ranks: one token has a large share
+        return np.minimum(np.exp(rng.random(T) * np.log(V + 1)).astype(np.int64) - 1, V - 1)
+    if kind == "one":
+        return np.full(T, V - 1)
+    if kind == "none":  # nothing but padding and ids past the vocabulary
+        return np.where(rng.random(T) < 0.5, -1, V + rng.integers(0, 5, T))
+    if kind == "padded":
+        return np.where(rng.random(T) < 0.3, rng.choice([-1, -7, V, V + 3, 2 ** 31 - 1], T),
+                        rng.integers(0, V, T))
+    raise ValueError(kind)
+
+
+FWD = [  # tokens, vocab, d, io, ids
+    (1, 1, 1, "f32", "uniform"),
+    (1, 100, 768, "bf16", "uniform"),
+    (7, 50, 5, "bf16", "padded"),
+    (33, 1000, 96, "f32", "padded"),
+    (300, 129, 1023, "f32", "zipf"),
+    (129, 77, 2049, "bf16", "padded"),
+    (40, 31, 4100, "f32", "uniform"),
+    (5, 9, 16, "bf16", "none"),
+]
+
+
+@pytest.mark.parametrize("case", FWD, ids=lambda c: "t%d_v%d_d%d_%s_%s" % c)
+def test_embed_fwd(case):
+    T, V, d, io, kind = case
+    print("embed_fwd", case, flush=True)
+    rng = np.random.default_rng(3)
+    W = rng.standard_normal((V, d), dtype=np.float32)
+    W = inputs.bf16_round(W) if io == "bf16" else W
+    ids = draw_ids(rng, T, V, kind)
+    got = host(nb.embed_fwd(ids_dev(ids), to_dev(W, io), 27.5))
+    ref = lm.embed_fwd(ids, W, 27.5)
+    tol = 2.0 ** -24 if io == "f32" else 2.0 ** -8
+    assert np.all(np.abs(got - ref) <= tol * np.abs(ref))
+
+
+def test_embed_fwd_padding_is_zero_whatever_the_table_holds():
+    W = torch.full((4, 24), float("inf"), device=dev())
+    out = nb.embed_fwd(ids_dev([-1, 4, 0]), W, 2.0)
+    assert torch.equal(out[:2], torch.zeros(2, 24, device=dev()))
+    assert torch.isinf(out[2]).all()
+
+
+def test_embed_fwd_keeps_the_shape_of_ids():
+    W = torch.randn(10, 6, device=dev())
+    ids = ids_dev([[1, 2, 3], [9, -1, 0]])
+    out = nb.embed_fwd(ids, W)
+    assert out.shape == (2, 3, 6)
+    assert torch.equal(out[0, 1], W[2])
+
+
+BWD = [  # tokens, vocab, d, io, ids.  Sort tiles hold 4096 ids, sum blocks 128, waves 16
+    (1, 1, 1, "f32", "uniform"),
+    (1, 50, 768, "bf16", "uniform"),
+    (16, 3, 40, "f32", "uniform"),
+    (17, 1, 300, "bf16", "one"),
+    (127, 4, 257, "f32", "zipf"),
+    (128, 2, 256, "bf16", "one"),
+    (129, 1000, 255, "bf16", "padded"),
+    (129, 2, 66, "f32", "one"),
+    (1000, 300, 96, "bf16", "zipf"),
+    (1000, 3, 515, "f32", "uniform"),
+    (2500, 513, 7, "f32", "padded"),
+    (4096, 511, 33, "bf16", "uniform"),
+    (4097, 512, 33, "bf16", "zipf"),
+    (9000, 100003, 64, "f32", "zipf"),
+    (9000, 262145, 9, "bf16", "padded"),
+    (16385, 70000, 24, "bf16", "zipf"),
+    (20000, 5, 130, "f32", "one"),
+    (40000, 40, 12, "bf16", "zipf"),
+    (300, 20, 31, "f32", "none"),
+]
+
+
+@pytest.mark.parametrize("accumulate", [False, True], ids=["write", "add"])
+@pytest.mark.parametrize("case", BWD, ids=lambda c: "t%d_v%d_d%d_%s_%s" % c)
+def test_embed_bwd(case, accumulate):
+    T, V, d, io, kind = case
+    print("embed_bwd", case, accumulate, flush=True)
+    rng = np.random.default_rng(4)
+    dout = rng.standard_normal((T, d), dtype=np.float32)
+    dout = inputs.bf16_round(dout) if io == "bf16" else dout
+    ids = draw_ids(rng, T, V, kind)
+    before = rng.standard_normal((V, d), dtype=np.float32) if accumulate else None
+    dW = f32_dev(before) if accumulate else None
+    got = host(nb.embed_bwd(ids_dev(ids), to_dev(dout, io), V, 0.75, dW=dW))
+    ok = (ids >= 0) & (ids < V)
+    ref = np.zeros((V, d))
+    size = np.zeros((V, d))
+    np.add.at(ref, ids[ok], 0.75 * dout[ok].astype(np.float64))
+    np.add.at(size, ids[ok], 0.75 * np.abs(dout[ok]).astype(np.float64))
+    n = np.bincount(ids[ok], minlength=V)[:, None]
+    if T <= 3000:  # (the oracle's own loop is slow)
+        assert np.allclose(ref, lm.embed_bwd(ids, dout, V, 0.75), rtol=1e-12, atol=1e-12)
+    if accumulate:
+        ref += before
+        size += np.abs(before) * (n > 0)
+    assert np.all(np.abs(got - ref) <= (n + 1) * 2.0 ** -23 * size)
+    if not accumulate:
+        assert np.all(got[n[:, 0] == 0] == 0)
+    else:
+        assert np.array_equal(got[n[:, 0] == 0], before[n[:, 0] == 0].astype(np.float64))
+
+
+def test_embed_bwd_equal_inputs_give_equal_bits():
+    rng = np.random.default_rng(5)
+    ids = ids_dev(draw_ids(rng, 20000, 900, "zipf"))
+    dout = torch.randn(20000, 100, device=dev())
+    first = nb.embed_bwd(ids, dout, 900)
+    for _ in range(3):
+        assert torch.equal(nb.embed_bwd(ids, dout, 900), first)
+
+
+def test_embed_bwd_non_finite_rows_stay_with_their_token():
+    ids = ids_dev([2, 0, 2, 1, -1])
+    dout = torch.ones(5, 8, device=dev())
+    dout[0, 3] = float("inf")
+    dout[3, 0] = float("nan")
+    dout[4] = float("nan")  # padding
+    dW = nb.embed_bwd(ids, dout, 4)
+    assert torch.isinf(dW[2, 3]) and torch.isnan(dW[1, 0])
+    rest = dW.clone()
+    rest[2, 3] = 2.0
+    rest[1, 0] = 1.0
+    assert torch.equal(rest, torch.tensor([1., 1., 2., 0.], device=dev())[:, None].expand(4, 8))
+
+
+def test_embed_empty_problems():
+    W = torch.randn(5, 12, device=dev())
+    assert nb.embed_fwd(ids_dev([]), W).shape == (0, 12)
+    none = torch.empty(0, 12, device=dev())
+    assert torch.equal(nb.embed_bwd(ids_dev([]), none, 5), torch.zeros(5, 12, device=dev()))
+    kept = W.clone()
+    assert torch.equal(nb.embed_bwd(ids_dev([]), none, 5, dW=kept), W)
+
+
+def test_embed_on_another_stream():
+    s = torch.cuda.Stream()
+    W = torch.randn(300, 40, device=dev())
+    ids = ids_dev(np.arange(1000) % 300)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        out = nb.embed_fwd(ids, W, 2.0)
+        dW = nb.embed_bwd(ids, out, 300, 0.5)
+    s.synchronize()
+    assert torch.equal(out, 2.0 * W[ids.long()])
+    n = torch.bincount(ids.long(), minlength=300)[:, None]
+    assert torch.allclose(dW, W * n, rtol=1e-5, atol=1e-5)
+
+
+def test_embed_refusals():
+    W = torch.randn(5, 12, device=dev())
+    ids = ids_dev([0, 1])
+    with pytest.raises(TypeError):
+        nb.embed_fwd(ids.long(), W)
+    with pytest.raises(TypeError):
+        nb.embed_fwd(ids, W.half())
+    with pytest.raises(ValueError):
+        nb.embed_fwd(ids, W[:, ::2])
+    with pytest.raises(ValueError):
+        nb.embed_bwd(ids, torch.randn(3, 12, device=dev()), 5)
+    with pytest.raises(ValueError):
+        nb.embed_bwd(ids, torch.randn(2, 12, device=dev()), 5, dW=torch.zeros(4, 12, device=dev()))
+    with pytest.raises(ValueError):
+        nb.embed_bwd(ids.cpu(), torch.randn(2, 12, device=dev()), 5)
