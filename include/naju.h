@@ -353,6 +353,53 @@ naju_status_t naju_embed_bwd(int64_t tokens, int64_t vocab, int64_t d_model, int
                              int32_t accumulate, float *dW, void *ws, size_t ws_bytes,
                              void *stream);
 
+/*
+ * Distillation from a teacher's top logits.  Per row, with student logits s,
+ * teacher entries (i_j, t_j), j < k, and temperature tau:
+ *     x_v = s_v / tau,  lse = log sum_v exp x_v
+ *     p   = softmax over the valid entries of t_j / tau
+ *     loss = tau^2 sum_j p_j (log p_j - (x_{i_j} - lse))
+ * An entry is valid when i_j lies in [0, vocab) and t_j is not -inf; shorter
+ * lists are filled up with either.  A row without a valid entry has loss 0 and
+ * gradient 0.  An index that a row lists more than once counts each time.  A
+ * student logit of -inf has probability 0 (a teacher probability above 0 there
+ * makes the loss +inf); NaN, and +inf, make the row's results NaN.  With k == 1
+ * and tau == 1 the loss is the cross entropy of a hard label.  No workspace.
+ *   logits    [rows][ld] io, the first vocab of every row's ld >= vocab elements
+ *   t_ids     [rows][k] int32;  t_logits [rows][k] fp32;  k <= 512
+ *   temperature  > 0, finite
+ *   loss, lse [rows] fp32 (written)
+ * rows, vocab <= 2^30.
+ */
+naju_status_t naju_distill_fwd(int64_t rows, int64_t vocab, int64_t k, int32_t io,
+                               const void *logits, int64_t ld, const int32_t *t_ids,
+                               const float *t_logits, float temperature, float *loss, float *lse,
+                               void *stream);
+
+/*
+ * Its gradient for the upstream gradient g of each row's loss:
+ *     dlogits_v = g tau ([any valid entry] exp(x_v - lse) - sum_{j : i_j = v} p_j)
+ * A row with g == 0 gets zeros, whatever it holds.
+ *   lse       [rows] fp32 from naju_distill_fwd on the same inputs
+ *   g         [rows] fp32
+ *   dlogits   [rows][ld_d] io: the first vocab elements of every row are written,
+ *             the others are not touched
+ */
+naju_status_t naju_distill_bwd(int64_t rows, int64_t vocab, int64_t k, int32_t io,
+                               const void *logits, int64_t ld, const int32_t *t_ids,
+                               const float *t_logits, float temperature, const float *lse,
+                               const float *g, void *dlogits, int64_t ld_d, void *stream);
+
+/*
+ * Loss and gradient in one call, for upstream gradients that are known before
+ * the loss is (a mean or a weighted sum over rows).  Arguments as above.
+ */
+naju_status_t naju_distill_fwd_bwd(int64_t rows, int64_t vocab, int64_t k, int32_t io,
+                                   const void *logits, int64_t ld, const int32_t *t_ids,
+                                   const float *t_logits, float temperature, const float *g,
+                                   float *loss, float *lse, void *dlogits, int64_t ld_d,
+                                   void *stream);
+
 /* Thread-local description of the last non-OK status ("" if none). */
 const char *naju_last_error(void);
 

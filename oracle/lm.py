@@ -26,3 +26,31 @@ def embed_bwd(ids, dout, vocab, scale):
         if 0 <= v < vocab:
             dW[v] += scale * dout[t]
     return dW
+
+
+def distill(logits, t_ids, t_logits, tau, g=None):
+    """loss, lse and (with g) the gradient of the distillation loss, row by row."""
+    R, V = logits.shape
+    loss, lse, grad = np.zeros(R), np.zeros(R), np.zeros((R, V))
+    with np.errstate(all="ignore"):
+        for r in range(R):
+            x = np.asarray(logits[r], dtype=np.float64) / tau
+            top = x.max() if np.isfinite(x.max()) else 0.0
+            lse[r] = top + np.log(np.exp(x - top).sum())
+            use = [j for j, i in enumerate(t_ids[r]) if 0 <= i < V and t_logits[r, j] != -np.inf]
+            if not use:
+                continue
+            idx = t_ids[r, use]
+            t = np.asarray(t_logits[r, use], dtype=np.float64) / tau
+            e = np.exp(t - t.max())
+            p = e / e.sum()
+            logp = t - t.max() - np.log(e.sum())
+            logq = np.where(x == -np.inf, -np.inf, x - lse[r])
+            terms = np.where(p == 0, 0.0, p * (logp - logq[idx]))
+            loss[r] = tau * tau * terms.sum()
+            if g is not None and g[r] != 0:
+                d = np.exp(logq)
+                for j, i in enumerate(idx):
+                    d[i] -= p[j]
+                grad[r] = g[r] * tau * d
+    return loss, lse, grad

@@ -29,7 +29,8 @@ EXPORTS = ("naju_workspace_bytes", "naju_ckpt_bytes", "naju_workspace_init",
            "naju_block_bwd", "naju_scan_step", "naju_block_step", "naju_mixer_workspace_bytes",
            "naju_mixer_fwd", "naju_mixer_bwd_workspace_bytes", "naju_mixer_bwd",
            "naju_scan_fwd_noalloc", "naju_embed_fwd", "naju_embed_bwd_workspace_bytes",
-           "naju_embed_bwd", "naju_last_error", "naju_version")
+           "naju_embed_bwd", "naju_distill_fwd", "naju_distill_bwd", "naju_distill_fwd_bwd",
+           "naju_last_error", "naju_version")
 
 
 class NajuError(RuntimeError):
@@ -99,6 +100,14 @@ def lib() -> ctypes.CDLL:
         L.naju_embed_bwd_workspace_bytes.restype = sz
         L.naju_embed_bwd.argtypes = [i64, i64, i64, i32, vp, vp, f32, i32, vp, vp, sz, vp]
         L.naju_embed_bwd.restype = st
+        L.naju_distill_fwd.argtypes = [i64, i64, i64, i32, vp, i64, vp, vp, f32] + [vp] * 3
+        L.naju_distill_fwd.restype = st
+        L.naju_distill_bwd.argtypes = [i64, i64, i64, i32, vp, i64, vp, vp, f32, vp, vp, vp, i64,
+                                       vp]
+        L.naju_distill_bwd.restype = st
+        L.naju_distill_fwd_bwd.argtypes = [i64, i64, i64, i32, vp, i64, vp, vp, f32, vp, vp, vp,
+                                           vp, i64, vp]
+        L.naju_distill_fwd_bwd.restype = st
         L.naju_last_error.argtypes = []
         L.naju_last_error.restype = ctypes.c_char_p
         L.naju_version.argtypes = []
@@ -504,3 +513,73 @@ def embed_bwd(ids, dout, vocab, scale=1.0, *, dW=None, ws=None):
     check(lib().naju_embed_bwd(T, vocab, d, io, _p(ids), _p(dout), float(scale),
                                int(accumulate), _p(dW), ws.ptr, ws.nbytes, stream_handle(dev)))
     return dW
+
+
+def _req_rows(t, name, shape, dtype, device) -> int:
+    """A matrix of contiguous rows, any distance apart; returns that distance."""
+    if t is None:
+        raise ValueError("%s is required" % name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    R, V = shape
+    if (V > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < V):
+        raise ValueError("%s must have contiguous rows that do not overlap" % name)
+    return t.stride(0) if R > 1 else V
+
+
+def _distill_args(logits, t_ids, t_logits, temperature):
+    if logits.dim() != 2 or t_ids.dim() != 2:
+        raise ValueError("logits and t_ids must be matrices")
+    R, V = logits.shape
+    k = t_ids.shape[1]
+    dt, dev = logits.dtype, logits.device
+    io = _io_of(logits)
+    ld = _req_rows(logits, "logits", (R, V), dt, dev)
+    _req(t_ids, "t_ids", (R, k), torch.int32, dev)
+    _req(t_logits, "t_logits", (R, k), torch.float32, dev)
+    return R, V, dev, (R, V, k, io, _p(logits), ld, _p(t_ids), _p(t_logits), float(temperature))
+
+
+def _distill_grad_out(logits, g, dlogits):
+    R, V = logits.shape
+    _req(g, "g", (R,), torch.float32, logits.device)
+    if dlogits is None:
+        dlogits = torch.empty((R, V), dtype=logits.dtype, device=logits.device)
+    return dlogits, _req_rows(dlogits, "dlogits", (R, V), logits.dtype, logits.device)
+
+
+def distill_fwd(logits, t_ids, t_logits, temperature=1.0):
+    """loss, lse = naju_distill_fwd(...), fp32 [rows] each.  logits [rows, vocab] (contiguous
+    rows, any row stride); t_ids int32 and t_logits fp32 [rows, k]: the teacher's top logits
+    (index -1 or value -inf: no entry)."""
+    R, V, dev, args = _distill_args(logits, t_ids, t_logits, temperature)
+    loss = torch.empty(R, dtype=torch.float32, device=dev)
+    lse = torch.empty(R, dtype=torch.float32, device=dev)
+    check(lib().naju_distill_fwd(*args, _p(loss), _p(lse), stream_handle(dev)))
+    return loss, lse
+
+
+def distill_bwd(logits, t_ids, t_logits, lse, g, temperature=1.0, *, dlogits=None):
+    """dlogits = naju_distill_bwd(...) for the upstream gradient g [rows] of the loss and the
+    lse that distill_fwd returned; dlogits: a tensor to write (contiguous rows, any stride)."""
+    R, V, dev, args = _distill_args(logits, t_ids, t_logits, temperature)
+    _req(lse, "lse", (R,), torch.float32, dev)
+    dlogits, ldd = _distill_grad_out(logits, g, dlogits)
+    check(lib().naju_distill_bwd(*args, _p(lse), _p(g), _p(dlogits), ldd, stream_handle(dev)))
+    return dlogits
+
+
+def distill_fwd_bwd(logits, t_ids, t_logits, g, temperature=1.0, *, dlogits=None):
+    """loss, dlogits = naju_distill_fwd_bwd(...): both in one pass over the logits, for row
+    weights g that are known before the loss."""
+    R, V, dev, args = _distill_args(logits, t_ids, t_logits, temperature)
+    loss = torch.empty(R, dtype=torch.float32, device=dev)
+    lse = torch.empty(R, dtype=torch.float32, device=dev)
+    dlogits, ldd = _distill_grad_out(logits, g, dlogits)
+    check(lib().naju_distill_fwd_bwd(*args, _p(g), _p(loss), _p(lse), _p(dlogits), ldd,
+                                     stream_handle(dev)))
+    return loss, dlogits

@@ -1,0 +1,347 @@
+// naju_distill.hip -- distillation of a student's logits from a teacher's top
+// logits: the loss of each row, its gradient, or both in one call.
+//
+// With temperature tau, student logits s_v, teacher entries (i_j, t_j):
+//     x_v = s_v / tau,  lse = log sum_v exp x_v,  q_v = exp(x_v - lse)
+//     p = softmax over the valid entries of t_j / tau
+//     loss = tau^2 sum_j p_j (log p_j - (x_{i_j} - lse))
+//     dloss/ds_v = tau ([any valid] q_v - sum_{j : i_j = v} p_j)
+// An entry is valid when its index lies in [0, V) and t_j is not -inf.  One
+// entry and tau = 1 make the loss the cross entropy of a hard label.
+//
+// The rows are long (tens of thousands of logits) and the entries few, so a
+// workgroup takes a row, streams it with 16-byte accesses and keeps one entry
+// per thread; statistics and sums are fp32, each rounded once on output.
+#include <math.h>
+
+#include "naju_device.h"
+#include "naju_host.h"
+#include "naju_launch.h"
+#include "naju_vec.h"
+
+namespace naju {
+
+constexpr int kDistThreads = 512;
+constexpr int kDistWaves = kDistThreads / 64;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// running maximum and sum of exp(. - maximum)
+struct MaxSum {
+    float m, s;
+};
+
+__device__ __forceinline__ float exp_nat(float d) { return ex2(d * kLog2e); }
+// the exponent base of a row or list without any finite value is 0, not -inf
+__device__ __forceinline__ float base_of(float m) { return m == kNegInf ? 0.f : m; }
+
+__device__ __forceinline__ MaxSum wave_maxsum(MaxSum a)
+{
+    float M = a.m;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
+    float s = a.s * exp_nat(a.m - base_of(M));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    return {M, s};
+}
+
+__device__ __forceinline__ MaxSum join_maxsum(const MaxSum *w)
+{
+    float M = w[0].m;
+#pragma unroll
+    for (int i = 1; i < kDistWaves; ++i) M = fmaxf(M, w[i].m);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDistWaves; ++i) s += w[i].s * exp_nat(w[i].m - base_of(M));
+    return {M, s};
+}
+
+// One teacher entry per thread.
+struct Entry {
+    int id;      // -1: not valid
+    float t;     // t / tau, -inf if not valid
+};
+
+__device__ __forceinline__ Entry load_entry(const int32_t *t_ids, const float *t_logits, int k,
+                                            int64_t V, float inv_tau)
+{
+    Entry e{-1, kNegInf};
+    if ((int)threadIdx.x < k) {
+        const int id = t_ids[threadIdx.x];
+        const float t = t_logits[threadIdx.x];
+        if (id >= 0 && id < V && t != kNegInf) {
+            e.id = id;
+            e.t = t * inv_tau;
+        }
+    }
+    return e;
+}
+__device__ __forceinline__ MaxSum entry_maxsum(const Entry &e)
+{
+    return wave_maxsum({e.t, e.id >= 0 ? exp_nat(e.t - base_of(e.t)) : 0.f});
+}
+
+// ------------------------------------------------------------------ loss
+// Reads the row once with a running maximum and sum per thread.
+template <typename IO>
+__global__ __launch_bounds__(kDistThreads) void distill_loss_kernel(
+    const int64_t R, const int64_t V, const int k, const IO *__restrict__ logits,
+    const int64_t ld, const int32_t *__restrict__ t_ids, const float *__restrict__ t_logits,
+    const float tau, const float inv_tau, float *__restrict__ loss, float *__restrict__ lse)
+{
+    constexpr int n = kPer16<IO>;
+    __shared__ MaxSum row_ms[kDistWaves], ent_ms[kDistWaves];
+    __shared__ float sum[kDistWaves];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
+        const IO *row = logits + r * ld;
+        const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
+        const float at = e.id >= 0 ? to_f(row[e.id]) : 0.f;
+        MaxSum a{kNegInf, 0.f};
+        for (int64_t c = (int64_t)tid * n; c < V; c += kDistThreads * n) {
+            Run<IO, n> v;
+            const int m = V - c < n ? (int)(V - c) : n;
+            if (m == n) v.load(row + c);
+            else v.load_part(row + c, m);
+            float top = a.m;
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                if (i < m) top = fmaxf(top, v.get(i) * inv_tau);
+            const float b = base_of(top);
+            float s = a.s * exp_nat(a.m - b);
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                if (i < m) s += exp_nat(fmaf(v.get(i), inv_tau, -b));
+            a = {top, s};
+        }
+        const MaxSum ws = wave_maxsum(a), es = entry_maxsum(e);
+        if (lane == 0) {
+            row_ms[w] = ws;
+            ent_ms[w] = es;
+        }
+        __syncthreads();
+        const MaxSum rs = join_maxsum(row_ms), ts = join_maxsum(ent_ms);
+        const float log_s = logf(rs.s);
+        float term = 0.f;
+        if (e.id >= 0) {
+            const float gap = e.t - base_of(ts.m);
+            const float p = exp_nat(gap) / ts.s;
+            const float logp = gap - logf(ts.s);
+            const float logq = at == kNegInf ? kNegInf : fmaf(at, inv_tau, -base_of(rs.m)) - log_s;
+            if (!(p == 0.f)) term = p * (logp - logq);  // 0 log 0 = 0; NaN goes on
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) term += __shfl_xor(term, o);
+        if (lane == 0) sum[w] = term;
+        __syncthreads();
+        if (tid == 0) {
+            float t = 0.f;
+            for (int i = 0; i < kDistWaves; ++i) t += sum[i];
+            loss[r] = tau * tau * t;
+            lse[r] = rs.m + log_s;
+        }
+        // (the next row writes row_ms and ent_ms: every thread has read them by now)
+    }
+}
+
+// -------------------------------------------------------------- gradient
+// A workgroup takes kGradRuns accesses per thread of one row.  The dense part
+// g tau q_v is stored first; then the elements that the entries name are
+// written again with their share of p, by the first entry that names each.
+constexpr int kGradRuns = 4;
+
+template <typename IO>
+__global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(
+    const int64_t R, const int64_t V, const int k, const int64_t n_chunks,
+    const IO *__restrict__ logits, const int64_t ld, const int32_t *__restrict__ t_ids,
+    const float *__restrict__ t_logits, const float tau, const float inv_tau,
+    const float *__restrict__ lse, const float *__restrict__ g, IO *__restrict__ dlogits,
+    const int64_t ldd)
+{
+    constexpr int n = kPer16<IO>;
+    constexpr int64_t chunk = (int64_t)kDistThreads * n * kGradRuns;
+    __shared__ MaxSum ent_ms[kDistWaves];
+    __shared__ int ids[kDistThreads];
+    __shared__ float ps[kDistThreads];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    for (int64_t u = blockIdx.x; u < R * n_chunks; u += gridDim.x) {
+        const int64_t r = u / n_chunks, c0 = (u - r * n_chunks) * chunk;
+        const int64_t c1 = c0 + chunk < V ? c0 + chunk : V;
+        const IO *row = logits + r * ld;
+        IO *out = dlogits + r * ldd;
+        const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
+        const MaxSum es = entry_maxsum(e);
+        if (lane == 0) ent_ms[w] = es;
+        __syncthreads();
+        const MaxSum ts = join_maxsum(ent_ms);
+        const float L = lse[r], gr = g[r];
+        // no valid entry: no loss to descend; weight 0: a row that does not count
+        const bool some = ts.m != kNegInf && gr != 0.f;
+        const float f = some ? gr * tau : 0.f;
+        ids[tid] = e.id;
+        ps[tid] = e.id >= 0 ? exp_nat(e.t - base_of(ts.m)) / ts.s : 0.f;
+        auto q_of = [&](float s) {
+            return L == kNegInf ? 0.f : exp_nat(fmaf(s, inv_tau, -L));
+        };
+#pragma unroll
+        for (int i = 0; i < kGradRuns; ++i) {
+            const int64_t c = c0 + ((int64_t)i * kDistThreads + tid) * n;
+            if (c >= c1) continue;
+            const int m = c1 - c < n ? (int)(c1 - c) : n;
+            Run<IO, n> v;
+            if (m == n) v.load(row + c);
+            else v.load_part(row + c, m);
+            float d[n];
+#pragma unroll
+            for (int j = 0; j < n; ++j) d[j] = some ? f * q_of(v.get(j)) : 0.f;
+            const Run<IO, n> o = round_run<IO, n>(d);
+            if (m == n) o.store(out + c);
+            else o.store_part(out + c, m);
+        }
+        // the dense stores are done before an element is written again
+        wait_mem();
+        __syncthreads();
+        if (some && e.id >= c0 && e.id < c1) {
+            float p = 0.f;
+            bool first = true;
+            for (int j = 0; j < k; ++j)
+                if (ids[j] == e.id) {
+                    first = first && j >= tid;
+                    p += ps[j];
+                }
+            if (first) out[e.id] = from_f<IO>(f * (q_of(to_f(row[e.id])) - p));
+        }
+        __syncthreads();
+    }
+}
+
+struct DistillArgs {
+    int64_t R, V;
+    int k;
+    const void *logits;
+    int64_t ld;
+    const int32_t *t_ids;
+    const float *t_logits;
+    float tau;
+    float *loss, *lse;          // forward
+    const float *g;             // backward
+    void *dlogits;
+    int64_t ldd;
+};
+
+template <typename IO> static hipError_t launch_loss(const DistillArgs &a, hipStream_t st)
+{
+    const unsigned grid = (unsigned)(a.R < (1 << 20) ? a.R : 1 << 20);
+    hipLaunchKernelGGL(distill_loss_kernel<IO>, dim3(grid), dim3(kDistThreads), 0, st, a.R, a.V,
+                       a.k, (const IO *)a.logits, a.ld, a.t_ids, a.t_logits, a.tau, 1.f / a.tau,
+                       a.loss, a.lse);
+    return hipGetLastError();
+}
+
+template <typename IO> static hipError_t launch_grad(const DistillArgs &a, hipStream_t st)
+{
+    constexpr int64_t chunk = (int64_t)kDistThreads * kPer16<IO> * kGradRuns;
+    const int64_t n_chunks = (a.V + chunk - 1) / chunk, units = a.R * n_chunks;
+    const unsigned grid = (unsigned)(units < (1 << 22) ? units : 1 << 22);
+    hipLaunchKernelGGL(distill_grad_kernel<IO>, dim3(grid), dim3(kDistThreads), 0, st, a.R, a.V,
+                       a.k, n_chunks, (const IO *)a.logits, a.ld, a.t_ids, a.t_logits, a.tau,
+                       1.f / a.tau, a.lse, a.g, (IO *)a.dlogits, a.ldd);
+    return hipGetLastError();
+}
+
+static naju_status_t check_distill(int64_t R, int64_t V, int64_t k, int32_t io, const void *logits,
+                                   int64_t ld, const void *t_ids, const void *t_logits, float tau)
+{
+    if (R < 0 || V < 0 || k < 0)
+        return fail(NAJU_EINVAL, "negative size (rows=%lld vocab=%lld k=%lld)", (long long)R,
+                    (long long)V, (long long)k);
+    if (io != NAJU_F32 && io != NAJU_BF16)
+        return fail(NAJU_EINVAL, "io dtype %d is neither NAJU_F32 nor NAJU_BF16", (int)io);
+    if (R > ((int64_t)1 << 30) || V > ((int64_t)1 << 30))
+        return fail(NAJU_EINVAL, "rows or vocab too large (2^30 max)");
+    if (k > kDistThreads)
+        return fail(NAJU_EUNSUPPORTED, "k %lld teacher entries a row (%d max)", (long long)k,
+                    kDistThreads);
+    if (!(tau > 0.f) || !(tau < __builtin_huge_valf()))
+        return fail(NAJU_EINVAL, "temperature must be positive and finite");
+    if (R == 0 || V == 0) return NAJU_OK;
+    if (ld < V) return fail(NAJU_EINVAL, "row stride of logits %lld is less than vocab %lld",
+                            (long long)ld, (long long)V);
+    if (ld > ((int64_t)1 << 31)) return fail(NAJU_EINVAL, "row stride of logits too large");
+    NAJU_TRY(need(logits, "logits", io == NAJU_F32 ? 4 : 2));
+    if (k > 0) {
+        NAJU_TRY(need(t_ids, "t_ids", 4));
+        NAJU_TRY(need(t_logits, "t_logits", 4));
+    }
+    return NAJU_OK;
+}
+
+static naju_status_t check_dlogits(int64_t V, int32_t io, const float *g, const void *dlogits,
+                                   int64_t ldd)
+{
+    if (ldd < V) return fail(NAJU_EINVAL, "row stride of dlogits %lld is less than vocab %lld",
+                             (long long)ldd, (long long)V);
+    if (ldd > ((int64_t)1 << 31)) return fail(NAJU_EINVAL, "row stride of dlogits too large");
+    NAJU_TRY(need(g, "g", 4));
+    return need(dlogits, "dlogits", io == NAJU_F32 ? 4 : 2);
+}
+
+}  // namespace naju
+
+using namespace naju;
+
+extern "C" {
+
+naju_status_t naju_distill_fwd(int64_t rows, int64_t vocab, int64_t k, int32_t io,
+                               const void *logits, int64_t ld, const int32_t *t_ids,
+                               const float *t_logits, float temperature, float *loss, float *lse,
+                               void *stream)
+{
+    NAJU_TRY(check_distill(rows, vocab, k, io, logits, ld, t_ids, t_logits, temperature));
+    if (rows == 0 || vocab == 0) return NAJU_OK;
+    NAJU_TRY(need(loss, "loss", 4));
+    NAJU_TRY(need(lse, "lse", 4));
+    const DistillArgs a{rows, vocab, (int)k, logits, ld, t_ids, t_logits, temperature,
+                        loss, lse, nullptr, nullptr, 0};
+    hipStream_t st = (hipStream_t)stream;
+    return hip_status(io == NAJU_F32 ? launch_loss<float>(a, st) : launch_loss<bf16>(a, st),
+                      "distillation loss launch");
+}
+
+naju_status_t naju_distill_bwd(int64_t rows, int64_t vocab, int64_t k, int32_t io,
+                               const void *logits, int64_t ld, const int32_t *t_ids,
+                               const float *t_logits, float temperature, const float *lse,
+                               const float *g, void *dlogits, int64_t ld_d, void *stream)
+{
+    NAJU_TRY(check_distill(rows, vocab, k, io, logits, ld, t_ids, t_logits, temperature));
+    if (rows == 0 || vocab == 0) return NAJU_OK;
+    NAJU_TRY(need(lse, "lse", 4));
+    NAJU_TRY(check_dlogits(vocab, io, g, dlogits, ld_d));
+    const DistillArgs a{rows, vocab, (int)k, logits, ld, t_ids, t_logits, temperature,
+                        nullptr, const_cast<float *>(lse), g, dlogits, ld_d};
+    hipStream_t st = (hipStream_t)stream;
+    return hip_status(io == NAJU_F32 ? launch_grad<float>(a, st) : launch_grad<bf16>(a, st),
+                      "distillation gradient launch");
+}
+
+naju_status_t naju_distill_fwd_bwd(int64_t rows, int64_t vocab, int64_t k, int32_t io,
+                                   const void *logits, int64_t ld, const int32_t *t_ids,
+                                   const float *t_logits, float temperature, const float *g,
+                                   float *loss, float *lse, void *dlogits, int64_t ld_d,
+                                   void *stream)
+{
+    NAJU_TRY(check_distill(rows, vocab, k, io, logits, ld, t_ids, t_logits, temperature));
+    if (rows == 0 || vocab == 0) return NAJU_OK;
+    NAJU_TRY(need(loss, "loss", 4));
+    NAJU_TRY(need(lse, "lse", 4));
+    NAJU_TRY(check_dlogits(vocab, io, g, dlogits, ld_d));
+    const DistillArgs a{rows, vocab, (int)k, logits, ld, t_ids, t_logits, temperature,
+                        loss, lse, g, dlogits, ld_d};
+    hipStream_t st = (hipStream_t)stream;
+    NAJU_TRY(hip_status(io == NAJU_F32 ? launch_loss<float>(a, st) : launch_loss<bf16>(a, st),
+                        "distillation loss launch"));
+    return hip_status(io == NAJU_F32 ? launch_grad<float>(a, st) : launch_grad<bf16>(a, st),
+                      "distillation gradient launch");
+}
+
+}  // extern "C"

@@ -52,6 +52,23 @@ int main()
            naju_embed_bwd(8, 8, 8, NAJU_BF16, ip, p, 1.f, 0, fp, buf + 64, big, nullptr),
            NAJU_EINVAL);
 
+    for (int64_t R : Ts)
+        for (int64_t V : Vs)
+            for (int64_t k : {(int64_t)-1, (int64_t)0, (int64_t)512, (int64_t)513, INT64_MAX}) {
+                const naju_status_t s =
+                    naju_distill_fwd(R, V, k, NAJU_F32, nullptr, V, nullptr, nullptr, 1.f, fp, fp,
+                                     nullptr);
+                if (R > 0 && V > 0 && s == NAJU_OK) {
+                    std::fprintf(stderr, "distill_fwd without pointers accepted\n");
+                    ++failures;
+                }
+            }
+    expect("distill_bwd stride", naju_distill_bwd(2, 8, 1, NAJU_F32, p, 7, ip, fp, 1.f, fp, fp, p,
+                                                  8, nullptr), NAJU_EINVAL);
+    expect("distill_fwd_bwd temperature",
+           naju_distill_fwd_bwd(2, 8, 1, NAJU_F32, p, 8, ip, fp, 0.f, fp, fp, fp, p, 8, nullptr),
+           NAJU_EINVAL);
+
     if (failures) return 1;
     std::puts("lm driver: ok");
     return 0;

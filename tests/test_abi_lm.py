@@ -57,3 +57,38 @@ def test_embed_bwd_refusals(lib):
     assert size(16384, 50000, 768) >= 4 * 4 * 16384
     assert size(-1, 5, 5) == 0 and size(2 ** 29, 5, 5) == 0
     assert size(2 ** 28, 2 ** 30, 2 ** 20) > 2 ** 40  # no overflow at the limits
+
+
+def test_distill_refusals(lib):
+    def args(R=4, V=100, k=8, io=nb.BF16, logits=FAKE, ld=None, ids=FAKE, t=FAKE, tau=1.0):
+        return (R, V, k, io, logits, V if ld is None else ld, ids, t, tau)
+
+    def fwd(loss=FAKE, lse=FAKE, **kw):
+        return lib.naju_distill_fwd(*args(**kw), loss, lse, None)
+
+    def bwd(lse=FAKE, g=FAKE, d=FAKE, ldd=100, **kw):
+        return lib.naju_distill_bwd(*args(**kw), lse, g, d, ldd, None)
+
+    def both(g=FAKE, loss=FAKE, lse=FAKE, d=FAKE, ldd=100, **kw):
+        return lib.naju_distill_fwd_bwd(*args(**kw), g, loss, lse, d, ldd, None)
+    for call in (fwd, bwd, both):
+        expect(call(R=-1), nb.EINVAL, "negative size")
+        expect(call(k=-1), nb.EINVAL, "negative size")
+        expect(call(io=3), nb.EINVAL, "io dtype")
+        expect(call(k=513), nb.EUNSUPPORTED, "teacher entries")
+        for tau in (0.0, -1.0, float("nan"), float("inf")):
+            expect(call(tau=tau), nb.EINVAL, "temperature")
+        expect(call(ld=99), nb.EINVAL, "row stride of logits")
+        expect(call(V=2 ** 31), nb.EINVAL, "too large")
+        expect(call(logits=None), nb.EINVAL, "logits is NULL")
+        expect(call(logits=FAKE + 1), nb.EINVAL, "aligned")
+        expect(call(ids=None), nb.EINVAL, "t_ids is NULL")
+        expect(call(t=None), nb.EINVAL, "t_logits is NULL")
+        expect(call(lse=None), nb.EINVAL, "lse is NULL")
+        assert call(R=0, logits=None, ids=None, t=None) == nb.OK
+        assert call(V=0, logits=None, ids=None, t=None) == nb.OK
+    expect(fwd(loss=None), nb.EINVAL, "loss is NULL")
+    for call in (bwd, both):
+        expect(call(g=None), nb.EINVAL, "g is NULL")
+        expect(call(d=None), nb.EINVAL, "dlogits is NULL")
+        expect(call(ldd=99), nb.EINVAL, "row stride of dlogits")

@@ -26,3 +26,58 @@ def test_embed_bwd_is_the_adjoint_and_the_difference_quotient():
         Wm[v, c] -= eps
         num = (dout * (lm.embed_fwd(ids, Wp, 0.3) - lm.embed_fwd(ids, Wm, 0.3))).sum() / (2 * eps)
         assert np.isclose(dW[v, c], num, atol=1e-8)
+
+
+def test_distill_with_one_entry_is_cross_entropy():
+    rng = np.random.default_rng(2)
+    x = rng.standard_normal((3, 11))
+    label = np.array([[4], [0], [10]])
+    loss, lse, grad = lm.distill(x, label, rng.standard_normal((3, 1)), 1.0, np.ones(3))
+    q = np.exp(x) / np.exp(x).sum(1, keepdims=True)
+    assert np.allclose(loss, -np.log(q[np.arange(3), label[:, 0]]))
+    assert np.allclose(lse, np.log(np.exp(x).sum(1)))
+    assert np.allclose(grad, q - (np.arange(11) == label))
+
+
+def test_distill_against_dense_kl_and_its_minimum():
+    rng = np.random.default_rng(3)
+    V, tau = 6, 2.5
+    t = rng.standard_normal((1, V))
+    ids = rng.permutation(V)[None]
+    x = rng.standard_normal((1, V))
+    p, q = np.zeros(V), np.exp(x[0] / tau) / np.exp(x[0] / tau).sum()
+    p[ids[0]] = np.exp(t[0] / tau) / np.exp(t[0] / tau).sum()
+    loss, _, _ = lm.distill(x, ids, t, tau)
+    assert np.isclose(loss[0], tau ** 2 * (p * np.log(p / q)).sum())
+    same = np.zeros((1, V))
+    same[0, ids[0]] = t[0] + 3.0  # the teacher's distribution itself
+    loss, _, grad = lm.distill(same, ids, t, tau, np.ones(1))
+    assert abs(loss[0]) < 1e-14 and np.abs(grad).max() < 1e-15
+
+
+def test_distill_gradient_is_the_difference_quotient():
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((2, 9))
+    ids = np.array([[3, 3, 8, -1], [0, 9, 2, 5]])  # an index twice, padding, one past the end
+    t = rng.standard_normal((2, 4))
+    t[1, 3] = -np.inf
+    g = np.array([0.7, -1.3])
+    _, _, grad = lm.distill(x, ids, t, 1.7, g)
+    eps = 1e-6
+    for r in range(2):
+        for v in range(9):
+            xp, xm = x.copy(), x.copy()
+            xp[r, v] += eps
+            xm[r, v] -= eps
+            num = (g * (lm.distill(xp, ids, t, 1.7)[0] - lm.distill(xm, ids, t, 1.7)[0])).sum()
+            assert np.isclose(grad[r, v], num / (2 * eps), atol=1e-8)
+    assert np.allclose(grad.sum(1), 0)  # probabilities and targets both sum to 1
+
+
+def test_distill_empty_and_impossible_rows():
+    x = np.array([[0.0, 1.0, -np.inf], [-np.inf, 0.5, 0.25]])
+    ids = np.array([[-1, 2], [0, 1]])
+    t = np.array([[1.0, -np.inf], [0.0, 0.0]])
+    loss, _, grad = lm.distill(x, ids, t, 1.0, np.ones(2))
+    assert loss[0] == 0 and not grad[0].any()       # no valid entry
+    assert loss[1] == np.inf and grad[1, 0] == -0.5  # a target where the student has 0
