@@ -400,6 +400,43 @@ naju_status_t naju_distill_fwd_bwd(int64_t rows, int64_t vocab, int64_t k, int32
                                    float *loss, float *lse, void *dlogits, int64_t ld_d,
                                    void *stream);
 
+/*
+ * Logits made ready for the choice of a token.  Per row, with c_v the number of
+ * times v occurs among the first lengths[row] entries of the row's history:
+ *     x = l_v
+ *     where c_v > 0:  x = x > 0 ? x / repetition : x * repetition;
+ *                     x = x - frequency c_v;  x = x - presence
+ *     x = x + bias of v
+ *     x = -inf where bit v of the row's mask is 0
+ *     out_v = x;  best = the lowest v whose x is largest
+ * in fp32, every operation rounded by itself.  best is -1 where no x is above
+ * -inf (NaN is never best).
+ *   logits    [rows][ld] io, the first vocab of every row's ld >= vocab elements
+ *   history   [rows][history_len] int32, entries outside [0, vocab) ignored
+ *             (NULL with history_len 0); history_len < 2^20
+ *   lengths   [rows] int32 (taken into [0, history_len]), or NULL (= history_len)
+ *   repetition, presence, frequency  [rows] fp32, each may be NULL (= none)
+ *   bias_ids, bias  [rows][n_bias] int32 and fp32: pairs of a token and what is
+ *             added to it (-inf forbids it); ids outside [0, vocab) are ignored; of
+ *             several pairs that name one token the first counts; n_bias < 4095
+ *   mask      [rows][ceil(vocab / 32)] uint32 or NULL (= all allowed): bit v % 32
+ *             of word v / 32, 1 = allowed; bits past vocab are ignored
+ *   out       [rows][vocab] fp32 (written)
+ *   best      [rows] int32 (written) or NULL
+ *   ws        naju_logits_workspace_bytes() bytes, 256-byte aligned, zero-filled
+ *             before its first use and left reusable for calls with up to that
+ *             many rows; may be NULL when best is
+ * rows <= 2^24, vocab <= 2^30.
+ */
+size_t naju_logits_workspace_bytes(int64_t rows);
+naju_status_t naju_logits_process(int64_t rows, int64_t vocab, int32_t io, const void *logits,
+                                  int64_t ld, const int32_t *history, int64_t history_len,
+                                  const int32_t *lengths, const float *repetition,
+                                  const float *presence, const float *frequency,
+                                  const int32_t *bias_ids, const float *bias, int64_t n_bias,
+                                  const uint32_t *mask, float *out, int32_t *best, void *ws,
+                                  size_t ws_bytes, void *stream);
+
 /* Thread-local description of the last non-OK status ("" if none). */
 const char *naju_last_error(void);
 

@@ -54,3 +54,42 @@ def distill(logits, t_ids, t_logits, tau, g=None):
                     d[i] -= p[j]
                 grad[r] = g[r] * tau * d
     return loss, lse, grad
+
+
+def logits_process(logits, history=None, lengths=None, repetition=None, presence=None,
+                   frequency=None, bias_ids=None, bias=None, mask=None):
+    """out, best: penalties, biases and mask, token by token of each row's lists."""
+    out = np.array(logits, dtype=np.float64)
+    R, V = out.shape
+    best = np.full(R, -1, dtype=np.int64)
+    for b in range(R):
+        counts = {}
+        if history is not None:
+            n = history.shape[1] if lengths is None else min(max(int(lengths[b]), 0),
+                                                             history.shape[1])
+            for v in history[b, :n].tolist():
+                if 0 <= v < V:
+                    counts[v] = counts.get(v, 0) + 1
+        for v, c in counts.items():
+            x = out[b, v]
+            if repetition is not None:
+                x = x / float(repetition[b]) if x > 0 else x * float(repetition[b])
+            if frequency is not None:
+                x -= float(frequency[b]) * c
+            if presence is not None:
+                x -= float(presence[b])
+            out[b, v] = x
+        if bias_ids is not None:
+            done = set()
+            for v, add in zip(bias_ids[b].tolist(), bias[b].tolist()):
+                if 0 <= v < V and v not in done:
+                    done.add(v)
+                    out[b, v] += add
+        if mask is not None:
+            for v in range(V):
+                if not (int(mask[b, v // 32]) >> (v % 32)) & 1:
+                    out[b, v] = -np.inf
+        x = np.where(np.isnan(out[b]), -np.inf, out[b])
+        if V and x.max() > -np.inf:
+            best[b] = int(np.flatnonzero(x == x.max())[0])
+    return out, best

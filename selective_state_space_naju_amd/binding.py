@@ -30,7 +30,7 @@ EXPORTS = ("naju_workspace_bytes", "naju_ckpt_bytes", "naju_workspace_init",
            "naju_mixer_fwd", "naju_mixer_bwd_workspace_bytes", "naju_mixer_bwd",
            "naju_scan_fwd_noalloc", "naju_embed_fwd", "naju_embed_bwd_workspace_bytes",
            "naju_embed_bwd", "naju_distill_fwd", "naju_distill_bwd", "naju_distill_fwd_bwd",
-           "naju_last_error", "naju_version")
+           "naju_logits_workspace_bytes", "naju_logits_process", "naju_last_error", "naju_version")
 
 
 class NajuError(RuntimeError):
@@ -108,6 +108,11 @@ def lib() -> ctypes.CDLL:
         L.naju_distill_fwd_bwd.argtypes = [i64, i64, i64, i32, vp, i64, vp, vp, f32, vp, vp, vp,
                                            vp, i64, vp]
         L.naju_distill_fwd_bwd.restype = st
+        L.naju_logits_workspace_bytes.argtypes = [i64]
+        L.naju_logits_workspace_bytes.restype = sz
+        L.naju_logits_process.argtypes = ([i64, i64, i32, vp, i64, vp, i64] + [vp] * 6 +
+                                          [i64, vp, vp, vp, vp, sz, vp])
+        L.naju_logits_process.restype = st
         L.naju_last_error.argtypes = []
         L.naju_last_error.restype = ctypes.c_char_p
         L.naju_version.argtypes = []
@@ -535,6 +540,8 @@ def _distill_args(logits, t_ids, t_logits, temperature):
     if logits.dim() != 2 or t_ids.dim() != 2:
         raise ValueError("logits and t_ids must be matrices")
     R, V = logits.shape
+    if V == 0:
+        raise ValueError("logits: the vocabulary is empty")
     k = t_ids.shape[1]
     dt, dev = logits.dtype, logits.device
     io = _io_of(logits)
@@ -583,3 +590,44 @@ def distill_fwd_bwd(logits, t_ids, t_logits, g, temperature=1.0, *, dlogits=None
     check(lib().naju_distill_fwd_bwd(*args, _p(g), _p(loss), _p(lse), _p(dlogits), ldd,
                                      stream_handle(dev)))
     return loss, dlogits
+
+
+def logits_process(logits, history=None, lengths=None, repetition=None, presence=None,
+                   frequency=None, bias_ids=None, bias=None, mask=None, *, ws=None):
+    """out, best = naju_logits_process(...): penalties for the tokens of each row's history
+    (int32 [rows, n], the first lengths[row] of it), biases (pairs bias_ids int32, bias fp32
+    [rows, n]) and a grammar mask (int32 words [rows, ceil(vocab / 32)], bit set = allowed).
+    out: fp32 [rows, vocab]; best: int32 [rows], -1 where nothing is allowed.  repetition,
+    presence and frequency are fp32 [rows] or None."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be a matrix")
+    R, V = logits.shape
+    if V == 0:
+        raise ValueError("logits: the vocabulary is empty")
+    dt, dev = logits.dtype, logits.device
+    io = _io_of(logits)
+    ld = _req_rows(logits, "logits", (R, V), dt, dev)
+    H = nb = 0
+    if history is not None:
+        H = history.shape[-1]
+        _req(history, "history", (R, H), torch.int32, dev)
+    _opt(lengths, "lengths", (R,), torch.int32, dev)
+    _opt(repetition, "repetition", (R,), torch.float32, dev)
+    _opt(presence, "presence", (R,), torch.float32, dev)
+    _opt(frequency, "frequency", (R,), torch.float32, dev)
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias_ids is not None:
+        nb = bias_ids.shape[-1]
+        _req(bias_ids, "bias_ids", (R, nb), torch.int32, dev)
+        _req(bias, "bias", (R, nb), torch.float32, dev)
+    _opt(mask, "mask", (R, (V + 31) // 32), torch.int32, dev)
+    out = torch.empty((R, V), dtype=torch.float32, device=dev)
+    best = torch.empty((R,), dtype=torch.int32, device=dev)
+    ws = ws or _cached_workspace("logits", (R,),
+                                 lambda: lib().naju_logits_workspace_bytes(R), dev)
+    check(lib().naju_logits_process(R, V, io, _p(logits), ld, _p(history), H, _p(lengths),
+                                    _p(repetition), _p(presence), _p(frequency), _p(bias_ids),
+                                    _p(bias), nb, _p(mask), _p(out), _p(best), ws.ptr, ws.nbytes,
+                                    stream_handle(dev)))
+    return out, best

@@ -1,0 +1,317 @@
+// naju_logits.hip -- logits made ready for the choice of a token: penalties for
+// tokens that occurred before, biases, a grammar's mask, and the best token.
+//
+// Per row, with c_v the occurrences of v among the row's earlier tokens:
+//     x = l_v
+//     if c_v > 0:  x = x > 0 ? x / r : x r;   x = x - f c_v;   x = x - a
+//     x = x + bias_v                     (the first listed pair of v)
+//     x = -inf where the mask does not allow v
+// and best = the lowest index of the largest x, -1 where nothing is above -inf.
+//
+// Few tokens of a row are penalised or biased, so the arithmetic is done for
+// those alone.  A workgroup owns a tile of one row's vocabulary and keeps one
+// LDS word per token of it: the row's bias list and history are scanned and
+// counted there, the tokens that were touched are listed, their values are
+// computed once each into their words, and the dense pass that follows only
+// selects between a word and the logit.  It reads every logit and writes every
+// result once: the bytes bound it.
+#include "naju_device.h"
+#include "naju_host.h"
+#include "naju_launch.h"
+#include "naju_vec.h"
+
+namespace naju {
+
+constexpr int kLogThreads = 512;
+constexpr int kLogTile = 8192;         // most tokens of a workgroup
+constexpr int kLogSmallTile = 2048;
+constexpr int kCountBits = 20;         // a word: list place (12 bits) | count (20 bits)
+constexpr uint32_t kCountMask = (1u << kCountBits) - 1;
+constexpr int kPlaces = 4095;          // biases of a row
+constexpr int64_t kMostHistory = kCountMask;
+
+struct LogitsArgs {
+    int64_t B, V;
+    int tile;
+    int64_t n_tiles;
+    int64_t ld;
+    const int32_t *history;       // [B][H] or null
+    int64_t H;
+    const int32_t *lengths;       // [B] or null (= H)
+    const float *rep, *pres, *freq;  // [B] or null
+    const int32_t *bias_ids;      // [B][nb] or null
+    const float *bias;
+    int nb;
+    const uint32_t *mask;         // [B][ceil(V / 32)] or null
+    float *out;                   // [B][V]
+    int32_t *best;                // [B] or null
+    char *ws;                     // RowBest[B]
+};
+
+// the best token over the tiles of a row, and the tiles that have reported
+struct RowBest {
+    uint64_t key;
+    uint32_t done, pad;
+};
+
+// Order-preserving key of (value, index): larger values first, then lower
+// indices; 0 stands for nothing above -inf.
+__device__ __forceinline__ uint64_t best_key(float v, int32_t idx)
+{
+    if (idx < 0) return 0;
+    const uint32_t b = __float_as_uint(v + 0.f);  // (-0 and 0 are equal)
+    const uint32_t o = (b >> 31) ? ~b : b | 0x80000000u;
+    return ((uint64_t)o << 32) | (uint32_t)~(uint32_t)idx;
+}
+__device__ __forceinline__ int32_t key_index(uint64_t k)
+{
+    return k ? (int32_t)~(uint32_t)k : -1;
+}
+
+// A touched token's value.  Every operation rounds by itself, as written.
+__device__ __forceinline__ float penalised(float x, uint32_t count, const LogitsArgs &g, int64_t b)
+{
+#pragma clang fp contract(off)
+    if (count > 0) {
+        if (g.rep) {
+            const float r = g.rep[b];
+            x = x > 0.f ? x / r : x * r;
+        }
+        if (g.freq) {
+            const float f = g.freq[b] * (float)count;
+            x = x - f;
+        }
+        if (g.pres) x = x - g.pres[b];
+    }
+    return x;
+}
+
+template <typename IO>
+__global__ __launch_bounds__(kLogThreads) void logits_kernel(const LogitsArgs g,
+                                                             const IO *__restrict__ logits)
+{
+    __shared__ __attribute__((aligned(16))) uint32_t word[kLogTile];
+    __shared__ uint16_t list[kLogTile];
+    __shared__ uint32_t n_list;
+    __shared__ uint64_t wave_best[kLogThreads / 64];
+    const int tid = threadIdx.x;
+    const bool touched = g.H > 0 || g.nb > 0;
+    for (int64_t u = blockIdx.x; u < g.B * g.n_tiles; u += gridDim.x) {
+        const int64_t b = u / g.n_tiles, v0 = (u - b * g.n_tiles) * g.tile;
+        const int nv = g.V - v0 < g.tile ? (int)(g.V - v0) : g.tile;
+        const IO *row = logits + b * g.ld + v0;
+        const uint32_t *mrow = g.mask ? g.mask + b * ((g.V + 31) / 32) + v0 / 32 : nullptr;
+        if (touched) {
+            for (int i = tid * 4; i < g.tile; i += kLogThreads * 4)
+                *(uint4 *)&word[i] = make_uint4(0, 0, 0, 0);
+            if (tid == 0) n_list = 0;
+            __syncthreads();
+            // bias list: the first pair that names a token has the highest mark
+            const int32_t *bi = g.bias_ids + b * g.nb;
+            for (int j = tid; j < g.nb; j += kLogThreads) {
+                const int64_t v = bi[j] - v0;
+                if (v >= 0 && v < nv) atomicMax(&word[v], (uint32_t)(kPlaces - j) << kCountBits);
+            }
+            __syncthreads();
+            for (int j = tid; j < g.nb; j += kLogThreads) {
+                const int64_t v = bi[j] - v0;
+                if (v >= 0 && v < nv && (word[v] >> kCountBits) == (uint32_t)(kPlaces - j))
+                    list[atomicAdd(&n_list, 1u)] = (uint16_t)v;
+            }
+            // history: whoever counts a token first lists it
+            int64_t len = g.H;
+            if (g.lengths) {
+                len = g.lengths[b];
+                len = len < 0 ? 0 : len > g.H ? g.H : len;
+            }
+            const int32_t *h = g.history + b * g.H;
+            for (int64_t i = (int64_t)tid * 4; i < len; i += kLogThreads * 4) {
+                Run<float, 4> r;
+                const int m = len - i < 4 ? (int)(len - i) : 4;
+                if (m == 4) r.load((const float *)h + i);
+                else r.load_part((const float *)h + i, m);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int64_t v = (int32_t)r.w[q] - v0;
+                    if (q < m && v >= 0 && v < nv)
+                        if (atomicAdd(&word[v], 1u) == 0) list[atomicAdd(&n_list, 1u)] = (uint16_t)v;
+                }
+            }
+            __syncthreads();
+            const int n = (int)n_list;
+            for (int i = tid; i < n; i += kLogThreads) {
+                const int v = list[i];
+                const uint32_t w = word[v];
+                float x = penalised(to_f(row[v]), w & kCountMask, g, b);
+                if (w >> kCountBits) x = x + g.bias[b * g.nb + (kPlaces - (w >> kCountBits))];
+                if (x != x) x = __uint_as_float(0x7fc00000u);
+                word[v] = ~__float_as_uint(x);  // (0 only for a NaN pattern that is not used)
+            }
+            __syncthreads();
+        }
+        // dense pass
+        float top = -__builtin_huge_valf();
+        int32_t at = -1;
+        float *out = g.out + b * g.V + v0;
+        for (int c = tid * 4; c < nv; c += kLogThreads * 4) {
+            const int m = nv - c < 4 ? nv - c : 4;
+            Run<IO, 4> r;
+            if (m == 4) r.load(row + c);
+            else r.load_part(row + c, m);
+            float x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[q] = r.get(q);
+            if (touched) {
+                const uint4 w = *(const uint4 *)&word[c];
+                x[0] = w.x ? __uint_as_float(~w.x) : x[0];
+                x[1] = w.y ? __uint_as_float(~w.y) : x[1];
+                x[2] = w.z ? __uint_as_float(~w.z) : x[2];
+                x[3] = w.w ? __uint_as_float(~w.w) : x[3];
+            }
+            if (mrow) {
+                const uint32_t bits = mrow[c >> 5] >> (c & 31);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (!((bits >> q) & 1u)) x[q] = -__builtin_huge_valf();
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < m && x[q] > top) {
+                    top = x[q];
+                    at = (int32_t)(v0 + c + q);
+                }
+            const Run<float, 4> o = round_run<float, 4>(x);
+            if (m == 4) o.store(out + c);
+            else o.store_part(out + c, m);
+        }
+        if (g.best) {
+            uint64_t k = best_key(top, at);
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) {
+                const uint64_t x = __shfl_xor(k, o);
+                k = x > k ? x : k;
+            }
+            if ((tid & 63) == 0) wave_best[tid >> 6] = k;
+            __syncthreads();
+            if (tid == 0) {
+                for (int i = 1; i < kLogThreads / 64; ++i) k = wave_best[i] > k ? wave_best[i] : k;
+                if (g.n_tiles == 1) {
+                    g.best[b] = key_index(k);
+                } else {
+                    // the last tile of the row to report reads the row's key and clears
+                    // the record for the next call
+                    RowBest *rb = (RowBest *)g.ws + b;
+                    __hip_atomic_fetch_max(&rb->key, k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    const uint32_t d = __hip_atomic_fetch_add(&rb->done, 1u, __ATOMIC_ACQ_REL,
+                                                              __HIP_MEMORY_SCOPE_AGENT);
+                    if (d + 1 == (uint32_t)g.n_tiles) {
+                        k = __hip_atomic_exchange(&rb->key, (uint64_t)0, __ATOMIC_RELAXED,
+                                                  __HIP_MEMORY_SCOPE_AGENT);
+                        __hip_atomic_store(&rb->done, 0u, __ATOMIC_RELAXED,
+                                           __HIP_MEMORY_SCOPE_AGENT);
+                        g.best[b] = key_index(k);
+                    }
+                }
+            }
+        }
+        __syncthreads();  // (word, list and wave_best are reused)
+    }
+}
+
+static size_t logits_ws_bytes(int64_t rows) { return align256(sizeof(RowBest) * (size_t)rows); }
+
+template <typename IO>
+static hipError_t launch_logits(const LogitsArgs &g, const void *logits, hipStream_t st)
+{
+    const int64_t units = g.B * g.n_tiles;
+    const unsigned grid = (unsigned)(units < (1 << 22) ? units : 1 << 22);
+    hipLaunchKernelGGL(logits_kernel<IO>, dim3(grid), dim3(kLogThreads), 0, st, g,
+                       (const IO *)logits);
+    return hipGetLastError();
+}
+
+static naju_status_t check_logits(int64_t rows, int64_t vocab)
+{
+    if (rows < 0 || vocab < 0)
+        return fail(NAJU_EINVAL, "negative size (rows=%lld vocab=%lld)", (long long)rows,
+                    (long long)vocab);
+    if (rows > ((int64_t)1 << 24) || vocab > ((int64_t)1 << 30))
+        return fail(NAJU_EINVAL, "rows (2^24 max) or vocab (2^30 max) too large");
+    return NAJU_OK;
+}
+
+}  // namespace naju
+
+using namespace naju;
+
+extern "C" {
+
+size_t naju_logits_workspace_bytes(int64_t rows)
+{
+    if (check_logits(rows, 1) != NAJU_OK) return 0;
+    return logits_ws_bytes(rows);
+}
+
+naju_status_t naju_logits_process(int64_t rows, int64_t vocab, int32_t io, const void *logits,
+                                  int64_t ld, const int32_t *history, int64_t history_len,
+                                  const int32_t *lengths, const float *repetition,
+                                  const float *presence, const float *frequency,
+                                  const int32_t *bias_ids, const float *bias, int64_t n_bias,
+                                  const uint32_t *mask, float *out, int32_t *best, void *ws,
+                                  size_t ws_bytes, void *stream)
+{
+    NAJU_TRY(check_logits(rows, vocab));
+    if (io != NAJU_F32 && io != NAJU_BF16)
+        return fail(NAJU_EINVAL, "io dtype %d is neither NAJU_F32 nor NAJU_BF16", (int)io);
+    if (history_len < 0 || n_bias < 0)
+        return fail(NAJU_EINVAL, "negative size (history_len=%lld n_bias=%lld)",
+                    (long long)history_len, (long long)n_bias);
+    if (history_len > kMostHistory)
+        return fail(NAJU_EUNSUPPORTED, "history_len %lld (%lld max)", (long long)history_len,
+                    (long long)kMostHistory);
+    if (n_bias >= kPlaces)
+        return fail(NAJU_EUNSUPPORTED, "n_bias %lld (%d max)", (long long)n_bias, kPlaces - 1);
+    if (rows == 0 || vocab == 0) return NAJU_OK;
+    if (ld < vocab || ld > ((int64_t)1 << 31))
+        return fail(NAJU_EINVAL, "row stride of logits %lld (vocab is %lld)", (long long)ld,
+                    (long long)vocab);
+    NAJU_TRY(need(logits, "logits", io == NAJU_F32 ? 4 : 2));
+    NAJU_TRY(need(out, "out", 4));
+    if (history_len > 0) NAJU_TRY(need(history, "history", 4));
+    NAJU_TRY(opt(lengths, "lengths", 4));
+    NAJU_TRY(opt(repetition, "repetition", 4));
+    NAJU_TRY(opt(presence, "presence", 4));
+    NAJU_TRY(opt(frequency, "frequency", 4));
+    if (n_bias > 0) {
+        NAJU_TRY(need(bias_ids, "bias_ids", 4));
+        NAJU_TRY(need(bias, "bias", 4));
+    }
+    NAJU_TRY(opt(mask, "mask", 4));
+    NAJU_TRY(opt(best, "best", 4));
+    if (best) NAJU_TRY(need_ws(ws, ws_bytes, logits_ws_bytes(rows)));
+    LogitsArgs g{};
+    g.B = rows;
+    g.V = vocab;
+    g.tile = rows * ((vocab + kLogTile - 1) / kLogTile) >= 512 ? kLogTile : kLogSmallTile;
+    g.n_tiles = (vocab + g.tile - 1) / g.tile;
+    g.ld = ld;
+    g.history = history;
+    g.H = history_len;
+    g.lengths = lengths;
+    g.rep = repetition;
+    g.pres = presence;
+    g.freq = frequency;
+    g.bias_ids = bias_ids;
+    g.bias = bias;
+    g.nb = (int)n_bias;
+    g.mask = mask;
+    g.out = out;
+    g.best = best;
+    g.ws = (char *)ws;
+    hipStream_t st = (hipStream_t)stream;
+    return hip_status(io == NAJU_F32 ? launch_logits<float>(g, logits, st)
+                                     : launch_logits<bf16>(g, logits, st),
+                      "logits launch");
+}
+
+}  // extern "C"

@@ -69,6 +69,19 @@ int main()
            naju_distill_fwd_bwd(2, 8, 1, NAJU_F32, p, 8, ip, fp, 0.f, fp, fp, fp, p, 8, nullptr),
            NAJU_EINVAL);
 
+    for (int64_t R : Ts)
+        for (int64_t V : Vs)
+            for (int64_t n : {(int64_t)-1, (int64_t)0, (int64_t)4094, INT64_MAX}) {
+                (void)naju_logits_workspace_bytes(R);
+                const naju_status_t s = naju_logits_process(
+                    R, V, NAJU_F32, nullptr, V, nullptr, n, nullptr, nullptr, nullptr, nullptr,
+                    nullptr, nullptr, n, nullptr, nullptr, nullptr, nullptr, 0, nullptr);
+                if (R > 0 && V > 0 && s == NAJU_OK) {
+                    std::fprintf(stderr, "logits_process without pointers accepted\n");
+                    ++failures;
+                }
+            }
+
     if (failures) return 1;
     std::puts("lm driver: ok");
     return 0;

@@ -92,3 +92,32 @@ def test_distill_refusals(lib):
         expect(call(g=None), nb.EINVAL, "g is NULL")
         expect(call(d=None), nb.EINVAL, "dlogits is NULL")
         expect(call(ldd=99), nb.EINVAL, "row stride of dlogits")
+
+
+def test_logits_refusals(lib):
+    def call(R=4, V=100, io=nb.BF16, logits=FAKE, ld=100, hist=FAKE, H=10, lengths=None, rep=None,
+             pres=None, freq=None, ids=FAKE, bias=FAKE, n=3, mask=None, out=FAKE, best=FAKE,
+             ws=FAKE, wsb=1 << 30):
+        return lib.naju_logits_process(R, V, io, logits, ld, hist, H, lengths, rep, pres, freq,
+                                       ids, bias, n, mask, out, best, ws, wsb, None)
+    expect(call(R=-1), nb.EINVAL, "negative size")
+    expect(call(H=-1), nb.EINVAL, "negative size")
+    expect(call(n=-1), nb.EINVAL, "negative size")
+    expect(call(R=2 ** 25), nb.EINVAL, "too large")
+    expect(call(io=4), nb.EINVAL, "io dtype")
+    expect(call(H=2 ** 20), nb.EUNSUPPORTED, "history_len")
+    expect(call(n=4095), nb.EUNSUPPORTED, "n_bias")
+    expect(call(ld=99), nb.EINVAL, "row stride")
+    expect(call(logits=None), nb.EINVAL, "logits is NULL")
+    expect(call(out=None), nb.EINVAL, "out is NULL")
+    expect(call(hist=None), nb.EINVAL, "history is NULL")
+    expect(call(ids=None), nb.EINVAL, "bias_ids is NULL")
+    expect(call(bias=None), nb.EINVAL, "bias is NULL")
+    for name in ("lengths", "rep", "pres", "freq", "mask"):
+        expect(call(**{name: FAKE + 2}), nb.EINVAL, "aligned")
+    expect(call(best=FAKE + 2), nb.EINVAL, "best is not")
+    expect(call(ws=None), nb.EWORKSPACE, "workspace is NULL")
+    expect(call(wsb=16), nb.EWORKSPACE, "needs")
+    assert call(R=0, logits=None, out=None, ws=None) == nb.OK
+    assert lib.naju_logits_workspace_bytes(100) >= 1600
+    assert lib.naju_logits_workspace_bytes(-1) == 0

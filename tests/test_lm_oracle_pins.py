@@ -81,3 +81,20 @@ def test_distill_empty_and_impossible_rows():
     loss, _, grad = lm.distill(x, ids, t, 1.0, np.ones(2))
     assert loss[0] == 0 and not grad[0].any()       # no valid entry
     assert loss[1] == np.inf and grad[1, 0] == -0.5  # a target where the student has 0
+
+
+def test_logits_process_by_hand():
+    x = np.array([[2.0, -2.0, 1.0, 4.0, 4.0], [0.0, 0.0, 0.0, 0.0, 0.0]])
+    hist = np.array([[0, 1, 1, -1, 9, 3], [2, 2, 2, 2, 2, 2]])
+    out, best = lm.logits_process(x, hist, np.array([5, 0]), np.array([2.0, 2.0]),
+                                  np.array([0.25, 1.0]), np.array([0.5, 1.0]),
+                                  np.array([[2, 2, 9], [-1, 1, 1]]),
+                                  np.array([[10.0, 99.0, 99.0], [99.0, -1.0, 99.0]]))
+    #               2/2 - .5 - .25, -2*2 - 1 - .25, 1 + 10
+    assert np.array_equal(out, [[0.25, -5.25, 11.0, 4.0, 4.0], [0.0, -1.0, 0.0, 0.0, 0.0]])
+    assert best.tolist() == [2, 0]
+    out, best = lm.logits_process(x, mask=np.array([[0b11010], [0]]))
+    assert np.array_equal(out[0], [-np.inf, -2.0, -np.inf, 4.0, 4.0])
+    assert best.tolist() == [3, -1]
+    nan = np.array([[np.nan, 1.0, np.nan, 1.0]])
+    assert lm.logits_process(nan)[1].tolist() == [1]
