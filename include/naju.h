@@ -437,6 +437,40 @@ naju_status_t naju_logits_process(int64_t rows, int64_t vocab, int32_t io, const
                                   const uint32_t *mask, float *out, int32_t *best, void *ws,
                                   size_t ws_bytes, void *stream);
 
+/*
+ * Linear layer with 4-bit weights, for the few rows of a decode step:
+ *     y[r][n] = sum_k x[r][k] (q[n][k] - z[n][k / group]) s[n][k / group]
+ *               + bias[n] + res[r][n]
+ * summed in fp32, one rounding to bf16.  No workspace.
+ *   x         [rows][d_in] bf16
+ *   qweight   [d_out][d_in / 2] uint8: the code of input 2i in the low half of byte
+ *             i, that of input 2i + 1 in the high half (any alignment)
+ *   scales    [d_out][ceil(d_in / group)] bf16
+ *   zeros     [d_out][ceil(d_in / group)] uint8, or NULL (= 8 everywhere)
+ *   bias      [d_out] fp32 or NULL;  res [rows][d_out] bf16 or NULL
+ *   y         [rows][d_out] bf16 (written)
+ * d_in even, at most 2^24; d_out <= 2^26; group 32, 64 or 128 (the last group of a
+ * row may be shorter).  Any number of rows up to 2^20; the weights are read once
+ * for every 64 of them.  An infinite or NaN x makes its row of y NaN or infinite.
+ */
+naju_status_t naju_w4_linear(int64_t rows, int64_t d_in, int64_t d_out, int64_t group,
+                             const void *x, const uint8_t *qweight, const void *scales,
+                             const uint8_t *zeros, const float *bias, const void *res, void *y,
+                             void *stream);
+
+/*
+ * Quantises weights stored [in][out], as the mixer layer's are, into that
+ * layout.  Per output and group, to the nearest code: without zeros
+ * s = max|w| / 7 and codes 8 + round(w / s); with them s = (max(w, 0) -
+ * min(w, 0)) / 15, z = round(-min / s) and codes z + round(w / s), into 0 .. 15.
+ * The scale is rounded to bf16 before the codes are formed.
+ *   W         [d_in][d_out] io (fp32 or bf16), finite
+ *   qweight, scales (written);  zeros (written) or NULL (codes around 8)
+ */
+naju_status_t naju_w4_quantize(int64_t d_in, int64_t d_out, int64_t group, int32_t io,
+                               const void *W, uint8_t *qweight, void *scales, uint8_t *zeros,
+                               void *stream);
+
 /* Thread-local description of the last non-OK status ("" if none). */
 const char *naju_last_error(void);
 

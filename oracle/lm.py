@@ -93,3 +93,27 @@ def logits_process(logits, history=None, lengths=None, repetition=None, presence
         if V and x.max() > -np.inf:
             best[b] = int(np.flatnonzero(x == x.max())[0])
     return out, best
+
+
+def w4_weights(qweight, scales, group, zeros=None):
+    """The weights [d_out, d_in] that codes, scales and zeros stand for."""
+    q = np.asarray(qweight, dtype=np.int64)
+    N, half = q.shape
+    w = np.zeros((N, 2 * half))
+    for i in range(half):
+        w[:, 2 * i] = q[:, i] % 16
+        w[:, 2 * i + 1] = q[:, i] // 16
+    for k in range(2 * half):
+        z = 8.0 if zeros is None else np.asarray(zeros[:, k // group], dtype=np.float64)
+        w[:, k] = (w[:, k] - z) * np.asarray(scales[:, k // group], dtype=np.float64)
+    return w
+
+
+def w4_linear(x, qweight, scales, group, zeros=None, bias=None, res=None):
+    """y = x W^T + bias + res with the weights above."""
+    y = np.asarray(x, dtype=np.float64) @ w4_weights(qweight, scales, group, zeros).T
+    if bias is not None:
+        y = y + np.asarray(bias, dtype=np.float64)
+    if res is not None:
+        y = y + np.asarray(res, dtype=np.float64)
+    return y

@@ -30,7 +30,8 @@ EXPORTS = ("naju_workspace_bytes", "naju_ckpt_bytes", "naju_workspace_init",
            "naju_mixer_fwd", "naju_mixer_bwd_workspace_bytes", "naju_mixer_bwd",
            "naju_scan_fwd_noalloc", "naju_embed_fwd", "naju_embed_bwd_workspace_bytes",
            "naju_embed_bwd", "naju_distill_fwd", "naju_distill_bwd", "naju_distill_fwd_bwd",
-           "naju_logits_workspace_bytes", "naju_logits_process", "naju_last_error", "naju_version")
+           "naju_logits_workspace_bytes", "naju_logits_process", "naju_w4_linear", "naju_w4_quantize",
+           "naju_last_error", "naju_version")
 
 
 class NajuError(RuntimeError):
@@ -113,6 +114,10 @@ def lib() -> ctypes.CDLL:
         L.naju_logits_process.argtypes = ([i64, i64, i32, vp, i64, vp, i64] + [vp] * 6 +
                                           [i64, vp, vp, vp, vp, sz, vp])
         L.naju_logits_process.restype = st
+        L.naju_w4_linear.argtypes = [i64, i64, i64, i64] + [vp] * 8
+        L.naju_w4_linear.restype = st
+        L.naju_w4_quantize.argtypes = [i64, i64, i64, i32] + [vp] * 5
+        L.naju_w4_quantize.restype = st
         L.naju_last_error.argtypes = []
         L.naju_last_error.restype = ctypes.c_char_p
         L.naju_version.argtypes = []
@@ -631,3 +636,42 @@ def logits_process(logits, history=None, lengths=None, repetition=None, presence
                                     _p(bias), nb, _p(mask), _p(out), _p(best), ws.ptr, ws.nbytes,
                                     stream_handle(dev)))
     return out, best
+
+
+def w4_quantize(W, group=64, *, zeros=False):
+    """qweight, scales, zeros = naju_w4_quantize(W): weights W [d_in, d_out] (fp32 or bf16) as
+    4-bit codes with one bf16 scale per `group` inputs of an output.  zeros=False: codes around
+    8, and None is returned for the zeros."""
+    K, N = W.shape
+    dev = W.device
+    io = _io_of(W)
+    _req(W, "W", (K, N), W.dtype, dev)
+    ng = -(-K // group)
+    qw = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((N, ng), dtype=torch.bfloat16, device=dev)
+    z = torch.empty((N, ng), dtype=torch.uint8, device=dev) if zeros else None
+    check(lib().naju_w4_quantize(K, N, group, io, _p(W), _p(qw), _p(scales), _p(z),
+                                 stream_handle(dev)))
+    return qw, scales, z
+
+
+def w4_linear(x, qweight, scales, group, zeros=None, bias=None, res=None):
+    """y = naju_w4_linear(x, ...), bf16 [rows, d_out]: x bf16 [rows, d_in], qweight uint8
+    [d_out, d_in / 2], scales bf16 and zeros uint8 (None: 8) [d_out, ceil(d_in / group)], bias
+    fp32 [d_out] or None, res bf16 [rows, d_out] or None."""
+    R, K = x.shape
+    N = qweight.shape[0]
+    dev = x.device
+    ng = -(-K // group)
+    if K % 2:
+        raise ValueError("x: an odd number of inputs (two codes share a byte)")
+    _req(x, "x", (R, K), torch.bfloat16, dev)
+    _req(qweight, "qweight", (N, K // 2), torch.uint8, dev)
+    _req(scales, "scales", (N, ng), torch.bfloat16, dev)
+    _opt(zeros, "zeros", (N, ng), torch.uint8, dev)
+    _opt(bias, "bias", (N,), torch.float32, dev)
+    _opt(res, "res", (R, N), torch.bfloat16, dev)
+    y = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+    check(lib().naju_w4_linear(R, K, N, group, _p(x), _p(qweight), _p(scales), _p(zeros),
+                               _p(bias), _p(res), _p(y), stream_handle(dev)))
+    return y

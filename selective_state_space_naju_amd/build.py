@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libnaju.so")
 SOURCES = ["naju_api.hip", "naju_fwd.hip", "naju_fwd_mfma.hip", "naju_fwd_mfma64.hip", "naju_bwd.hip",
            "naju_bwd_mfma.hip",
            "naju_step.hip", "naju_mixer.hip", "naju_embed.hip",
-           "naju_distill.hip", "naju_logits.hip"]
+           "naju_distill.hip", "naju_logits.hip", "naju_w4.hip"]
 ARCH = os.environ.get("NAJU_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -82,6 +82,21 @@ int main()
                 }
             }
 
+    for (int64_t R : Ts)
+        for (int64_t K : Vs)
+            for (int64_t G : {(int64_t)0, (int64_t)32, (int64_t)-64, INT64_MIN}) {
+                const naju_status_t s = naju_w4_linear(R, K, 5, G, nullptr, nullptr, nullptr,
+                                                       nullptr, nullptr, nullptr, nullptr, nullptr);
+                if (R > 0 && s == NAJU_OK) {
+                    std::fprintf(stderr, "w4_linear without pointers accepted\n");
+                    ++failures;
+                }
+                expect("w4_quantize without pointers",
+                       naju_w4_quantize(2, R > 0 ? 3 : -1, G, NAJU_F32, nullptr, nullptr, nullptr,
+                                        nullptr, nullptr),
+                       G == 32 || R <= 0 ? NAJU_EINVAL : NAJU_EUNSUPPORTED);
+            }
+
     if (failures) return 1;
     std::puts("lm driver: ok");
     return 0;

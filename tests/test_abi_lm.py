@@ -121,3 +121,29 @@ def test_logits_refusals(lib):
     assert call(R=0, logits=None, out=None, ws=None) == nb.OK
     assert lib.naju_logits_workspace_bytes(100) >= 1600
     assert lib.naju_logits_workspace_bytes(-1) == 0
+
+
+def test_w4_refusals(lib):
+    def lin(R=2, K=64, N=10, G=32, x=FAKE, q=FAKE, s=FAKE, z=None, bias=None, res=None, y=FAKE):
+        return lib.naju_w4_linear(R, K, N, G, x, q, s, z, bias, res, y, None)
+
+    def quant(K=64, N=10, G=32, io=nb.F32, W=FAKE, q=FAKE, s=FAKE, z=None):
+        return lib.naju_w4_quantize(K, N, G, io, W, q, s, z, None)
+    for call in (lin, quant):
+        expect(call(K=-2), nb.EINVAL, "negative size")
+        expect(call(K=63), nb.EUNSUPPORTED, "odd")
+        expect(call(G=16), nb.EUNSUPPORTED, "group")
+        expect(call(N=2 ** 27), nb.EINVAL, "too large")
+        expect(call(q=None), nb.EINVAL, "qweight is NULL")
+        expect(call(s=FAKE + 1), nb.EINVAL, "aligned")
+        assert call(N=0, q=None, s=None) == nb.OK
+    expect(lin(R=-1), nb.EINVAL, "negative size")
+    expect(lin(R=2 ** 21), nb.EINVAL, "too large")
+    expect(lin(x=None), nb.EINVAL, "x is NULL")
+    expect(lin(y=None), nb.EINVAL, "y is NULL")
+    expect(lin(bias=FAKE + 2), nb.EINVAL, "aligned")
+    expect(lin(res=FAKE + 1), nb.EINVAL, "aligned")
+    expect(quant(io=5), nb.EINVAL, "io dtype")
+    expect(quant(W=None), nb.EINVAL, "W is NULL")
+    assert lin(R=0, x=None, y=None) == nb.OK
+    assert quant(K=0, W=None) == nb.OK

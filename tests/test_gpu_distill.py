@@ -12,7 +12,7 @@ weights that sum to 1: |loss error| <= tau^2 u (30 X' + 64 + V/512) with X' also
 over the teacher's values, plus the rounding of p against the size of the gaps,
 16 u max|gap| tau^2.  The gradient's q has relative error e_q = u (20 X + 64 +
 V/512), p the same with X', so |err| <= |g| tau (q e_q + p e_q) + the io rounding
-(2^-9 relative, and the fp32 one) of the result.
+(2^-8 relative for bf16) of the result.
 """
 import numpy as np
 import pytest

@@ -2,7 +2,7 @@
 
 Tolerances, derived before the first run.  Forward: one fp32 product, then one
 rounding to the io type: 2^-24 relative for fp32 output (the fp32 product's own
-rounding), 2^-8 for bf16 (half a spacing, 2^-9, plus the fp32 rounding that can
+rounding), 2^-8 for bf16 (half a spacing; the fp32 rounding before it can only
 move a tie).  Gradient: the sum of n rows is formed in fp32 in an order the sort
 fixes, at most n - 1 additions and one product: |err| <= n 2^-23 sum |terms|,
 with n the number of occurrences of the token.  Ids are exact: a row of a token

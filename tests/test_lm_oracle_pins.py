@@ -98,3 +98,15 @@ def test_logits_process_by_hand():
     assert best.tolist() == [3, -1]
     nan = np.array([[np.nan, 1.0, np.nan, 1.0]])
     assert lm.logits_process(nan)[1].tolist() == [1]
+
+
+def test_w4_weights_by_hand():
+    # bytes 0x2f 0x08: codes 15, 2, 8, 0; groups of 2
+    q = np.array([[0x2f, 0x08], [0x00, 0xff]], dtype=np.uint8)
+    s = np.array([[0.5, 2.0], [1.0, 0.25]])
+    assert np.array_equal(lm.w4_weights(q, s, 2), [[3.5, -3.0, 0.0, -16.0], [-8, -8, 1.75, 1.75]])
+    z = np.array([[15, 0], [1, 3]], dtype=np.uint8)
+    assert np.array_equal(lm.w4_weights(q, s, 2, z), [[0.0, -6.5, 16.0, 0.0], [-1, -1, 3, 3]])
+    x = np.array([[1.0, 0.0, 2.0, 0.0]])
+    assert np.array_equal(lm.w4_linear(x, q, s, 2, bias=np.array([1.0, 2.0]),
+                                       res=np.array([[0.5, 0.0]])), [[5.0, -2.5]])
