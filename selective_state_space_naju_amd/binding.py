@@ -157,11 +157,24 @@ def ckpt_bytes(dims: Dims) -> int:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def stream_handle(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(dev) -> int:
+    """The current stream's handle on dev (a device of tensors), without building a stream
+    object: 4 us less a call, which single-token calls notice."""
+    if dev.type != "cuda":
+        raise ValueError("tensors must be on a GPU, got %s" % dev)
+    if _raw_stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index)
 
 
 class Workspace:
@@ -208,6 +221,9 @@ def _io_of(t: torch.Tensor) -> int:
 
 
 def _req(t, name, shape, dtype, device):
+    if (t is not None and t.shape == shape and t.dtype == dtype and t.device == device
+            and t.is_contiguous()):
+        return t
     if t is None:
         raise ValueError("%s is required" % name)
     if tuple(t.shape) != tuple(shape):
@@ -481,9 +497,9 @@ def mixer_bwd(xn, W_u, W_z, conv_w, W_a, a_bias, W_b, b_bias, W_B, W_C, D, W_out
 
 
 # ------------------------------------------------- around the mixer layer
-def _cached_workspace(kind, sizes, nbytes, dev) -> Workspace:
+def _cached_workspace(kind, sizes, nbytes, dev, stream) -> Workspace:
     """Cached workspace per (device, stream, kind, sizes); nbytes() is asked once."""
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream, kind) + sizes
+    key = (dev.index, stream, kind) + sizes
     ws = _ws_cache.get(key)
     if ws is None:
         ws = _ws_cache[key] = Workspace(nbytes(), dev)
@@ -495,12 +511,12 @@ def embed_fwd(ids, W, scale=1.0):
     the vocabulary.  ids: int32 of any shape; W [vocab, d_model]; out ids.shape + (d_model,)."""
     V, d = W.shape
     dt, dev = W.dtype, W.device
-    io = _io_of(W)
+    io, st = _io_of(W), _stream(dev)
     _req(W, "W", (V, d), dt, dev)
     _req(ids, "ids", ids.shape, torch.int32, dev)
     out = torch.empty(tuple(ids.shape) + (d,), dtype=dt, device=dev)
     check(lib().naju_embed_fwd(ids.numel(), V, d, io, _p(ids), _p(W), float(scale), _p(out),
-                               stream_handle(dev)))
+                               st))
     return out
 
 
@@ -509,7 +525,7 @@ def embed_bwd(ids, dout, vocab, scale=1.0, *, dW=None, ws=None):
     gradient is added to it (rows of tokens that do not occur are not touched)."""
     d = dout.shape[-1]
     dt, dev = dout.dtype, dout.device
-    io = _io_of(dout)
+    io, st = _io_of(dout), _stream(dev)
     _req(ids, "ids", ids.shape, torch.int32, dev)
     _req(dout, "dout", tuple(ids.shape) + (d,), dt, dev)
     _opt(dW, "dW", (vocab, d), torch.float32, dev)
@@ -519,9 +535,9 @@ def embed_bwd(ids, dout, vocab, scale=1.0, *, dW=None, ws=None):
     T = ids.numel()
     ws = ws or _cached_workspace(
         "embed_bwd", (T, vocab, d),
-        lambda: lib().naju_embed_bwd_workspace_bytes(T, vocab, d), dev)
+        lambda: lib().naju_embed_bwd_workspace_bytes(T, vocab, d), dev, st)
     check(lib().naju_embed_bwd(T, vocab, d, io, _p(ids), _p(dout), float(scale),
-                               int(accumulate), _p(dW), ws.ptr, ws.nbytes, stream_handle(dev)))
+                               int(accumulate), _p(dW), ws.tensor.data_ptr(), ws.nbytes, st))
     return dW
 
 
@@ -529,7 +545,7 @@ def _req_rows(t, name, shape, dtype, device) -> int:
     """A matrix of contiguous rows, any distance apart; returns that distance."""
     if t is None:
         raise ValueError("%s is required" % name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if t.dtype != dtype:
         raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
@@ -549,11 +565,11 @@ def _distill_args(logits, t_ids, t_logits, temperature):
         raise ValueError("logits: the vocabulary is empty")
     k = t_ids.shape[1]
     dt, dev = logits.dtype, logits.device
-    io = _io_of(logits)
+    io, st = _io_of(logits), _stream(dev)
     ld = _req_rows(logits, "logits", (R, V), dt, dev)
     _req(t_ids, "t_ids", (R, k), torch.int32, dev)
     _req(t_logits, "t_logits", (R, k), torch.float32, dev)
-    return R, V, dev, (R, V, k, io, _p(logits), ld, _p(t_ids), _p(t_logits), float(temperature))
+    return R, dev, st, (R, V, k, io, _p(logits), ld, _p(t_ids), _p(t_logits), float(temperature))
 
 
 def _distill_grad_out(logits, g, dlogits):
@@ -568,32 +584,32 @@ def distill_fwd(logits, t_ids, t_logits, temperature=1.0):
     """loss, lse = naju_distill_fwd(...), fp32 [rows] each.  logits [rows, vocab] (contiguous
     rows, any row stride); t_ids int32 and t_logits fp32 [rows, k]: the teacher's top logits
     (index -1 or value -inf: no entry)."""
-    R, V, dev, args = _distill_args(logits, t_ids, t_logits, temperature)
+    R, dev, st, args = _distill_args(logits, t_ids, t_logits, temperature)
     loss = torch.empty(R, dtype=torch.float32, device=dev)
     lse = torch.empty(R, dtype=torch.float32, device=dev)
-    check(lib().naju_distill_fwd(*args, _p(loss), _p(lse), stream_handle(dev)))
+    check(lib().naju_distill_fwd(*args, _p(loss), _p(lse), st))
     return loss, lse
 
 
 def distill_bwd(logits, t_ids, t_logits, lse, g, temperature=1.0, *, dlogits=None):
     """dlogits = naju_distill_bwd(...) for the upstream gradient g [rows] of the loss and the
     lse that distill_fwd returned; dlogits: a tensor to write (contiguous rows, any stride)."""
-    R, V, dev, args = _distill_args(logits, t_ids, t_logits, temperature)
+    R, dev, st, args = _distill_args(logits, t_ids, t_logits, temperature)
     _req(lse, "lse", (R,), torch.float32, dev)
     dlogits, ldd = _distill_grad_out(logits, g, dlogits)
-    check(lib().naju_distill_bwd(*args, _p(lse), _p(g), _p(dlogits), ldd, stream_handle(dev)))
+    check(lib().naju_distill_bwd(*args, _p(lse), _p(g), _p(dlogits), ldd, st))
     return dlogits
 
 
 def distill_fwd_bwd(logits, t_ids, t_logits, g, temperature=1.0, *, dlogits=None):
     """loss, dlogits = naju_distill_fwd_bwd(...): both in one pass over the logits, for row
     weights g that are known before the loss."""
-    R, V, dev, args = _distill_args(logits, t_ids, t_logits, temperature)
+    R, dev, st, args = _distill_args(logits, t_ids, t_logits, temperature)
     loss = torch.empty(R, dtype=torch.float32, device=dev)
     lse = torch.empty(R, dtype=torch.float32, device=dev)
     dlogits, ldd = _distill_grad_out(logits, g, dlogits)
     check(lib().naju_distill_fwd_bwd(*args, _p(g), _p(loss), _p(lse), _p(dlogits), ldd,
-                                     stream_handle(dev)))
+                                     st))
     return loss, dlogits
 
 
@@ -610,7 +626,7 @@ def logits_process(logits, history=None, lengths=None, repetition=None, presence
     if V == 0:
         raise ValueError("logits: the vocabulary is empty")
     dt, dev = logits.dtype, logits.device
-    io = _io_of(logits)
+    io, st = _io_of(logits), _stream(dev)
     ld = _req_rows(logits, "logits", (R, V), dt, dev)
     H = nb = 0
     if history is not None:
@@ -630,11 +646,11 @@ def logits_process(logits, history=None, lengths=None, repetition=None, presence
     out = torch.empty((R, V), dtype=torch.float32, device=dev)
     best = torch.empty((R,), dtype=torch.int32, device=dev)
     ws = ws or _cached_workspace("logits", (R,),
-                                 lambda: lib().naju_logits_workspace_bytes(R), dev)
+                                 lambda: lib().naju_logits_workspace_bytes(R), dev, st)
     check(lib().naju_logits_process(R, V, io, _p(logits), ld, _p(history), H, _p(lengths),
                                     _p(repetition), _p(presence), _p(frequency), _p(bias_ids),
-                                    _p(bias), nb, _p(mask), _p(out), _p(best), ws.ptr, ws.nbytes,
-                                    stream_handle(dev)))
+                                    _p(bias), nb, _p(mask), _p(out), _p(best), ws.tensor.data_ptr(),
+                                    ws.nbytes, st))
     return out, best
 
 
@@ -644,14 +660,14 @@ def w4_quantize(W, group=64, *, zeros=False):
     8, and None is returned for the zeros."""
     K, N = W.shape
     dev = W.device
-    io = _io_of(W)
+    io, st = _io_of(W), _stream(dev)
     _req(W, "W", (K, N), W.dtype, dev)
     ng = -(-K // group)
     qw = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
     scales = torch.empty((N, ng), dtype=torch.bfloat16, device=dev)
     z = torch.empty((N, ng), dtype=torch.uint8, device=dev) if zeros else None
     check(lib().naju_w4_quantize(K, N, group, io, _p(W), _p(qw), _p(scales), _p(z),
-                                 stream_handle(dev)))
+                                 st))
     return qw, scales, z
 
 
@@ -662,6 +678,7 @@ def w4_linear(x, qweight, scales, group, zeros=None, bias=None, res=None):
     R, K = x.shape
     N = qweight.shape[0]
     dev = x.device
+    st = _stream(dev)
     ng = -(-K // group)
     if K % 2:
         raise ValueError("x: an odd number of inputs (two codes share a byte)")
@@ -673,5 +690,5 @@ def w4_linear(x, qweight, scales, group, zeros=None, bias=None, res=None):
     _opt(res, "res", (R, N), torch.bfloat16, dev)
     y = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
     check(lib().naju_w4_linear(R, K, N, group, _p(x), _p(qweight), _p(scales), _p(zeros),
-                               _p(bias), _p(res), _p(y), stream_handle(dev)))
+                               _p(bias), _p(res), _p(y), st))
     return y
