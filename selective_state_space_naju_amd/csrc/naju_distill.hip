@@ -24,6 +24,7 @@ namespace naju {
 constexpr int kDistThreads = 512;
 constexpr int kDistWaves = kDistThreads / 64;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLn2 = 0.6931471805599453f;
 
 // running maximum and sum of exp(. - maximum)
 struct MaxSum {
@@ -215,6 +216,160 @@ __global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(
     }
 }
 
+// ------------------------------------------------- loss and gradient at once
+// The row stays in registers between its statistics and its gradient, NV
+// accesses per thread: every logit is read once and every gradient written
+// once.  Exponents are formed in base 2 with the maximum of the wave, so one
+// barrier joins the row's and the list's statistics; q is exp2(x - m) over the
+// row's sum, with no rounded lse in between.  Places past the row hold -inf,
+// which adds nothing.
+template <typename IO> __device__ __forceinline__ IO neg_inf_raw();
+template <> __device__ __forceinline__ float neg_inf_raw<float>() { return kNegInf; }
+template <> __device__ __forceinline__ bf16 neg_inf_raw<bf16>() { return 0xff80; }
+
+//
+// The waves per SIMD that the launch bounds ask for keep the row's packed words
+// (4 NV registers) and little else live, so that several workgroups share a CU
+// and one loads while another computes.
+template <typename IO, int NV>
+__global__ __launch_bounds__(kDistThreads, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_step_kernel(
+    const uint32_t V, const int k, const IO *__restrict__ logits, const int64_t ld,
+    const int32_t *__restrict__ t_ids, const float *__restrict__ t_logits, const float tau,
+    const float inv_tau, const float *__restrict__ g, float *__restrict__ loss,
+    float *__restrict__ lse, IO *__restrict__ dlogits, const int64_t ldd)
+{
+    constexpr int n = kPer16<IO>;
+    constexpr uint32_t per = kDistThreads * n;
+    __shared__ MaxSum row_ms[kDistWaves], ent_ms[kDistWaves];
+    __shared__ float sum[kDistWaves];
+    __shared__ int ids[kDistThreads];
+    __shared__ float ps[kDistThreads];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const float c2 = inv_tau * kLog2e;
+    const int64_t r = blockIdx.x;
+    const IO *row = logits + r * ld;
+    IO *out = dlogits + r * ldd;
+    const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
+    const float gr = g[r];
+    // an access past the row's end is moved back to end there: no load waits on a branch
+    const uint32_t last = V - n;
+    Run<IO, n> v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const uint32_t c = i * per + tid * n;
+        v[i].load_at(row, (c < last ? c : last) * (uint32_t)sizeof(IO));
+    }
+    const float at = e.id >= 0 ? to_f(row[e.id]) : 0.f;
+    const MaxSum es = entry_maxsum(e);
+    // what an access moved back holds of its neighbours is taken for -inf
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if ((i + 1) * per > V) {  // (uniform)
+            const int twice = (int)(i * per + tid * n - last);
+#pragma unroll
+            for (int j = 0; j < n; ++j)
+                if (twice > j) v[i].set_raw(j, neg_inf_raw<IO>());
+        }
+    }
+    // the row, in base 2: maximum of the wave, sum of exp2(x - maximum)
+    float top = kNegInf;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (i * per < V) {
+#pragma unroll
+            for (int j = 0; j < n; ++j) top = fmaxf(top, v[i].get(j));
+        }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+    const float m_wave = base_of(top) * c2;
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (i * per < V) {
+            v[i].repack();
+#pragma unroll
+            for (int j = 0; j < n; ++j) s += ex2(fmaf(v[i].get(j), c2, -m_wave));
+            v[i].repack();
+        }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if (lane == 0) {
+        row_ms[w] = {top == kNegInf ? kNegInf : m_wave, s};
+        ent_ms[w] = es;
+    }
+    __syncthreads();
+    const MaxSum ts = join_maxsum(ent_ms);
+    float m = row_ms[0].m;
+#pragma unroll
+    for (int i = 1; i < kDistWaves; ++i) m = fmaxf(m, row_ms[i].m);
+    const float b = base_of(m);
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDistWaves; ++i) s += row_ms[i].s * ex2(row_ms[i].m - b);
+    // the entries: their probabilities and their terms of the loss
+    const float log2_s = log2f(s), log_t = logf(ts.s);
+    float p = 0.f, term = 0.f;
+    if (e.id >= 0) {
+        const float gap = e.t - base_of(ts.m);
+        p = exp_nat(gap) / ts.s;
+        const float logq = at == kNegInf ? kNegInf : (fmaf(at, c2, -b) - log2_s) * kLn2;
+        if (!(p == 0.f)) term = p * ((gap - log_t) - logq);
+    }
+    ids[tid] = e.id;
+    ps[tid] = p;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) term += __shfl_xor(term, o);
+    if (lane == 0) sum[w] = term;
+    // the dense part of the gradient: f q_v (a row of -inf alone has q = 0)
+    const bool some = ts.m != kNegInf && gr != 0.f;
+    const float f = some ? gr * tau : 0.f;
+    const float fq = m == kNegInf ? 0.f : f / s;
+    uint32_t c0 = tid * n;
+    asm volatile("" : "+v"(c0));  // (offsets formed anew, not kept since the loads)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (i * per < V) {
+            const uint32_t c = i * per + c0;
+            float d[n];
+#pragma unroll
+            for (int j = 0; j < n; ++j) d[j] = fq * ex2(fmaf(v[i].get(j), c2, -b));
+            Run<IO, n> o = round_run<IO, n>(d);
+            if (!some) o.zero();
+            if (c <= last) {
+                o.store_at(out, c * (uint32_t)sizeof(IO));
+            } else if (c < V) {
+#pragma unroll
+                for (int j = 1; j < n; ++j)
+                    if (j >= (int)(c - last)) out[last + j] = o.get_raw(j);
+            }
+        }
+    }
+    // the dense stores are done before an element is written again
+    wait_mem();
+    __syncthreads();
+    if (tid == 0) {
+        float t = 0.f;
+        for (int i = 0; i < kDistWaves; ++i) t += sum[i];
+        loss[r] = tau * tau * t;
+        lse[r] = m == kNegInf ? kNegInf : (m + log2_s) * kLn2;
+    }
+    if (some && e.id >= 0) {
+        float all = 0.f;
+        bool first = true;
+        for (int j = 0; j < k; ++j)
+            if (ids[j] == e.id) {
+                first = first && j >= tid;
+                all += ps[j];
+            }
+        if (first) {
+            const float q = m == kNegInf ? 0.f : ex2(fmaf(at, c2, -b)) / s;
+            out[e.id] = from_f<IO>(f * (q - all));
+        }
+    }
+}
+
 struct DistillArgs {
     int64_t R, V;
     int k;
@@ -247,6 +402,37 @@ template <typename IO> static hipError_t launch_grad(const DistillArgs &a, hipSt
                        a.k, n_chunks, (const IO *)a.logits, a.ld, a.t_ids, a.t_logits, a.tau,
                        1.f / a.tau, a.lse, a.g, (IO *)a.dlogits, a.ldd);
     return hipGetLastError();
+}
+
+template <typename IO, int NV>
+static hipError_t launch_step_t(const DistillArgs &a, hipStream_t st)
+{
+    constexpr int64_t most = 1 << 22;  // rows of a launch
+    for (int64_t r = 0; r < a.R; r += most) {
+        const int64_t rows = a.R - r < most ? a.R - r : most;
+        hipLaunchKernelGGL((distill_step_kernel<IO, NV>), dim3((unsigned)rows), dim3(kDistThreads),
+                           0, st, (uint32_t)a.V, a.k, (const IO *)a.logits + r * a.ld, a.ld,
+                           a.t_ids + r * a.k, a.t_logits + r * a.k, a.tau, 1.f / a.tau, a.g + r,
+                           a.loss + r, a.lse + r, (IO *)a.dlogits + r * a.ldd, a.ldd);
+    }
+    return hipGetLastError();
+}
+
+template <typename IO> static hipError_t launch_step(const DistillArgs &a, hipStream_t st)
+{
+    constexpr int64_t per = (int64_t)kDistThreads * kPer16<IO>;  // logits of one access each
+    if (a.V < kPer16<IO>) {  // (shorter than an access)
+        const hipError_t e = launch_loss<IO>(a, st);
+        return e == hipSuccess ? launch_grad<IO>(a, st) : e;
+    }
+    if (a.V <= 2 * per) return launch_step_t<IO, 2>(a, st);
+    if (a.V <= 4 * per) return launch_step_t<IO, 4>(a, st);
+    if (a.V <= 8 * per) return launch_step_t<IO, 8>(a, st);
+    if (a.V <= 16 * per) return launch_step_t<IO, 16>(a, st);
+    if (a.V <= 32 * per) return launch_step_t<IO, 32>(a, st);
+    // the row does not fit the registers: it is read again for the gradient
+    const hipError_t e = launch_loss<IO>(a, st);
+    return e == hipSuccess ? launch_grad<IO>(a, st) : e;
 }
 
 static naju_status_t check_distill(int64_t R, int64_t V, int64_t k, int32_t io, const void *logits,
@@ -338,10 +524,8 @@ naju_status_t naju_distill_fwd_bwd(int64_t rows, int64_t vocab, int64_t k, int32
     const DistillArgs a{rows, vocab, (int)k, logits, ld, t_ids, t_logits, temperature,
                         loss, lse, g, dlogits, ld_d};
     hipStream_t st = (hipStream_t)stream;
-    NAJU_TRY(hip_status(io == NAJU_F32 ? launch_loss<float>(a, st) : launch_loss<bf16>(a, st),
-                        "distillation loss launch"));
-    return hip_status(io == NAJU_F32 ? launch_grad<float>(a, st) : launch_grad<bf16>(a, st),
-                      "distillation gradient launch");
+    return hip_status(io == NAJU_F32 ? launch_step<float>(a, st) : launch_step<bf16>(a, st),
+                      "distillation launch");
 }
 
 }  // extern "C"

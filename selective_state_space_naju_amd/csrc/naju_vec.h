@@ -16,6 +16,13 @@ template <typename IO, int n> struct Run {
 
     __device__ __forceinline__ void load(const IO *p) { __builtin_memcpy(w, p, sizeof(w)); }
     __device__ __forceinline__ void store(IO *p) const { __builtin_memcpy(p, w, sizeof(w)); }
+    // at a 32-bit byte offset from an address that the wave shares
+    __device__ __forceinline__ void load_at(const IO *base, uint32_t bytes) {
+        __builtin_memcpy(w, (const char *)base + bytes, sizeof(w));
+    }
+    __device__ __forceinline__ void store_at(IO *base, uint32_t bytes) const {
+        __builtin_memcpy((char *)base + bytes, w, sizeof(w));
+    }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < kWords; ++i) w[i] = 0u;
@@ -35,6 +42,18 @@ template <typename IO, int n> struct Run {
     __device__ __forceinline__ IO get_raw(int i) const;
     __device__ __forceinline__ void put_raw(int i, IO v);
     __device__ __forceinline__ float get(int i) const { return to_f(get_raw(i)); }
+    // The packed words as if they were new: what was unpacked from them before is
+    // not kept in registers for a later use.
+    __device__ __forceinline__ void repack() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
+    }
+    // replaces an element
+    __device__ __forceinline__ void set_raw(int i, IO v) {
+        if constexpr (sizeof(IO) == 2) w[i / 2] &= 0xffff0000u >> (16 * (i % 2));
+        else w[i] = 0u;
+        put_raw(i, v);
+    }
 };
 
 template <typename IO, int n> __device__ __forceinline__ IO Run<IO, n>::get_raw(int i) const
@@ -45,7 +64,7 @@ template <typename IO, int n> __device__ __forceinline__ IO Run<IO, n>::get_raw(
 template <typename IO, int n> __device__ __forceinline__ void Run<IO, n>::put_raw(int i, IO v)
 {
     if constexpr (sizeof(IO) == 4) w[i] = __builtin_bit_cast(uint32_t, v);
-    else w[i / 2] |= (uint32_t)v << (16 * (i % 2));  // into a zeroed word
+    else w[i / 2] |= (uint32_t)v << (16 * (i % 2));  // (its half is zero)
 }
 
 // n floats rounded to the io type
