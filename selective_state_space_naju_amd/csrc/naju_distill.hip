@@ -21,8 +21,7 @@
 
 namespace naju {
 
-constexpr int kDistThreads = 512;
-constexpr int kDistWaves = kDistThreads / 64;
+constexpr int kMostEntries = 512;  // entries of a row: one per thread of a large workgroup
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -46,14 +45,14 @@ __device__ __forceinline__ MaxSum wave_maxsum(MaxSum a)
     return {M, s};
 }
 
-__device__ __forceinline__ MaxSum join_maxsum(const MaxSum *w)
+template <int kWaves> __device__ __forceinline__ MaxSum join_maxsum(const MaxSum *w)
 {
     float M = w[0].m;
 #pragma unroll
-    for (int i = 1; i < kDistWaves; ++i) M = fmaxf(M, w[i].m);
+    for (int i = 1; i < kWaves; ++i) M = fmaxf(M, w[i].m);
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kDistWaves; ++i) s += w[i].s * exp_nat(w[i].m - base_of(M));
+    for (int i = 0; i < kWaves; ++i) s += w[i].s * exp_nat(w[i].m - base_of(M));
     return {M, s};
 }
 
@@ -84,22 +83,22 @@ __device__ __forceinline__ MaxSum entry_maxsum(const Entry &e)
 
 // ------------------------------------------------------------------ loss
 // Reads the row once with a running maximum and sum per thread.
-template <typename IO>
-__global__ __launch_bounds__(kDistThreads) void distill_loss_kernel(
+template <typename IO, int BS>
+__global__ __launch_bounds__(BS) void distill_loss_kernel(
     const int64_t R, const int64_t V, const int k, const IO *__restrict__ logits,
     const int64_t ld, const int32_t *__restrict__ t_ids, const float *__restrict__ t_logits,
     const float tau, const float inv_tau, float *__restrict__ loss, float *__restrict__ lse)
 {
     constexpr int n = kPer16<IO>;
-    __shared__ MaxSum row_ms[kDistWaves], ent_ms[kDistWaves];
-    __shared__ float sum[kDistWaves];
+    __shared__ MaxSum row_ms[BS / 64], ent_ms[BS / 64];
+    __shared__ float sum[BS / 64];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
         const IO *row = logits + r * ld;
         const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
         const float at = e.id >= 0 ? to_f(row[e.id]) : 0.f;
         MaxSum a{kNegInf, 0.f};
-        for (int64_t c = (int64_t)tid * n; c < V; c += kDistThreads * n) {
+        for (int64_t c = (int64_t)tid * n; c < V; c += BS * n) {
             Run<IO, n> v;
             const int m = V - c < n ? (int)(V - c) : n;
             if (m == n) v.load(row + c);
@@ -121,7 +120,7 @@ __global__ __launch_bounds__(kDistThreads) void distill_loss_kernel(
             ent_ms[w] = es;
         }
         __syncthreads();
-        const MaxSum rs = join_maxsum(row_ms), ts = join_maxsum(ent_ms);
+        const MaxSum rs = join_maxsum<BS / 64>(row_ms), ts = join_maxsum<BS / 64>(ent_ms);
         const float log_s = logf(rs.s);
         float term = 0.f;
         if (e.id >= 0) {
@@ -137,7 +136,7 @@ __global__ __launch_bounds__(kDistThreads) void distill_loss_kernel(
         __syncthreads();
         if (tid == 0) {
             float t = 0.f;
-            for (int i = 0; i < kDistWaves; ++i) t += sum[i];
+            for (int i = 0; i < (BS / 64); ++i) t += sum[i];
             loss[r] = tau * tau * t;
             lse[r] = rs.m + log_s;
         }
@@ -151,8 +150,8 @@ __global__ __launch_bounds__(kDistThreads) void distill_loss_kernel(
 // written again with their share of p, by the first entry that names each.
 constexpr int kGradRuns = 4;
 
-template <typename IO>
-__global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(
+template <typename IO, int BS>
+__global__ __launch_bounds__(BS) void distill_grad_kernel(
     const int64_t R, const int64_t V, const int k, const int64_t n_chunks,
     const IO *__restrict__ logits, const int64_t ld, const int32_t *__restrict__ t_ids,
     const float *__restrict__ t_logits, const float tau, const float inv_tau,
@@ -160,10 +159,10 @@ __global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(
     const int64_t ldd)
 {
     constexpr int n = kPer16<IO>;
-    constexpr int64_t chunk = (int64_t)kDistThreads * n * kGradRuns;
-    __shared__ MaxSum ent_ms[kDistWaves];
-    __shared__ int ids[kDistThreads];
-    __shared__ float ps[kDistThreads];
+    constexpr int64_t chunk = (int64_t)BS * n * kGradRuns;
+    __shared__ MaxSum ent_ms[BS / 64];
+    __shared__ int ids[BS];
+    __shared__ float ps[BS];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     for (int64_t u = blockIdx.x; u < R * n_chunks; u += gridDim.x) {
         const int64_t r = u / n_chunks, c0 = (u - r * n_chunks) * chunk;
@@ -174,7 +173,7 @@ __global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(
         const MaxSum es = entry_maxsum(e);
         if (lane == 0) ent_ms[w] = es;
         __syncthreads();
-        const MaxSum ts = join_maxsum(ent_ms);
+        const MaxSum ts = join_maxsum<BS / 64>(ent_ms);
         const float L = lse[r], gr = g[r];
         // no valid entry: no loss to descend; weight 0: a row that does not count
         const bool some = ts.m != kNegInf && gr != 0.f;
@@ -186,7 +185,7 @@ __global__ __launch_bounds__(kDistThreads) void distill_grad_kernel(
         };
 #pragma unroll
         for (int i = 0; i < kGradRuns; ++i) {
-            const int64_t c = c0 + ((int64_t)i * kDistThreads + tid) * n;
+            const int64_t c = c0 + ((int64_t)i * BS + tid) * n;
             if (c >= c1) continue;
             const int m = c1 - c < n ? (int)(c1 - c) : n;
             Run<IO, n> v;
@@ -231,19 +230,19 @@ template <> __device__ __forceinline__ bf16 neg_inf_raw<bf16>() { return 0xff80;
 // The waves per SIMD that the launch bounds ask for keep the row's packed words
 // (4 NV registers) and little else live, so that several workgroups share a CU
 // and one loads while another computes.
-template <typename IO, int NV>
-__global__ __launch_bounds__(kDistThreads, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_step_kernel(
+template <typename IO, int NV, int BS>
+__global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_step_kernel(
     const uint32_t V, const int k, const IO *__restrict__ logits, const int64_t ld,
     const int32_t *__restrict__ t_ids, const float *__restrict__ t_logits, const float tau,
     const float inv_tau, const float *__restrict__ g, float *__restrict__ loss,
     float *__restrict__ lse, IO *__restrict__ dlogits, const int64_t ldd)
 {
     constexpr int n = kPer16<IO>;
-    constexpr uint32_t per = kDistThreads * n;
-    __shared__ MaxSum row_ms[kDistWaves], ent_ms[kDistWaves];
-    __shared__ float sum[kDistWaves];
-    __shared__ int ids[kDistThreads];
-    __shared__ float ps[kDistThreads];
+    constexpr uint32_t per = BS * n;
+    __shared__ MaxSum row_ms[BS / 64], ent_ms[BS / 64];
+    __shared__ float sum[BS / 64];
+    __shared__ int ids[BS];
+    __shared__ float ps[BS];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const float c2 = inv_tau * kLog2e;
     const int64_t r = blockIdx.x;
@@ -300,14 +299,14 @@ __global__ __launch_bounds__(kDistThreads, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void 
         ent_ms[w] = es;
     }
     __syncthreads();
-    const MaxSum ts = join_maxsum(ent_ms);
+    const MaxSum ts = join_maxsum<BS / 64>(ent_ms);
     float m = row_ms[0].m;
 #pragma unroll
-    for (int i = 1; i < kDistWaves; ++i) m = fmaxf(m, row_ms[i].m);
+    for (int i = 1; i < (BS / 64); ++i) m = fmaxf(m, row_ms[i].m);
     const float b = base_of(m);
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kDistWaves; ++i) s += row_ms[i].s * ex2(row_ms[i].m - b);
+    for (int i = 0; i < (BS / 64); ++i) s += row_ms[i].s * ex2(row_ms[i].m - b);
     // the entries: their probabilities and their terms of the loss
     const float log2_s = log2f(s), log_t = logf(ts.s);
     float p = 0.f, term = 0.f;
@@ -351,7 +350,7 @@ __global__ __launch_bounds__(kDistThreads, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void 
     __syncthreads();
     if (tid == 0) {
         float t = 0.f;
-        for (int i = 0; i < kDistWaves; ++i) t += sum[i];
+        for (int i = 0; i < (BS / 64); ++i) t += sum[i];
         loss[r] = tau * tau * t;
         lse[r] = m == kNegInf ? kNegInf : (m + log2_s) * kLn2;
     }
@@ -384,34 +383,52 @@ struct DistillArgs {
     int64_t ldd;
 };
 
-template <typename IO> static hipError_t launch_loss(const DistillArgs &a, hipStream_t st)
+// Short rows take workgroups of two waves: the rows, not the logits, are then what there are
+// many of (65536 x 1000 fp32, loss and gradient: 367 us with eight waves a row).
+constexpr int kSmallBS = 128, kLargeBS = 512;
+template <typename IO> static bool short_rows(const DistillArgs &a)
 {
-    const unsigned grid = (unsigned)(a.R < (1 << 20) ? a.R : 1 << 20);
-    hipLaunchKernelGGL(distill_loss_kernel<IO>, dim3(grid), dim3(kDistThreads), 0, st, a.R, a.V,
-                       a.k, (const IO *)a.logits, a.ld, a.t_ids, a.t_logits, a.tau, 1.f / a.tau,
-                       a.loss, a.lse);
-    return hipGetLastError();
+    return a.V <= (int64_t)kSmallBS * kPer16<IO> * 4 && a.k <= kSmallBS;
 }
 
-template <typename IO> static hipError_t launch_grad(const DistillArgs &a, hipStream_t st)
+template <typename IO, int BS> static hipError_t launch_loss_t(const DistillArgs &a, hipStream_t st)
 {
-    constexpr int64_t chunk = (int64_t)kDistThreads * kPer16<IO> * kGradRuns;
+    const unsigned grid = (unsigned)(a.R < (1 << 22) ? a.R : 1 << 22);
+    hipLaunchKernelGGL((distill_loss_kernel<IO, BS>), dim3(grid), dim3(BS), 0, st, a.R, a.V, a.k,
+                       (const IO *)a.logits, a.ld, a.t_ids, a.t_logits, a.tau, 1.f / a.tau, a.loss,
+                       a.lse);
+    return hipGetLastError();
+}
+template <typename IO> static hipError_t launch_loss(const DistillArgs &a, hipStream_t st)
+{
+    return short_rows<IO>(a) ? launch_loss_t<IO, kSmallBS>(a, st)
+                             : launch_loss_t<IO, kLargeBS>(a, st);
+}
+
+template <typename IO, int BS> static hipError_t launch_grad_t(const DistillArgs &a, hipStream_t st)
+{
+    constexpr int64_t chunk = (int64_t)BS * kPer16<IO> * kGradRuns;
     const int64_t n_chunks = (a.V + chunk - 1) / chunk, units = a.R * n_chunks;
     const unsigned grid = (unsigned)(units < (1 << 22) ? units : 1 << 22);
-    hipLaunchKernelGGL(distill_grad_kernel<IO>, dim3(grid), dim3(kDistThreads), 0, st, a.R, a.V,
-                       a.k, n_chunks, (const IO *)a.logits, a.ld, a.t_ids, a.t_logits, a.tau,
+    hipLaunchKernelGGL((distill_grad_kernel<IO, BS>), dim3(grid), dim3(BS), 0, st, a.R, a.V, a.k,
+                       n_chunks, (const IO *)a.logits, a.ld, a.t_ids, a.t_logits, a.tau,
                        1.f / a.tau, a.lse, a.g, (IO *)a.dlogits, a.ldd);
     return hipGetLastError();
 }
+template <typename IO> static hipError_t launch_grad(const DistillArgs &a, hipStream_t st)
+{
+    return short_rows<IO>(a) ? launch_grad_t<IO, kSmallBS>(a, st)
+                             : launch_grad_t<IO, kLargeBS>(a, st);
+}
 
-template <typename IO, int NV>
+template <typename IO, int NV, int BS>
 static hipError_t launch_step_t(const DistillArgs &a, hipStream_t st)
 {
     constexpr int64_t most = 1 << 22;  // rows of a launch
     for (int64_t r = 0; r < a.R; r += most) {
         const int64_t rows = a.R - r < most ? a.R - r : most;
-        hipLaunchKernelGGL((distill_step_kernel<IO, NV>), dim3((unsigned)rows), dim3(kDistThreads),
-                           0, st, (uint32_t)a.V, a.k, (const IO *)a.logits + r * a.ld, a.ld,
+        hipLaunchKernelGGL((distill_step_kernel<IO, NV, BS>), dim3((unsigned)rows), dim3(BS), 0, st,
+                           (uint32_t)a.V, a.k, (const IO *)a.logits + r * a.ld, a.ld,
                            a.t_ids + r * a.k, a.t_logits + r * a.k, a.tau, 1.f / a.tau, a.g + r,
                            a.loss + r, a.lse + r, (IO *)a.dlogits + r * a.ldd, a.ldd);
     }
@@ -420,16 +437,20 @@ static hipError_t launch_step_t(const DistillArgs &a, hipStream_t st)
 
 template <typename IO> static hipError_t launch_step(const DistillArgs &a, hipStream_t st)
 {
-    constexpr int64_t per = (int64_t)kDistThreads * kPer16<IO>;  // logits of one access each
-    if (a.V < kPer16<IO>) {  // (shorter than an access)
+    constexpr int n = kPer16<IO>;
+    if (a.V < n) {  // (shorter than an access)
         const hipError_t e = launch_loss<IO>(a, st);
         return e == hipSuccess ? launch_grad<IO>(a, st) : e;
     }
-    if (a.V <= 2 * per) return launch_step_t<IO, 2>(a, st);
-    if (a.V <= 4 * per) return launch_step_t<IO, 4>(a, st);
-    if (a.V <= 8 * per) return launch_step_t<IO, 8>(a, st);
-    if (a.V <= 16 * per) return launch_step_t<IO, 16>(a, st);
-    if (a.V <= 32 * per) return launch_step_t<IO, 32>(a, st);
+    if (short_rows<IO>(a))
+        return a.V <= kSmallBS * n ? launch_step_t<IO, 1, kSmallBS>(a, st)
+                                   : launch_step_t<IO, 4, kSmallBS>(a, st);
+    constexpr int64_t per = kLargeBS * n;  // logits of one access each
+    if (a.V <= 2 * per) return launch_step_t<IO, 2, kLargeBS>(a, st);
+    if (a.V <= 4 * per) return launch_step_t<IO, 4, kLargeBS>(a, st);
+    if (a.V <= 8 * per) return launch_step_t<IO, 8, kLargeBS>(a, st);
+    if (a.V <= 16 * per) return launch_step_t<IO, 16, kLargeBS>(a, st);
+    if (a.V <= 32 * per) return launch_step_t<IO, 32, kLargeBS>(a, st);
     // the row does not fit the registers: it is read again for the gradient
     const hipError_t e = launch_loss<IO>(a, st);
     return e == hipSuccess ? launch_grad<IO>(a, st) : e;
@@ -445,9 +466,9 @@ static naju_status_t check_distill(int64_t R, int64_t V, int64_t k, int32_t io, 
         return fail(NAJU_EINVAL, "io dtype %d is neither NAJU_F32 nor NAJU_BF16", (int)io);
     if (R > ((int64_t)1 << 30) || V > ((int64_t)1 << 30))
         return fail(NAJU_EINVAL, "rows or vocab too large (2^30 max)");
-    if (k > kDistThreads)
+    if (k > kMostEntries)
         return fail(NAJU_EUNSUPPORTED, "k %lld teacher entries a row (%d max)", (long long)k,
-                    kDistThreads);
+                    kMostEntries);
     if (!(tau > 0.f) || !(tau < __builtin_huge_valf()))
         return fail(NAJU_EINVAL, "temperature must be positive and finite");
     if (R == 0 || V == 0) return NAJU_OK;
