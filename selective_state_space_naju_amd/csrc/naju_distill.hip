@@ -145,73 +145,110 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
 }
 
 // -------------------------------------------------------------- gradient
-// A workgroup takes kGradRuns accesses per thread of one row.  The dense part
-// g tau q_v is stored first; then the elements that the entries name are
-// written again with their share of p, by the first entry that names each.
-constexpr int kGradRuns = 4;
+// A workgroup takes NV accesses per thread of one row, all loads issued before
+// the first is used.  The dense part g tau q_v is stored first; then the
+// elements that the entries name are written again with their share of p, by
+// the first entry that names each.  The accesses are laid out from a 16-byte
+// boundary of the gradient's row at or before its start (rows of an odd
+// vocabulary start anywhere).
 
-template <typename IO, int BS>
-__global__ __launch_bounds__(BS) void distill_grad_kernel(
-    const int64_t R, const int64_t V, const int k, const int64_t n_chunks,
-    const IO *__restrict__ logits, const int64_t ld, const int32_t *__restrict__ t_ids,
-    const float *__restrict__ t_logits, const float tau, const float inv_tau,
-    const float *__restrict__ lse, const float *__restrict__ g, IO *__restrict__ dlogits,
-    const int64_t ldd)
+// elements between p and the 16-byte boundary before it
+template <typename IO> __device__ __forceinline__ int past_boundary(const IO *p)
+{
+    return (int)((uintptr_t)p % 16 / sizeof(IO));
+}
+
+template <typename IO, int NV, int BS>
+__global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
+    const int64_t V, const int k, const int n_chunks, const IO *__restrict__ logits,
+    const int64_t ld, const int32_t *__restrict__ t_ids, const float *__restrict__ t_logits,
+    const float tau, const float inv_tau, const float *__restrict__ lse,
+    const float *__restrict__ g, IO *__restrict__ dlogits, const int64_t ldd)
 {
     constexpr int n = kPer16<IO>;
-    constexpr int64_t chunk = (int64_t)BS * n * kGradRuns;
+    constexpr int chunk = BS * n * NV;
     __shared__ MaxSum ent_ms[BS / 64];
     __shared__ int ids[BS];
     __shared__ float ps[BS];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    for (int64_t u = blockIdx.x; u < R * n_chunks; u += gridDim.x) {
-        const int64_t r = u / n_chunks, c0 = (u - r * n_chunks) * chunk;
-        const int64_t c1 = c0 + chunk < V ? c0 + chunk : V;
-        const IO *row = logits + r * ld;
-        IO *out = dlogits + r * ldd;
-        const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
-        const MaxSum es = entry_maxsum(e);
-        if (lane == 0) ent_ms[w] = es;
-        __syncthreads();
-        const MaxSum ts = join_maxsum<BS / 64>(ent_ms);
-        const float L = lse[r], gr = g[r];
-        // no valid entry: no loss to descend; weight 0: a row that does not count
-        const bool some = ts.m != kNegInf && gr != 0.f;
-        const float f = some ? gr * tau : 0.f;
-        ids[tid] = e.id;
-        ps[tid] = e.id >= 0 ? exp_nat(e.t - base_of(ts.m)) / ts.s : 0.f;
-        auto q_of = [&](float s) {
-            return L == kNegInf ? 0.f : exp_nat(fmaf(s, inv_tau, -L));
-        };
+    const int64_t r = blockIdx.x / (unsigned)n_chunks;
+    const int part = (int)(blockIdx.x - (unsigned)r * (unsigned)n_chunks);
+    const IO *row = logits + r * ld;
+    IO *out = dlogits + r * ldd;
+    // this chunk: elements [c0, c0 + chunk) of the row, c0 on a boundary; the last chunk also
+    // takes the few that the shift pushes past it
+    const int64_t c0 = (int64_t)part * chunk - past_boundary(out);
+    const bool is_last = part == n_chunks - 1;
+    const int64_t lo = c0 > 0 ? c0 : 0, hi = is_last ? V : c0 + chunk;
+    const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
+    const float L = lse[r], gr = g[r];
+    Run<IO, n> v[NV];
+    if (V >= n) {
+        const IO *at_c0 = row + c0;  // (the accesses are moved into the row)
+        const int least = c0 < 0 ? (int)-c0 : 0;
+        const int most = V - n - c0 < chunk ? (int)(V - n - c0) : chunk;
 #pragma unroll
-        for (int i = 0; i < kGradRuns; ++i) {
-            const int64_t c = c0 + ((int64_t)i * BS + tid) * n;
-            if (c >= c1) continue;
-            const int m = c1 - c < n ? (int)(c1 - c) : n;
-            Run<IO, n> v;
-            if (m == n) v.load(row + c);
-            else v.load_part(row + c, m);
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * BS + tid) * n;
+            const int in = c < least ? least : c > most ? most : c;
+            v[i].load(at_c0 + in);
+        }
+    }
+    const bool mine = e.id >= lo && e.id < hi;
+    const float at = mine ? to_f(row[e.id]) : 0.f;
+    const MaxSum es = entry_maxsum(e);
+    if (lane == 0) ent_ms[w] = es;
+    __syncthreads();
+    const MaxSum ts = join_maxsum<BS / 64>(ent_ms);
+    // no valid entry: no loss to descend; weight 0: a row that does not count
+    const bool some = ts.m != kNegInf && gr != 0.f;
+    const float f = some ? gr * tau : 0.f;
+    ids[tid] = e.id;
+    ps[tid] = e.id >= 0 ? exp_nat(e.t - base_of(ts.m)) / ts.s : 0.f;
+    const float fq = L == kNegInf ? 0.f : f, base = L == kNegInf ? 0.f : L;
+    auto dense = [&](float s) { return fq * exp_nat(fmaf(s, inv_tau, -base)); };
+    if (V >= n) {
+        IO *out_c0 = out + c0;
+        const int64_t left = V - c0;  // elements from c0 to the row's end
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = (i * BS + tid) * n;
             float d[n];
 #pragma unroll
-            for (int j = 0; j < n; ++j) d[j] = some ? f * q_of(v.get(j)) : 0.f;
-            const Run<IO, n> o = round_run<IO, n>(d);
-            if (m == n) o.store(out + c);
-            else o.store_part(out + c, m);
+            for (int j = 0; j < n; ++j) d[j] = dense(v[i].get(j));
+            Run<IO, n> o = round_run<IO, n>(d);
+            if (!some) o.zero();
+            if (c0 + c >= 0 && c + n <= left) {
+                o.store(out_c0 + c);
+            } else if (c0 + c > -n && c < left) {
+                // the row's first or last access, moved inside it: its own elements
+                const int in = c0 + c < 0 ? (int)-c0 : (int)(left - n);
+#pragma unroll
+                for (int j = 0; j < n; ++j)
+                    if (in + j >= c && in + j < c + n) out_c0[in + j] = o.get_raw(j);
+            }
         }
-        // the dense stores are done before an element is written again
-        wait_mem();
-        __syncthreads();
-        if (some && e.id >= c0 && e.id < c1) {
-            float p = 0.f;
-            bool first = true;
-            for (int j = 0; j < k; ++j)
-                if (ids[j] == e.id) {
-                    first = first && j >= tid;
-                    p += ps[j];
-                }
-            if (first) out[e.id] = from_f<IO>(f * (q_of(to_f(row[e.id])) - p));
+        const int64_t rest = c0 + chunk + tid;
+        if (is_last && tid < n && rest < V) {
+            const float d = dense(to_f(row[rest]));
+            out[rest] = from_f<IO>(some ? d : 0.f);
         }
-        __syncthreads();
+    } else if (tid < V) {  // (shorter than an access)
+        const float d = dense(to_f(row[tid]));
+        out[tid] = from_f<IO>(some ? d : 0.f);
+    }
+    // the dense stores are done before an element is written again
+    wait_mem();
+    __syncthreads();
+    if (some && mine) {
+        float p = 0.f;
+        bool first = true;
+        for (int j = 0; j < k; ++j)
+            if (ids[j] == e.id) {
+                first = first && j >= tid;
+                p += ps[j];
+            }
+        if (first) out[e.id] = from_f<IO>(dense(at) - f * p);
     }
 }
 
@@ -405,20 +442,29 @@ template <typename IO> static hipError_t launch_loss(const DistillArgs &a, hipSt
                              : launch_loss_t<IO, kLargeBS>(a, st);
 }
 
-template <typename IO, int BS> static hipError_t launch_grad_t(const DistillArgs &a, hipStream_t st)
+template <typename IO, int NV, int BS>
+static hipError_t launch_grad_t(const DistillArgs &a, hipStream_t st)
 {
-    constexpr int64_t chunk = (int64_t)BS * kPer16<IO> * kGradRuns;
-    const int64_t n_chunks = (a.V + chunk - 1) / chunk, units = a.R * n_chunks;
-    const unsigned grid = (unsigned)(units < (1 << 22) ? units : 1 << 22);
-    hipLaunchKernelGGL((distill_grad_kernel<IO, BS>), dim3(grid), dim3(BS), 0, st, a.R, a.V, a.k,
-                       n_chunks, (const IO *)a.logits, a.ld, a.t_ids, a.t_logits, a.tau,
-                       1.f / a.tau, a.lse, a.g, (IO *)a.dlogits, a.ldd);
+    constexpr int64_t chunk = (int64_t)BS * kPer16<IO> * NV;
+    const int64_t n_chunks = (a.V + chunk - 1) / chunk;
+    const int64_t most = ((int64_t)1 << 22) / n_chunks + 1;  // rows of a launch
+    for (int64_t r = 0; r < a.R; r += most) {
+        const int64_t rows = a.R - r < most ? a.R - r : most;
+        hipLaunchKernelGGL((distill_grad_kernel<IO, NV, BS>), dim3((unsigned)(rows * n_chunks)),
+                           dim3(BS), 0, st, a.V, a.k, (int)n_chunks,
+                           (const IO *)a.logits + r * a.ld, a.ld, a.t_ids + r * a.k,
+                           a.t_logits + r * a.k, a.tau, 1.f / a.tau, a.lse + r, a.g + r,
+                           (IO *)a.dlogits + r * a.ldd, a.ldd);
+    }
     return hipGetLastError();
 }
 template <typename IO> static hipError_t launch_grad(const DistillArgs &a, hipStream_t st)
 {
-    return short_rows<IO>(a) ? launch_grad_t<IO, kSmallBS>(a, st)
-                             : launch_grad_t<IO, kLargeBS>(a, st);
+    if (short_rows<IO>(a)) return launch_grad_t<IO, 4, kSmallBS>(a, st);
+    // eight accesses a thread amortise the entries' part of a workgroup; few rows are cut finer
+    constexpr int64_t per = kLargeBS * kPer16<IO>;
+    return a.R * ((a.V + 8 * per - 1) / (8 * per)) >= 512 ? launch_grad_t<IO, 8, kLargeBS>(a, st)
+                                                          : launch_grad_t<IO, 2, kLargeBS>(a, st);
 }
 
 template <typename IO, int NV, int BS>
