@@ -287,31 +287,35 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
     IO *out = dlogits + r * ldd;
     const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
     const float gr = g[r];
-    // an access past the row's end is moved back to end there: no load waits on a branch
-    const uint32_t last = V - n;
+    // accesses from the 16-byte boundary `before` elements ahead of the gradient's row, moved
+    // into the row at its ends: no load waits on a branch
+    const int before = past_boundary(out), last = (int)V - n;
+    const int c0 = tid * n - before;
     Run<IO, n> v[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const uint32_t c = i * per + tid * n;
-        v[i].load_at(row, (c < last ? c : last) * (uint32_t)sizeof(IO));
+        const int c = i * (int)per + c0;
+        const int in = c < 0 ? 0 : c < last ? c : last;
+        v[i].load_at(row, (uint32_t)in * (uint32_t)sizeof(IO));
     }
     const float at = e.id >= 0 ? to_f(row[e.id]) : 0.f;
     const MaxSum es = entry_maxsum(e);
-    // what an access moved back holds of its neighbours is taken for -inf
+    // what a moved access holds of its neighbours is taken for -inf
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if ((i + 1) * per > V) {  // (uniform)
-            const int twice = (int)(i * per + tid * n - last);
+        if ((i == 0 && before > 0) || (i + 1) * per > V + before) {  // (uniform)
+            const int c = i * (int)per + c0;
+            const int in = c < 0 ? 0 : c < last ? c : last;
 #pragma unroll
             for (int j = 0; j < n; ++j)
-                if (twice > j) v[i].set_raw(j, neg_inf_raw<IO>());
+                if (in + j < c || in + j >= c + n) v[i].set_raw(j, neg_inf_raw<IO>());
         }
     }
     // the row, in base 2: maximum of the wave, sum of exp2(x - maximum)
     float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (i * per < V) {
+        if (i * per < V + before) {
 #pragma unroll
             for (int j = 0; j < n; ++j) top = fmaxf(top, v[i].get(j));
         }
@@ -322,7 +326,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (i * per < V) {
+        if (i * per < V + before) {
             v[i].repack();
 #pragma unroll
             for (int j = 0; j < n; ++j) s += ex2(fmaf(v[i].get(j), c2, -m_wave));
@@ -362,23 +366,24 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
     const bool some = ts.m != kNegInf && gr != 0.f;
     const float f = some ? gr * tau : 0.f;
     const float fq = m == kNegInf ? 0.f : f / s;
-    uint32_t c0 = tid * n;
-    asm volatile("" : "+v"(c0));  // (offsets formed anew, not kept since the loads)
+    int c1 = c0;
+    asm volatile("" : "+v"(c1));  // (offsets formed anew, not kept since the loads)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        if (i * per < V) {
-            const uint32_t c = i * per + c0;
+        if (i * per < V + before) {
+            const int c = i * (int)per + c1;
             float d[n];
 #pragma unroll
             for (int j = 0; j < n; ++j) d[j] = fq * ex2(fmaf(v[i].get(j), c2, -b));
             Run<IO, n> o = round_run<IO, n>(d);
             if (!some) o.zero();
-            if (c <= last) {
-                o.store_at(out, c * (uint32_t)sizeof(IO));
-            } else if (c < V) {
+            if (c >= 0 && c <= last) {
+                o.store_at(out, (uint32_t)c * (uint32_t)sizeof(IO));
+            } else if (c > -n && c < (int)V) {
+                const int in = c < 0 ? 0 : last;
 #pragma unroll
-                for (int j = 1; j < n; ++j)
-                    if (j >= (int)(c - last)) out[last + j] = o.get_raw(j);
+                for (int j = 0; j < n; ++j)
+                    if (in + j >= c && in + j < c + n) out[in + j] = o.get_raw(j);
             }
         }
     }
@@ -488,15 +493,18 @@ template <typename IO> static hipError_t launch_step(const DistillArgs &a, hipSt
         const hipError_t e = launch_loss<IO>(a, st);
         return e == hipSuccess ? launch_grad<IO>(a, st) : e;
     }
-    if (short_rows<IO>(a))
-        return a.V <= kSmallBS * n ? launch_step_t<IO, 1, kSmallBS>(a, st)
+    // logits and what may lie between them and a 16-byte boundary of the gradient's row
+    const bool aligned = (uintptr_t)a.dlogits % 16 == 0 && a.ldd % n == 0;
+    const int64_t span = a.V + (aligned ? 0 : n - 1);
+    if (span <= kSmallBS * n * 4 && a.k <= kSmallBS)
+        return span <= kSmallBS * n ? launch_step_t<IO, 1, kSmallBS>(a, st)
                                    : launch_step_t<IO, 4, kSmallBS>(a, st);
     constexpr int64_t per = kLargeBS * n;  // logits of one access each
-    if (a.V <= 2 * per) return launch_step_t<IO, 2, kLargeBS>(a, st);
-    if (a.V <= 4 * per) return launch_step_t<IO, 4, kLargeBS>(a, st);
-    if (a.V <= 8 * per) return launch_step_t<IO, 8, kLargeBS>(a, st);
-    if (a.V <= 16 * per) return launch_step_t<IO, 16, kLargeBS>(a, st);
-    if (a.V <= 32 * per) return launch_step_t<IO, 32, kLargeBS>(a, st);
+    if (span <= 2 * per) return launch_step_t<IO, 2, kLargeBS>(a, st);
+    if (span <= 4 * per) return launch_step_t<IO, 4, kLargeBS>(a, st);
+    if (span <= 8 * per) return launch_step_t<IO, 8, kLargeBS>(a, st);
+    if (span <= 16 * per) return launch_step_t<IO, 16, kLargeBS>(a, st);
+    if (span <= 32 * per) return launch_step_t<IO, 32, kLargeBS>(a, st);
     // the row does not fit the registers: it is read again for the gradient
     const hipError_t e = launch_loss<IO>(a, st);
     return e == hipSuccess ? launch_grad<IO>(a, st) : e;
