@@ -81,8 +81,23 @@ __device__ __forceinline__ MaxSum entry_maxsum(const Entry &e)
     return wave_maxsum({e.t, e.id >= 0 ? exp_nat(e.t - base_of(e.t)) : 0.f});
 }
 
+// elements between p and the 16-byte boundary before it
+template <typename IO> __device__ __forceinline__ int past_boundary(const IO *p)
+{
+    return (int)((uintptr_t)p % 16 / sizeof(IO));
+}
+
+template <typename IO> __device__ __forceinline__ IO neg_inf_raw();
+template <> __device__ __forceinline__ float neg_inf_raw<float>() { return kNegInf; }
+template <> __device__ __forceinline__ bf16 neg_inf_raw<bf16>() { return 0xff80; }
+
 // ------------------------------------------------------------------ loss
-// Reads the row once with a running maximum and sum per thread.
+// Reads the row once, kLossRuns accesses per thread in flight, with a running
+// maximum and sum per thread in base 2.  Accesses start at a 16-byte boundary;
+// one that would leave the row is moved inside it, and what it holds of its
+// neighbours is taken for -inf.
+constexpr int kLossRuns = 4;
+
 template <typename IO, int BS>
 __global__ __launch_bounds__(BS) void distill_loss_kernel(
     const int64_t R, const int64_t V, const int k, const IO *__restrict__ logits,
@@ -90,45 +105,87 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
     const float tau, const float inv_tau, float *__restrict__ loss, float *__restrict__ lse)
 {
     constexpr int n = kPer16<IO>;
+    constexpr int per = BS * n * kLossRuns;
     __shared__ MaxSum row_ms[BS / 64], ent_ms[BS / 64];
     __shared__ float sum[BS / 64];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const float c2 = inv_tau * kLog2e;
     for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
         const IO *row = logits + r * ld;
         const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
         const float at = e.id >= 0 ? to_f(row[e.id]) : 0.f;
-        MaxSum a{kNegInf, 0.f};
-        for (int64_t c = (int64_t)tid * n; c < V; c += BS * n) {
-            Run<IO, n> v;
-            const int m = V - c < n ? (int)(V - c) : n;
-            if (m == n) v.load(row + c);
-            else v.load_part(row + c, m);
-            float top = a.m;
+        float m = kNegInf, s = 0.f;  // of x in base 2
+        if (V >= n) {
+            for (int64_t c0 = -past_boundary(row); c0 < V; c0 += per) {
+                Run<IO, n> v[kLossRuns];
 #pragma unroll
-            for (int i = 0; i < n; ++i)
-                if (i < m) top = fmaxf(top, v.get(i) * inv_tau);
-            const float b = base_of(top);
-            float s = a.s * exp_nat(a.m - b);
+                for (int i = 0; i < kLossRuns; ++i) {
+                    const int64_t c = c0 + (i * BS + tid) * n;
+                    v[i].load(row + (c < 0 ? 0 : c > V - n ? V - n : c));
+                }
 #pragma unroll
-            for (int i = 0; i < n; ++i)
-                if (i < m) s += exp_nat(fmaf(v.get(i), inv_tau, -b));
-            a = {top, s};
+                for (int i = 0; i < kLossRuns; ++i) {
+                    if ((i == 0 && c0 < 0) || c0 + (i + 1) * (BS * n) > V) {  // (uniform)
+                        const int64_t c = c0 + (i * BS + tid) * n;
+                        const int64_t in = c < 0 ? 0 : c > V - n ? V - n : c;
+#pragma unroll
+                        for (int j = 0; j < n; ++j)
+                            if (in + j < c || in + j >= c + n) v[i].set_raw(j, neg_inf_raw<IO>());
+                    }
+                }
+                float top = kNegInf;
+#pragma unroll
+                for (int i = 0; i < kLossRuns; ++i) {
+                    if (c0 + i * (BS * n) < V) {
+#pragma unroll
+                        for (int j = 0; j < n; ++j) top = fmaxf(top, v[i].get(j));
+                    }
+                }
+                top = fmaxf(m, top * c2);
+                const float b = base_of(top);
+                s *= ex2(m - b);
+                m = top;
+#pragma unroll
+                for (int i = 0; i < kLossRuns; ++i) {
+                    if (c0 + i * (BS * n) < V) {
+                        v[i].repack();
+#pragma unroll
+                        for (int j = 0; j < n; ++j) s += ex2(fmaf(v[i].get(j), c2, -b));
+                    }
+                }
+            }
+        } else if (tid < V) {  // (shorter than an access)
+            m = to_f(row[tid]) * c2;
+            s = m == kNegInf ? 0.f : fabsf(m) < -kNegInf ? 1.f : __builtin_nanf("");
         }
-        const MaxSum ws = wave_maxsum(a), es = entry_maxsum(e);
+        // over the wave, then over the workgroup
+        float top = m;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+        s *= ex2(m - base_of(top));
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+        const MaxSum es = entry_maxsum(e);
         if (lane == 0) {
-            row_ms[w] = ws;
+            row_ms[w] = {top, s};
             ent_ms[w] = es;
         }
         __syncthreads();
-        const MaxSum rs = join_maxsum<BS / 64>(row_ms), ts = join_maxsum<BS / 64>(ent_ms);
-        const float log_s = logf(rs.s);
+        const MaxSum ts = join_maxsum<BS / 64>(ent_ms);
+        m = row_ms[0].m;
+#pragma unroll
+        for (int i = 1; i < BS / 64; ++i) m = fmaxf(m, row_ms[i].m);
+        const float b = base_of(m);
+        s = 0.f;
+#pragma unroll
+        for (int i = 0; i < BS / 64; ++i) s += row_ms[i].s * ex2(row_ms[i].m - b);
+        const float log2_s = log2f(s);
         float term = 0.f;
         if (e.id >= 0) {
             const float gap = e.t - base_of(ts.m);
             const float p = exp_nat(gap) / ts.s;
-            const float logp = gap - logf(ts.s);
-            const float logq = at == kNegInf ? kNegInf : fmaf(at, inv_tau, -base_of(rs.m)) - log_s;
-            if (!(p == 0.f)) term = p * (logp - logq);  // 0 log 0 = 0; NaN goes on
+            const float logq = at == kNegInf ? kNegInf : (fmaf(at, c2, -b) - log2_s) * kLn2;
+            if (!(p == 0.f)) term = p * ((gap - logf(ts.s)) - logq);  // 0 log 0 = 0; NaN goes on
         }
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) term += __shfl_xor(term, o);
@@ -136,9 +193,9 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
         __syncthreads();
         if (tid == 0) {
             float t = 0.f;
-            for (int i = 0; i < (BS / 64); ++i) t += sum[i];
+            for (int i = 0; i < BS / 64; ++i) t += sum[i];
             loss[r] = tau * tau * t;
-            lse[r] = rs.m + log_s;
+            lse[r] = m == kNegInf ? kNegInf : (m + log2_s) * kLn2;
         }
         // (the next row writes row_ms and ent_ms: every thread has read them by now)
     }
@@ -151,12 +208,6 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
 // the first entry that names each.  The accesses are laid out from a 16-byte
 // boundary of the gradient's row at or before its start (rows of an odd
 // vocabulary start anywhere).
-
-// elements between p and the 16-byte boundary before it
-template <typename IO> __device__ __forceinline__ int past_boundary(const IO *p)
-{
-    return (int)((uintptr_t)p % 16 / sizeof(IO));
-}
 
 template <typename IO, int NV, int BS>
 __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
@@ -259,9 +310,6 @@ __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
 // barrier joins the row's and the list's statistics; q is exp2(x - m) over the
 // row's sum, with no rounded lse in between.  Places past the row hold -inf,
 // which adds nothing.
-template <typename IO> __device__ __forceinline__ IO neg_inf_raw();
-template <> __device__ __forceinline__ float neg_inf_raw<float>() { return kNegInf; }
-template <> __device__ __forceinline__ bf16 neg_inf_raw<bf16>() { return 0xff80; }
 
 //
 // The waves per SIMD that the launch bounds ask for keep the row's packed words
