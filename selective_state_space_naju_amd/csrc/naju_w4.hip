@@ -45,20 +45,6 @@ struct W4Args {
     bf16 *y;                   // [R][N]
 };
 
-// 16 bytes of a weight row from byte `off`, zeros past its `bytes`
-__device__ __forceinline__ u32x4 load_codes(const uint8_t *row, int64_t off, int64_t bytes)
-{
-    u32x4 d = {0, 0, 0, 0};
-    if (off + 16 <= bytes) {
-        __builtin_memcpy(&d, row + off, 16);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (off + j < bytes) d[j / 4] |= (uint32_t)row[off + j] << (8 * (j % 4));
-    }
-    return d;
-}
-
 // 4 x 4 transpose of dwords between the wave's quarters: afterwards dword j of
 // quarter h is what dword h of quarter j was.
 __device__ __forceinline__ u32x4 transpose_quarters(u32x4 d)
@@ -79,117 +65,194 @@ __device__ __forceinline__ bf16x8 unpack(uint32_t d)
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// RT: tiles of 16 rows of x; G: inputs of a group; WK: waves that share an
-// output tile and split the inputs between them (the other kW4Waves / WK take
-// neighbouring tiles).
-template <int RT, int G, int WK>
-__global__ __launch_bounds__(kW4Threads) void w4_kernel(const W4Args g)
+// One workgroup: WN = kW4Waves / WK tiles of 16 outputs; the WK waves of a tile
+// take every WK-th block of 128 inputs.  RT: tiles of 16 rows of x; G: inputs of
+// a group; D: blocks whose codes a wave holds or has in flight; Z: zeros are
+// given.
+//
+// x and the outputs' scales and zeros are staged in LDS, `stage` inputs at a time
+// (a multiple of 128 WK D): all of them where they fit, so that nothing but the
+// codes is waited for.  Rows past the last one are not staged: lanes that stand
+// for them compute what nobody stores.
+//
+// Four neighbouring lanes load the 64 bytes of one weight row, and the block
+// passes through 1 KB of LDS of its wave into the product's layout (a lane for
+// each output and quarter).  Loaded in that layout directly, every lane of a
+// quarter wave touches a line of its own, and address processing bounds the
+// kernel (one row of x, 4096 -> 131072: 76 us, the address units 80 % busy).
+//
+// The loads of whole blocks are unconditional (past the last one they repeat
+// it): a load that is issued under a condition makes the compiler wait for the
+// ones in flight where the branches meet.
+template <int RT, int G, int WK, int D, bool Z>
+__global__ __launch_bounds__(kW4Threads) void w4_kernel(const W4Args g, const int stage)
 {
     constexpr int WN = kW4Waves / WK;
-    constexpr int NB = WK >= 4 ? 1 : 4;           // blocks of 128 inputs per wave and stage
-    constexpr int SC = NB * WK * 128;             // inputs of a stage
-    constexpr int kRow = SC + 32;                 // staged row, padded to spread the banks
-    constexpr int NG = 128 / G;                   // groups of a block
-    constexpr int kRed = WK > 1 ? kW4Waves * RT * 256 : 0;  // floats of the final sums
-    constexpr int kStage = RT * 16 * kRow / 2;    // 32-bit words of the staged x
-    __shared__ __attribute__((aligned(16))) uint32_t lds[kStage > kRed ? kStage : kRed];
-    __shared__ __attribute__((aligned(16))) float sx[SC / 32][RT * 16];
-    bf16 *xs = (bf16 *)lds;
+    constexpr int NG = 128 / G;  // groups of a block
+    constexpr int NR = WN * 16;  // outputs of the workgroup
+    extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = w % WK, wn = w / WK, col = lane & 15, quarter = lane >> 4;
-    const int64_t n = ((int64_t)blockIdx.x * WN + wn) * 16 + col;
-    const int64_t nc = n < g.N ? n : g.N - 1;     // (lanes past the last output repeat it)
+    const int64_t n0 = (int64_t)blockIdx.x * NR;  // first output
+    const int64_t n = n0 + wn * 16 + col;
     const int64_t r0 = (int64_t)blockIdx.y * (RT * 16);
-    const int64_t row_bytes = g.K / 2;
-    const uint8_t *qrow = g.q + nc * row_bytes;
-    const bf16 *srow = g.scales + nc * g.ng;
-    const uint8_t *zrow = g.zeros ? g.zeros + nc * g.ng : nullptr;
+    const int rows = g.R - r0 < RT * 16 ? (int)(g.R - r0) : RT * 16;
+    const int outs = g.N - n0 < NR ? (int)(g.N - n0) : NR;
+    const int pitch = stage + 8;               // of a staged row: the pad spreads the banks
+    const int groups = stage / G;              // of a stage
+    uint32_t *slot = lds + w * 256;            // this wave's block of codes
+    bf16 *xs = (bf16 *)(lds + kW4Waves * 256);            // [rows][pitch]
+    float *sx = (float *)(xs + rows * pitch);             // [groups][RT * 16]: sums of x
+    bf16 *sl = (bf16 *)(sx + groups * (RT * 16));         // [groups][NR]: scales
+    uint8_t *zl = (uint8_t *)(sl + groups * NR);          // [groups][NR]: zeros
 
     f32x4 acc[RT];
 #pragma unroll
     for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int xrow[RT];  // where this lane's row of a tile is staged
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+        xrow[t] = (t * 16 + col < rows ? t * 16 + col : rows - 1) * pitch + quarter * 8;
 
-    u32x4 d[NB];
-    float s[NB][NG], z[NB][NG];
-    auto fetch = [&](int64_t k0) {
+    // codes: lane l loads 16 bytes of row l / 4 of the tile (past the last output: of that one)
+    const int lrow = wn * 16 + (lane >> 2) < outs ? wn * 16 + (lane >> 2) : outs - 1;
+    const uint32_t loff = (uint32_t)lrow * (uint32_t)(g.K / 2) + (lane & 3) * 16;
+    const uint8_t *qtile = g.q + n0 * (g.K / 2);
+    const int64_t whole = g.K / 128 * 128;  // inputs in whole blocks
+    u32x4 d[D];
+    auto fetch = [&](int u, int64_t k) {
+        k = k < whole ? k : whole - 128;
+        __builtin_memcpy(&d[u], qtile + k / 2 + loff, 16);
+    };
+    // a loaded block in the product's layout; within the slot a row's four parts are rotated by
+    // a quarter of its number, which spreads the banks of the read
+    const int put = (lane >> 2) * 4 + (((lane & 3) + (lane >> 4)) & 3);
+    const int get = col * 4 + ((quarter + (col >> 2)) & 3);
+    auto arrange = [&](const u32x4 v) {
+        ((u32x4 *)slot)[put] = v;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const u32x4 r = ((const u32x4 *)slot)[get];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        return transpose_quarters(r);
+    };
+    // the products of a block of 128 inputs, c0 inputs into the stage
+    auto block = [&](const u32x4 t4, int c0) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const int64_t k = k0 + (b * WK + wk) * 128;
-            d[b] = load_codes(qrow, k / 2 + quarter * 16, row_bytes);
+        for (int i = 0; i < NG; ++i) {
+            f32x4 p[RT];
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                const int64_t gi = k / G + i;
-                s[b][i] = gi < g.ng ? to_f(srow[gi]) : 0.f;
-                z[b][i] = zrow && gi < g.ng ? 128.f + (float)zrow[gi] : 136.f;
+            for (int t = 0; t < RT; ++t) p[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = i * (G / 32); j < (i + 1) * (G / 32); ++j) {
+                const bf16x8 wv = unpack(t4[j]);
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const bf16x8 xv = *(const bf16x8 *)(xs + xrow[t] + c0 + j * 32);
+                    p[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv, p[t], 0, 0, 0);
+                }
+            }
+            const int gi = c0 / G + i;
+            const float sc = to_f(sl[gi * NR + wn * 16 + col]);
+            const float cz = Z ? 128.f + (float)zl[gi * NR + wn * 16 + col] : 136.f;
+#pragma unroll
+            for (int t = 0; t < RT; ++t) {
+                const f32x4 tot = *(const f32x4 *)&sx[gi * (RT * 16) + t * 16 + quarter * 4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[t][q] = fmaf(sc, fmaf(-cz, tot[q], p[t][q]), acc[t][q]);
             }
         }
     };
-    fetch(0);
-    for (int64_t k0 = 0; k0 < g.K; k0 += SC) {
-        if (k0) __syncthreads();
-        // stage x[r0 .. ][k0 .. k0 + SC): 8 inputs a thread, and the sums of 32
-        for (int i = tid; i < RT * 16 * (SC / 8); i += kW4Threads) {
-            const int m = i / (SC / 8), c = (i % (SC / 8)) * 8;
+    if (whole > 0) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) fetch(u, (int64_t)(u * WK + wk) * 128);
+    }
+    constexpr int turn = 128 * WK * D;
+    for (int64_t s0 = 0; s0 < g.K; s0 += stage) {
+        if (s0) __syncthreads();
+        // stage x[r0 ..][s0 .. s0 + stage), and its sums over the groups; zeros past the inputs
+        const int64_t avail = (g.K - s0 + 127) / 128 * 128;
+        const int runs = (int)(avail < stage ? avail : stage) / 8;
+        for (int i = tid; i < rows * runs; i += kW4Threads) {
+            const int m = i / runs, c = (i - m * runs) * 8;
             Run<bf16, 8> v;
-            const int64_t left = g.K - k0 - c;
-            if (r0 + m >= g.R || left <= 0) v.zero();
-            else if (left >= 8) v.load(g.x + (r0 + m) * g.K + k0 + c);
-            else v.load_part(g.x + (r0 + m) * g.K + k0 + c, (int)left);
+            const bf16 *src = g.x + (r0 + m) * g.K + s0 + c;
+            const int64_t left = g.K - s0 - c;
+            if (left >= 8) v.load(src);
+            else if (left > 0) v.load_part(src, (int)left);
+            else v.zero();
             float sum = 0.f;
 #pragma unroll
             for (int q = 0; q < 8; ++q) sum += v.get(q);
             sum = quad_sum(sum);
+            if constexpr (G >= 64) sum += __shfl_xor(sum, 4);
+            if constexpr (G >= 128) sum += __shfl_xor(sum, 8);
             u32x4 o;  // pairs (0, 4) (1, 5) (2, 6) (3, 7)
             o[0] = __builtin_amdgcn_perm(v.w[2], v.w[0], 0x05040100);
             o[1] = __builtin_amdgcn_perm(v.w[2], v.w[0], 0x07060302);
             o[2] = __builtin_amdgcn_perm(v.w[3], v.w[1], 0x05040100);
             o[3] = __builtin_amdgcn_perm(v.w[3], v.w[1], 0x07060302);
-            *(u32x4 *)(xs + m * kRow + c) = o;
-            if ((i & 3) == 0) sx[c / 32][m] = sum;
+            *(u32x4 *)(xs + m * pitch + c) = o;
+            if (c % G == 0) sx[c / G * (RT * 16) + m] = sum;
         }
-        __syncthreads();
-        u32x4 cur[NB];
-        float cs[NB][NG], cz[NB][NG];
+        // the outputs' scales and zeros, 8 groups a thread; none past the last group
+        const int g0 = (int)(s0 / G), sets = (runs * 8 / G + 7) / 8;
+        for (int i = tid; i < outs * sets; i += kW4Threads) {
+            const int m = i / sets, c = (i - m * sets) * 8;
+            const int64_t at = (n0 + m) * g.ng + g0 + c;
+            const int left = (int)(g.ng - g0) - c;
+            Run<bf16, 8> v;
+            Run<uint8_t, 8> zv;
+            v.zero();
+            zv.zero();
+            if (left >= 8) {
+                v.load(g.scales + at);
+                if (Z) zv.load(g.zeros + at);
+            }
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            cur[b] = d[b];
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                cs[b][i] = s[b][i];
-                cz[b][i] = z[b][i];
+            for (int q = 0; q < 8; ++q) {
+                if (c + q >= groups) continue;
+                const bool alone = left < 8 && q < left;
+                sl[(c + q) * NR + m] = alone ? g.scales[at + q] : v.get_raw(q);
+                if (Z)
+                    zl[(c + q) * NR + m] =
+                        alone ? g.zeros[at + q] : (uint8_t)(zv.w[q / 4] >> (8 * (q % 4)));
             }
         }
-        if (k0 + SC < g.K) fetch(k0 + SC);
+        __syncthreads();
+        const int64_t s1 = s0 + stage < g.K ? s0 + stage : g.K;
+        int64_t k1 = s0;
+        for (; k1 + turn <= whole && k1 < s1; k1 += turn) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const u32x4 t4 = transpose_quarters(cur[b]);
-            const int c0 = (b * WK + wk) * 128;
+            for (int u = 0; u < D; ++u) {
+                const int64_t k = k1 + (u * WK + wk) * 128;
+                const u32x4 t4 = arrange(d[u]);
+                // what the next load overwrites is used up, and it is issued here: left to
+                // itself the scheduler collects the loads at the end of the loop and waits there
+                __builtin_amdgcn_sched_barrier(0);
+                fetch(u, k + turn);
+                __builtin_amdgcn_sched_barrier(0);
+                block(t4, (int)(k - s0));
+            }
+        }
+        if (k1 >= s1) continue;
+        // the last turn: the blocks in hand, and the one cut short by the end of the inputs,
+        // of which nothing past that end is read
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                f32x4 p[RT];
-                f32x4 tot[RT];
+        for (int u = 0; u < D; ++u) {
+            const int64_t k = k1 + (u * WK + wk) * 128;
+            if (k < whole) {
+                block(arrange(d[u]), (int)(k - s0));
+            } else if (k < g.K) {
+                u32x4 t = {0, 0, 0, 0};
+                const int left = (int)(g.K - k) / 2 - (lane & 3) * 16;
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    p[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-                    tot[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-                }
-#pragma unroll
-                for (int j = i * (G / 32); j < (i + 1) * (G / 32); ++j) {
-                    const bf16x8 wv = unpack(t4[j]);
-#pragma unroll
-                    for (int t = 0; t < RT; ++t) {
-                        const bf16x8 xv = *(const bf16x8 *)(xs + (t * 16 + col) * kRow + c0 +
-                                                            j * 32 + quarter * 8);
-                        p[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv, p[t], 0, 0, 0);
-                        tot[t] += *(const f32x4 *)&sx[c0 / 32 + j][t * 16 + quarter * 4];
-                    }
-                }
-#pragma unroll
-                for (int t = 0; t < RT; ++t)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        acc[t][q] = fmaf(cs[b][i], fmaf(-cz[b][i], tot[t][q], p[t][q]), acc[t][q]);
+                for (int j = 0; j < 16; ++j)
+                    if (j < left) t[j / 4] |= (uint32_t)qtile[k / 2 + loff + j] << (8 * (j % 4));
+                block(arrange(t), (int)(k - s0));
             }
         }
     }
@@ -222,21 +285,50 @@ __global__ __launch_bounds__(kW4Threads) void w4_kernel(const W4Args g)
         }
 }
 
-template <int RT, int G, int WK> static hipError_t launch_w4_t(const W4Args &g, hipStream_t st)
+template <int RT, int G, int WK, int D, bool Z>
+static hipError_t launch_w4_t(const W4Args &g, hipStream_t st)
 {
     constexpr int per = (kW4Waves / WK) * 16;
+    constexpr int64_t unit = 128 * WK * D;  // inputs of a turn of the ring
+    constexpr int64_t budget = 78 << 10;    // two workgroups on a CU
+    const int64_t rows = g.R < RT * 16 ? g.R : RT * 16;
+    // LDS of `s` staged inputs: the waves' blocks; rows of x; per group RT * 16 sums and `per`
+    // scales and zeros
+    auto bytes = [&](int64_t s) {
+        return 1024 * kW4Waves + rows * (s + 8) * 2 + s / G * (RT * 16 * 4 + per * (Z ? 3 : 2));
+    };
+    const int64_t all = (g.K + unit - 1) / unit * unit;
+    int64_t stage = unit;
+    while (stage < all && bytes(stage + unit) <= budget) stage += unit;
+    int64_t lds = bytes(stage);
+    const int64_t red = WK > 1 ? kW4Waves * RT * 256 * 4 : 0;
+    if (lds < red) lds = red;
+    // (above 64 KB a kernel has to ask for its LDS)
+    if (lds > (64 << 10)) {
+        const hipError_t e =
+            hipFuncSetAttribute((const void *)w4_kernel<RT, G, WK, D, Z>,
+                                hipFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
+        if (e != hipSuccess) return e;
+    }
     const dim3 grid((unsigned)((g.N + per - 1) / per), (unsigned)((g.R + RT * 16 - 1) / (RT * 16)));
-    hipLaunchKernelGGL((w4_kernel<RT, G, WK>), grid, dim3(kW4Threads), 0, st, g);
+    hipLaunchKernelGGL((w4_kernel<RT, G, WK, D, Z>), grid, dim3(kW4Threads), (size_t)lds, st, g,
+                       (int)stage);
     return hipGetLastError();
 }
 
+template <int G, bool Z> static hipError_t launch_w4_z(const W4Args &g, hipStream_t st)
+{
+    // few outputs: the waves of a workgroup split the inputs of a tile
+    const bool split = g.N < 16 * 8 * 512;
+    if (g.R <= 16)
+        return split ? launch_w4_t<1, G, 4, 4, Z>(g, st) : launch_w4_t<1, G, 1, 4, Z>(g, st);
+    if (g.R <= 32)
+        return split ? launch_w4_t<2, G, 4, 2, Z>(g, st) : launch_w4_t<2, G, 1, 4, Z>(g, st);
+    return split ? launch_w4_t<4, G, 2, 2, Z>(g, st) : launch_w4_t<4, G, 1, 4, Z>(g, st);
+}
 template <int G> static hipError_t launch_w4(const W4Args &g, hipStream_t st)
 {
-    // few outputs: the waves of a workgroup split the inputs of one tile
-    const bool split = g.N < 16 * 8 * 512;
-    if (g.R <= 16) return split ? launch_w4_t<1, G, 8>(g, st) : launch_w4_t<1, G, 1>(g, st);
-    if (g.R <= 32) return split ? launch_w4_t<2, G, 4>(g, st) : launch_w4_t<2, G, 1>(g, st);
-    return split ? launch_w4_t<4, G, 4>(g, st) : launch_w4_t<4, G, 1>(g, st);
+    return g.zeros ? launch_w4_z<G, true>(g, st) : launch_w4_z<G, false>(g, st);
 }
 
 // ------------------------------------------------------------ quantisation
