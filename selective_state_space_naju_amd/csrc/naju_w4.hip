@@ -56,18 +56,21 @@ __device__ __forceinline__ u32x4 transpose_quarters(u32x4 d)
     return u32x4{c[0], c[1], e[0], e[1]};
 }
 
-// 8 codes as the bf16 numbers 128 + q, in the order 0 4 1 5 2 6 3 7
-__device__ __forceinline__ bf16x8 unpack(uint32_t d)
+// 8 codes as the bf16 numbers 128 + q, in the order 0 4 1 5 2 6 3 7.  `ones` holds
+// 0x43004300 in a register: with one constant of its own the instruction can
+// mask and or at once.
+__device__ __forceinline__ bf16x8 unpack(uint32_t d, uint32_t ones)
 {
     u32x4 r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = ((d >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    for (int i = 0; i < 4; ++i) r[i] = ((d >> (4 * i)) & 0x000f000fu) | ones;
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// One workgroup: WN = kW4Waves / WK tiles of 16 outputs; the WK waves of a tile
-// take every WK-th block of 128 inputs.  RT: tiles of 16 rows of x; G: inputs of
-// a group; D: blocks whose codes a wave holds or has in flight; Z: zeros are
+// One workgroup: WN = kW4Waves / WK sets of 16 NT outputs; the WK waves of a set
+// take every WK-th block of 128 inputs.  RT: tiles of 16 rows of x; P: rows of x
+// that LDS has room for (lanes that stand for more repeat some); NT: tiles of
+// 16 outputs that a wave multiplies with the same x; G: inputs of a group; D: blocks whose codes a wave holds or has in flight; Z: zeros are
 // given.
 //
 // x and the outputs' scales and zeros are staged in LDS, `stage` inputs at a time
@@ -84,85 +87,111 @@ __device__ __forceinline__ bf16x8 unpack(uint32_t d)
 // The loads of whole blocks are unconditional (past the last one they repeat
 // it): a load that is issued under a condition makes the compiler wait for the
 // ones in flight where the branches meet.
-template <int RT, int G, int WK, int D, bool Z>
-__global__ __launch_bounds__(kW4Threads) void w4_kernel(const W4Args g, const int stage)
+template <int RT, int P, int G, int WK, int NT, int D, bool Z>
+__global__ __launch_bounds__(kW4Threads, 4) void w4_kernel(const W4Args g, const int stage,
+                                                           const FastDiv by_rows)
 {
     constexpr int WN = kW4Waves / WK;
     constexpr int NG = 128 / G;  // groups of a block
-    constexpr int NR = WN * 16;  // outputs of the workgroup
+    constexpr int NR = WN * NT * 16;  // outputs of the workgroup
     extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wk = w % WK, wn = w / WK, col = lane & 15, quarter = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * NR;  // first output
-    const int64_t n = n0 + wn * 16 + col;
+    const int o0 = wn * NT * 16;                  // the wave's first among them
     const int64_t r0 = (int64_t)blockIdx.y * (RT * 16);
     const int rows = g.R - r0 < RT * 16 ? (int)(g.R - r0) : RT * 16;
     const int outs = g.N - n0 < NR ? (int)(g.N - n0) : NR;
-    const int pitch = stage + 8;               // of a staged row: the pad spreads the banks
     const int groups = stage / G;              // of a stage
     uint32_t *slot = lds + w * 256;            // this wave's block of codes
-    bf16 *xs = (bf16 *)(lds + kW4Waves * 256);            // [rows][pitch]
-    float *sx = (float *)(xs + rows * pitch);             // [groups][RT * 16]: sums of x
-    bf16 *sl = (bf16 *)(sx + groups * (RT * 16));         // [groups][NR]: scales
+    // staged x: [stage / 8][P][8].  Row m of the 8 inputs from c stands at m ^ (c / 32 % 4): the
+    // lanes of a staging write, one row's neighbouring inputs, would otherwise all meet one bank
+    bf16 *xs = (bf16 *)(lds + kW4Waves * 256);
+    float *sx = (float *)(xs + P * stage);                // [groups][P]: sums of x
+    bf16 *sl = (bf16 *)(sx + groups * P);         // [groups][NR]: scales
     uint8_t *zl = (uint8_t *)(sl + groups * NR);          // [groups][NR]: zeros
 
-    f32x4 acc[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int xrow[RT];  // where this lane's row of a tile is staged
+    f32x4 acc[RT][NT];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
-        xrow[t] = (t * 16 + col < rows ? t * 16 + col : rows - 1) * pitch + quarter * 8;
+#pragma unroll
+        for (int v = 0; v < NT; ++v) acc[t][v] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int xrow[4];  // where this lane's row and quarter of the j-th 32 inputs is staged
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xrow[j] = ((j * 4 + quarter) * P + ((col & (P - 1)) ^ j)) * 8;
 
     // codes: lane l loads 16 bytes of row l / 4 of the tile (past the last output: of that one)
-    const int lrow = wn * 16 + (lane >> 2) < outs ? wn * 16 + (lane >> 2) : outs - 1;
-    const uint32_t loff = (uint32_t)lrow * (uint32_t)(g.K / 2) + (lane & 3) * 16;
+    uint32_t loff[NT];
+#pragma unroll
+    for (int v = 0; v < NT; ++v) {
+        const int o = o0 + v * 16 + (lane >> 2);
+        loff[v] = (uint32_t)(o < outs ? o : outs - 1) * (uint32_t)(g.K / 2) + (lane & 3) * 16;
+    }
     const uint8_t *qtile = g.q + n0 * (g.K / 2);
     const int64_t whole = g.K / 128 * 128;  // inputs in whole blocks
-    u32x4 d[D];
+    u32x4 d[D][NT];
     auto fetch = [&](int u, int64_t k) {
         k = k < whole ? k : whole - 128;
-        __builtin_memcpy(&d[u], qtile + k / 2 + loff, 16);
+#pragma unroll
+        for (int v = 0; v < NT; ++v) __builtin_memcpy(&d[u][v], qtile + k / 2 + loff[v], 16);
     };
-    // a loaded block in the product's layout; within the slot a row's four parts are rotated by
-    // a quarter of its number, which spreads the banks of the read
-    const int put = (lane >> 2) * 4 + (((lane & 3) + (lane >> 4)) & 3);
-    const int get = col * 4 + ((quarter + (col >> 2)) & 3);
-    auto arrange = [&](const u32x4 v) {
-        ((u32x4 *)slot)[put] = v;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        const u32x4 r = ((const u32x4 *)slot)[get];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        return transpose_quarters(r);
+    // a loaded block in the product's layout.  Within the slot a row's four parts are exchanged
+    // by the row's number / 4, so that neither the write nor the read meets a bank twice
+    auto part = [](int row, int p) { return row * 4 + ((row >> 2) ^ (p & 1 ? 3 : 0) ^ (p >> 1)); };
+    const int put = part(lane >> 2, lane & 3), get = part(col, quarter);
+    auto arrange = [&](u32x4 (&r)[NT], const u32x4 (&in)[NT]) {
+#pragma unroll
+        for (int v = 0; v < NT; ++v) {
+            ((u32x4 *)slot)[put] = in[v];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            r[v] = ((const u32x4 *)slot)[get];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
     };
+    uint32_t ones = 0x43004300u;
+    asm volatile("" : "+v"(ones));
     // the products of a block of 128 inputs, c0 inputs into the stage
-    auto block = [&](const u32x4 t4, int c0) {
+    auto block = [&](const u32x4 (&t4)[NT], int c0) {
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
-            f32x4 p[RT];
+            f32x4 p[RT][NT];
 #pragma unroll
-            for (int t = 0; t < RT; ++t) p[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int v = 0; v < NT; ++v) p[t][v] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = i * (G / 32); j < (i + 1) * (G / 32); ++j) {
-                const bf16x8 wv = unpack(t4[j]);
+                bf16x8 wv[NT];
+#pragma unroll
+                for (int v = 0; v < NT; ++v) wv[v] = unpack(t4[v][j], ones);
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    const bf16x8 xv = *(const bf16x8 *)(xs + xrow[t] + c0 + j * 32);
-                    p[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv, p[t], 0, 0, 0);
+                    const bf16x8 xv = *(const bf16x8 *)(xs + c0 * P + xrow[j] + t * 128);
+#pragma unroll
+                    for (int v = 0; v < NT; ++v)
+                        p[t][v] =
+                            __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, wv[v], p[t][v], 0, 0, 0);
                 }
             }
             const int gi = c0 / G + i;
-            const float sc = to_f(sl[gi * NR + wn * 16 + col]);
-            const float cz = Z ? 128.f + (float)zl[gi * NR + wn * 16 + col] : 136.f;
+            float sc[NT], cz[NT];
+#pragma unroll
+            for (int v = 0; v < NT; ++v) {
+                sc[v] = to_f(sl[gi * NR + o0 + v * 16 + col]);
+                cz[v] = Z ? 128.f + (float)zl[gi * NR + o0 + v * 16 + col] : 136.f;
+            }
 #pragma unroll
             for (int t = 0; t < RT; ++t) {
-                const f32x4 tot = *(const f32x4 *)&sx[gi * (RT * 16) + t * 16 + quarter * 4];
+                const f32x4 tot = *(const f32x4 *)&sx[gi * P + t * 16 + (quarter * 4 & (P - 1))];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    acc[t][q] = fmaf(sc, fmaf(-cz, tot[q], p[t][q]), acc[t][q]);
+                for (int v = 0; v < NT; ++v)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        acc[t][v][q] =
+                            fmaf(sc[v], fmaf(-cz[v], tot[q], p[t][v][q]), acc[t][v][q]);
             }
         }
     };
@@ -171,32 +200,51 @@ __global__ __launch_bounds__(kW4Threads) void w4_kernel(const W4Args g, const in
         for (int u = 0; u < D; ++u) fetch(u, (int64_t)(u * WK + wk) * 128);
     }
     constexpr int turn = 128 * WK * D;
+    // the block that comes next is passed through the slot while one is multiplied
+    u32x4 next[NT] = {};
+    if (whole > 0) arrange(next, d[0]);
     for (int64_t s0 = 0; s0 < g.K; s0 += stage) {
         if (s0) __syncthreads();
         // stage x[r0 ..][s0 .. s0 + stage), and its sums over the groups; zeros past the inputs
         const int64_t avail = (g.K - s0 + 127) / 128 * 128;
         const int runs = (int)(avail < stage ? avail : stage) / 8;
-        for (int i = tid; i < rows * runs; i += kW4Threads) {
-            const int m = i / runs, c = (i - m * runs) * 8;
-            Run<bf16, 8> v;
-            const bf16 *src = g.x + (r0 + m) * g.K + s0 + c;
-            const int64_t left = g.K - s0 - c;
-            if (left >= 8) v.load(src);
-            else if (left > 0) v.load_part(src, (int)left);
-            else v.zero();
-            float sum = 0.f;
+        // (rows of 512 inputs are dealt out to the waves, 2 RT of them in flight)
+        const int64_t left = g.K - s0;
+        const int parts = (int)by_rows.d * ((runs + 63) / 64);
+        const bf16 *src = g.x + r0 * g.K + s0;
+        for (int p0 = w; p0 < parts; p0 += kW4Waves * 2 * RT) {
+            Run<bf16, 8> v[2 * RT];
+            int m[2 * RT], c[2 * RT];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) sum += v.get(q);
-            sum = quad_sum(sum);
-            if constexpr (G >= 64) sum += __shfl_xor(sum, 4);
-            if constexpr (G >= 128) sum += __shfl_xor(sum, 8);
-            u32x4 o;  // pairs (0, 4) (1, 5) (2, 6) (3, 7)
-            o[0] = __builtin_amdgcn_perm(v.w[2], v.w[0], 0x05040100);
-            o[1] = __builtin_amdgcn_perm(v.w[2], v.w[0], 0x07060302);
-            o[2] = __builtin_amdgcn_perm(v.w[3], v.w[1], 0x05040100);
-            o[3] = __builtin_amdgcn_perm(v.w[3], v.w[1], 0x07060302);
-            *(u32x4 *)(xs + m * pitch + c) = o;
-            if (c % G == 0) sx[c / G * (RT * 16) + m] = sum;
+            for (int i = 0; i < 2 * RT; ++i) {
+                const int p = p0 + i * kW4Waves < parts ? p0 + i * kW4Waves : p0;
+                const int cb = (int)fdiv((uint32_t)p, by_rows);
+                m[i] = p - cb * (int)by_rows.d;
+                c[i] = cb * 512 + lane * 8;
+                const bf16 *at = src + m[i] * g.K;
+                if (m[i] >= rows) v[i].zero();  // (the last rows' workgroups have fewer)
+                else if (c[i] + 8 <= left) v[i].load(at + c[i]);
+                else if (c[i] < left) v[i].load_part(at + c[i], (int)(left - c[i]));
+                else v[i].zero();
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * RT; ++i) {
+                if (p0 + i * kW4Waves >= parts) break;  // (uniform)
+                float sum = 0.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) sum += v[i].get(q);
+                sum = quad_sum(sum);
+                if constexpr (G >= 64) sum += __shfl_xor(sum, 4);
+                if constexpr (G >= 128) sum += __shfl_xor(sum, 8);
+                if (c[i] >= runs * 8 || m[i] >= rows) continue;
+                u32x4 o;  // pairs (0, 4) (1, 5) (2, 6) (3, 7)
+                o[0] = __builtin_amdgcn_perm(v[i].w[2], v[i].w[0], 0x05040100);
+                o[1] = __builtin_amdgcn_perm(v[i].w[2], v[i].w[0], 0x07060302);
+                o[2] = __builtin_amdgcn_perm(v[i].w[3], v[i].w[1], 0x05040100);
+                o[3] = __builtin_amdgcn_perm(v[i].w[3], v[i].w[1], 0x07060302);
+                *(u32x4 *)(xs + c[i] * P + (m[i] ^ ((c[i] >> 5) & 3)) * 8) = o;
+                if (c[i] % G == 0) sx[c[i] / G * P + m[i]] = sum;
+            }
         }
         // the outputs' scales and zeros, 8 groups a thread; none past the last group
         const int g0 = (int)(s0 / G), sets = (runs * 8 / G + 7) / 8;
@@ -229,7 +277,10 @@ __global__ __launch_bounds__(kW4Threads) void w4_kernel(const W4Args g, const in
 #pragma unroll
             for (int u = 0; u < D; ++u) {
                 const int64_t k = k1 + (u * WK + wk) * 128;
-                const u32x4 t4 = arrange(d[u]);
+                u32x4 t4[NT];
+#pragma unroll
+                for (int v = 0; v < NT; ++v) t4[v] = transpose_quarters(next[v]);
+                arrange(next, d[(u + 1) % D]);
                 // what the next load overwrites is used up, and it is issued here: left to
                 // itself the scheduler collects the loads at the end of the loop and waits there
                 __builtin_amdgcn_sched_barrier(0);
@@ -245,74 +296,92 @@ __global__ __launch_bounds__(kW4Threads) void w4_kernel(const W4Args g, const in
         for (int u = 0; u < D; ++u) {
             const int64_t k = k1 + (u * WK + wk) * 128;
             if (k < whole) {
-                block(arrange(d[u]), (int)(k - s0));
+                u32x4 t4[NT];
+#pragma unroll
+                for (int v = 0; v < NT; ++v) t4[v] = transpose_quarters(next[v]);
+                if (u + 1 < D) arrange(next, d[u + 1 < D ? u + 1 : 0]);
+                block(t4, (int)(k - s0));
             } else if (k < g.K) {
-                u32x4 t = {0, 0, 0, 0};
+                u32x4 t4[NT] = {};
                 const int left = (int)(g.K - k) / 2 - (lane & 3) * 16;
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (j < left) t[j / 4] |= (uint32_t)qtile[k / 2 + loff + j] << (8 * (j % 4));
-                block(arrange(t), (int)(k - s0));
+                for (int v = 0; v < NT; ++v)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < left)
+                            t4[v][j / 4] |= (uint32_t)qtile[k / 2 + loff[v] + j] << (8 * (j % 4));
+                arrange(t4, t4);
+#pragma unroll
+                for (int v = 0; v < NT; ++v) t4[v] = transpose_quarters(t4[v]);
+                block(t4, (int)(k - s0));
             }
         }
     }
 
     // the waves of an output tile add their sums in order
     if constexpr (WK > 1) {
-        float *red = (float *)lds;
+        f32x4 *red = (f32x4 *)lds;
         __syncthreads();
 #pragma unroll
-        for (int t = 0; t < RT; ++t) *(f32x4 *)&red[((w * RT + t) * 64 + lane) * 4] = acc[t];
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int v = 0; v < NT; ++v) red[((w * RT + t) * NT + v) * 64 + lane] = acc[t][v];
         __syncthreads();
         if (wk != 0) return;
 #pragma unroll
         for (int i = 1; i < WK; ++i)
 #pragma unroll
             for (int t = 0; t < RT; ++t)
-                acc[t] += *(const f32x4 *)&red[(((w + i) * RT + t) * 64 + lane) * 4];
+#pragma unroll
+                for (int v = 0; v < NT; ++v)
+                    acc[t][v] += red[(((w + i) * RT + t) * NT + v) * 64 + lane];
     }
-    if (n >= g.N) return;
-    const float bias = g.bias ? g.bias[n] : 0.f;
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+    for (int v = 0; v < NT; ++v) {
+        const int64_t n = n0 + o0 + v * 16 + col;
+        if (n >= g.N) continue;
+        const float bias = g.bias ? g.bias[n] : 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t r = r0 + t * 16 + quarter * 4 + q;
-            if (r >= g.R) continue;
-            float v = acc[t][q] + bias;
-            if (g.res) v += to_f(g.res[r * g.N + n]);
-            g.y[r * g.N + n] = from_f<bf16>(v);
-        }
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t r = r0 + t * 16 + quarter * 4 + q;
+                if (r >= g.R) continue;
+                float y = acc[t][v][q] + bias;
+                if (g.res) y += to_f(g.res[r * g.N + n]);
+                g.y[r * g.N + n] = from_f<bf16>(y);
+            }
+    }
 }
 
-template <int RT, int G, int WK, int D, bool Z>
+template <int RT, int P, int G, int WK, int NT, int D, bool Z>
 static hipError_t launch_w4_t(const W4Args &g, hipStream_t st)
 {
-    constexpr int per = (kW4Waves / WK) * 16;
+    constexpr int per = (kW4Waves / WK) * NT * 16;
     constexpr int64_t unit = 128 * WK * D;  // inputs of a turn of the ring
     constexpr int64_t budget = 78 << 10;    // two workgroups on a CU
     const int64_t rows = g.R < RT * 16 ? g.R : RT * 16;
-    // LDS of `s` staged inputs: the waves' blocks; rows of x; per group RT * 16 sums and `per`
+    // LDS of `s` staged inputs: the waves' blocks; P rows of x; per group P sums and `per`
     // scales and zeros
     auto bytes = [&](int64_t s) {
-        return 1024 * kW4Waves + rows * (s + 8) * 2 + s / G * (RT * 16 * 4 + per * (Z ? 3 : 2));
+        return 1024 * kW4Waves + P * s * 2 + s / G * (P * 4 + per * (Z ? 3 : 2));
     };
     const int64_t all = (g.K + unit - 1) / unit * unit;
     int64_t stage = unit;
     while (stage < all && bytes(stage + unit) <= budget) stage += unit;
     int64_t lds = bytes(stage);
-    const int64_t red = WK > 1 ? kW4Waves * RT * 256 * 4 : 0;
+    const int64_t red = WK > 1 ? kW4Waves * RT * NT * 256 * 4 : 0;
     if (lds < red) lds = red;
     // (above 64 KB a kernel has to ask for its LDS)
     if (lds > (64 << 10)) {
         const hipError_t e =
-            hipFuncSetAttribute((const void *)w4_kernel<RT, G, WK, D, Z>,
+            hipFuncSetAttribute((const void *)w4_kernel<RT, P, G, WK, NT, D, Z>,
                                 hipFuncAttributeMaxDynamicSharedMemorySize, 160 << 10);
         if (e != hipSuccess) return e;
     }
     const dim3 grid((unsigned)((g.N + per - 1) / per), (unsigned)((g.R + RT * 16 - 1) / (RT * 16)));
-    hipLaunchKernelGGL((w4_kernel<RT, G, WK, D, Z>), grid, dim3(kW4Threads), (size_t)lds, st, g,
-                       (int)stage);
+    hipLaunchKernelGGL((w4_kernel<RT, P, G, WK, NT, D, Z>), grid, dim3(kW4Threads), (size_t)lds, st, g,
+                       (int)stage, make_fastdiv((uint32_t)rows));
     return hipGetLastError();
 }
 
@@ -320,11 +389,17 @@ template <int G, bool Z> static hipError_t launch_w4_z(const W4Args &g, hipStrea
 {
     // few outputs: the waves of a workgroup split the inputs of a tile
     const bool split = g.N < 16 * 8 * 512;
+    if (g.R <= 4)
+        return split ? launch_w4_t<1, 4, G, 4, 1, 4, Z>(g, st)
+                     : launch_w4_t<1, 4, G, 1, 1, 4, Z>(g, st);
     if (g.R <= 16)
-        return split ? launch_w4_t<1, G, 4, 4, Z>(g, st) : launch_w4_t<1, G, 1, 4, Z>(g, st);
+        return split ? launch_w4_t<1, 16, G, 4, 1, 4, Z>(g, st)
+                     : launch_w4_t<1, 16, G, 1, 1, 4, Z>(g, st);
     if (g.R <= 32)
-        return split ? launch_w4_t<2, G, 4, 2, Z>(g, st) : launch_w4_t<2, G, 1, 4, Z>(g, st);
-    return split ? launch_w4_t<4, G, 2, 2, Z>(g, st) : launch_w4_t<4, G, 1, 4, Z>(g, st);
+        return split ? launch_w4_t<2, 32, G, 4, 1, 2, Z>(g, st)
+                     : launch_w4_t<2, 32, G, 1, 2, 2, Z>(g, st);
+    return split ? launch_w4_t<4, 64, G, 2, 1, 2, Z>(g, st)
+                 : launch_w4_t<4, 64, G, 1, 1, 4, Z>(g, st);
 }
 template <int G> static hipError_t launch_w4(const W4Args &g, hipStream_t st)
 {
