@@ -76,11 +76,12 @@ static hipError_t launch_embed_fwd(int64_t T, int64_t V, int64_t d, const int32_
 // ------------------------------------------------------------------- sort
 // Stable least-significant-digit radix sort of (token, position), up to 9 bits
 // a pass.  Tokens outside [0, V) get the key V: they end up last and are
-// dropped there.  A pass is two kernels: every tile of kTile keys counts its
+// dropped there.  A pass is two kernels: every tile of 1024 ROUNDS keys counts its
 // digits, then every tile ranks its keys (in its own order) behind the smaller
 // digits of all tiles and the equal digits of the tiles before it.
-constexpr int kTile = 4096;
 constexpr int kDigits = 512;  // most values of a digit
+// keys of a tile: 1024 while that leaves a tile few others to look at, else 4096
+static int tile_rounds(int64_t T) { return T <= 16384 ? 1 : 4; }
 
 __device__ __forceinline__ uint32_t key_of(const int32_t *ids, const uint32_t *keys, int64_t i,
                                            uint32_t V)
@@ -90,18 +91,45 @@ __device__ __forceinline__ uint32_t key_of(const int32_t *ids, const uint32_t *k
     return id < V ? id : V;  // (a negative id is a large unsigned one)
 }
 
+// The zero fill of dW needs nothing from the sort, whose kernels leave most of
+// the device idle: each launch of the sort carries workgroups that fill a slice.
+// (16384 x 768 tokens over 50000 rows: 72 us with the fill in front of the
+// sort; the fill alone is 21 us, the sort 27 us.)
+struct Fill {
+    float *p;       // null: nothing to fill
+    int64_t n;      // floats of this launch's slice
+    int blocks;     // workgroups that share it
+};
+
+__device__ __forceinline__ void fill_slice(const Fill &f, int block)
+{
+    const int64_t per = (f.n + f.blocks - 1) / f.blocks;
+    const int64_t lo = per * block, hi = lo + per < f.n ? lo + per : f.n;
+    Run<float, 4> z;
+    z.zero();
+    for (int64_t i = lo + threadIdx.x * 4; i < hi; i += blockDim.x * 4) {
+        if (i + 4 <= hi) z.store(f.p + i);
+        else z.store_part(f.p + i, (int)(hi - i));
+    }
+}
+
+template <int ROUNDS>
 __global__ __launch_bounds__(1024) void radix_count_kernel(
     const int64_t T, const uint32_t V, const int32_t *__restrict__ ids,
-    const uint32_t *__restrict__ keys, const int shift, const int digits,
-    uint32_t *__restrict__ counts)
+    const uint32_t *__restrict__ keys, const int shift, const int digits, const int n_tiles,
+    uint32_t *__restrict__ counts, const Fill fill)
 {
     __shared__ uint32_t hist[kDigits];
     const int tid = threadIdx.x;
+    if ((int)blockIdx.x >= n_tiles) {
+        fill_slice(fill, (int)blockIdx.x - n_tiles);
+        return;
+    }
     if (tid < kDigits) hist[tid] = 0u;
     __syncthreads();
-    const int64_t base = (int64_t)blockIdx.x * kTile;
+    const int64_t base = (int64_t)blockIdx.x * (1024 * ROUNDS);
 #pragma unroll
-    for (int q = 0; q < kTile / 1024; ++q) {
+    for (int q = 0; q < ROUNDS; ++q) {
         const int64_t i = base + q * 1024 + tid;
         if (i < T) atomicAdd(&hist[(key_of(ids, keys, i, V) >> shift) & (digits - 1)], 1u);
     }
@@ -132,16 +160,21 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t dg, int bits, bool valid
     return m;
 }
 
+template <int ROUNDS>
 __global__ __launch_bounds__(1024) void radix_scatter_kernel(
     const int64_t T, const uint32_t V, const int32_t *__restrict__ ids,
     const uint32_t *__restrict__ keys, const int32_t *__restrict__ pos, const int shift,
     const int bits, const int n_tiles, const uint32_t *__restrict__ counts,
-    uint32_t *__restrict__ out_keys, int32_t *__restrict__ out_pos)
+    uint32_t *__restrict__ out_keys, int32_t *__restrict__ out_pos, const Fill fill)
 {
     // cnt[w][digit]: the keys of wave w with this digit, then where its first one goes
     __shared__ uint32_t cnt[16][kDigits];
     __shared__ uint32_t wsum[16];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    if ((int)blockIdx.x >= n_tiles) {
+        fill_slice(fill, (int)blockIdx.x - n_tiles);
+        return;
+    }
     const int digits = 1 << bits;
     for (int i = tid; i < 16 * kDigits; i += 1024) (&cnt[0][0])[i] = 0u;
     // digit tid: keys of the tiles before this one, and of all tiles
@@ -159,17 +192,16 @@ __global__ __launch_bounds__(1024) void radix_scatter_kernel(
     uint32_t start = incl - total + before;
     for (int i = 0; i < w; ++i) start += wsum[i];
 
-    // each wave ranks its 256 consecutive keys, 64 at a time
-    constexpr int kRounds = kTile / 1024;
-    const int64_t base = (int64_t)blockIdx.x * kTile + w * (64 * kRounds);
-    uint32_t key[kRounds], rank[kRounds];
+    // each wave ranks its consecutive keys, 64 at a time
+    const int64_t base = (int64_t)blockIdx.x * (1024 * ROUNDS) + w * (64 * ROUNDS);
+    uint32_t key[ROUNDS], rank[ROUNDS];
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
+    for (int q = 0; q < ROUNDS; ++q) {
         const int64_t i = base + q * 64 + lane;
         key[q] = i < T ? key_of(ids, keys, i, V) : 0u;
     }
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
+    for (int q = 0; q < ROUNDS; ++q) {
         const bool valid = base + q * 64 + lane < T;
         const uint32_t dg = (key[q] >> shift) & (digits - 1);
         const uint64_t m = same_digit(dg, bits, valid);
@@ -196,7 +228,7 @@ __global__ __launch_bounds__(1024) void radix_scatter_kernel(
     }
     __syncthreads();
 #pragma unroll
-    for (int q = 0; q < kRounds; ++q) {
+    for (int q = 0; q < ROUNDS; ++q) {
         const int64_t i = base + q * 64 + lane;
         if (i >= T) continue;
         const uint32_t dg = (key[q] >> shift) & (digits - 1);
@@ -206,10 +238,102 @@ __global__ __launch_bounds__(1024) void radix_scatter_kernel(
     }
 }
 
+// Up to kSmallTokens tokens: one workgroup sorts them in LDS, a word holding
+// key << 12 | position, while the others fill.  One launch in place of two per
+// digit.  (With four times the tokens the one CU takes 110 us; several tiles
+// take 25.)
+constexpr int kSmallTokens = 4096;
+constexpr int64_t kSmallVocab = ((int64_t)1 << 20) - 1;  // keys 0 .. V in 20 bits
+
+__global__ __launch_bounds__(1024) void small_sort_kernel(
+    const int T, const uint32_t V, const int32_t *__restrict__ ids, const int passes,
+    const int bits, uint32_t *__restrict__ out_keys, int32_t *__restrict__ out_pos,
+    const Fill fill)
+{
+    __shared__ uint32_t buf[kSmallTokens];
+    __shared__ uint32_t cnt[16][kDigits];
+    __shared__ uint32_t wsum[16];
+    constexpr int kMostRounds = kSmallTokens / 1024;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    if (blockIdx.x > 0) {
+        fill_slice(fill, (int)blockIdx.x - 1);
+        return;
+    }
+    // each wave holds `rounds` x 64 consecutive words
+    const int rounds = (T + 1023) / 1024, base = w * rounds * 64 + lane;
+    const uint32_t digits = 1u << bits;
+    uint32_t word[kMostRounds], at[kMostRounds];
+#pragma unroll
+    for (int q = 0; q < kMostRounds; ++q) {
+        const int i = base + q * 64;
+        word[q] = 0;
+        if (q < rounds && i < T) word[q] = key_of(ids, nullptr, i, V) << 12 | (uint32_t)i;
+    }
+    for (int p = 0; p < passes; ++p) {
+        const int shift = 12 + p * bits;
+        for (int i = tid; i < 16 * kDigits; i += 1024) (&cnt[0][0])[i] = 0u;
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kMostRounds; ++q) {
+            if (q < rounds) {
+                const bool valid = base + q * 64 < T;
+                const uint32_t dg = (word[q] >> shift) & (digits - 1);
+                const uint64_t m = same_digit(dg, bits, valid);
+                const uint32_t below = __popcll(m & ((1ull << lane) - 1));
+                const uint32_t c = valid ? cnt[w][dg] : 0u;
+                at[q] = c + below;
+                // (only this wave touches cnt[w], as in radix_scatter_kernel)
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+                if (valid && below == 0) cnt[w][dg] = c + (uint32_t)__popcll(m);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+        __syncthreads();
+        // where each wave's first word of each digit goes
+        uint32_t total = 0;
+        if (tid < (int)digits)
+            for (int i = 0; i < 16; ++i) total += cnt[i][tid];
+        const uint32_t incl = wave_scan(total, lane);
+        if (lane == 63) wsum[w] = incl;
+        __syncthreads();
+        if (tid < (int)digits) {
+            uint32_t start = incl - total;
+            for (int i = 0; i < w; ++i) start += wsum[i];
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t c = cnt[i][tid];
+                cnt[i][tid] = start;
+                start += c;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kMostRounds; ++q) {
+            if (q < rounds && base + q * 64 < T)
+                buf[cnt[w][(word[q] >> shift) & (digits - 1)] + at[q]] = word[q];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kMostRounds; ++q) {
+            const int i = base + q * 64;
+            if (q < rounds && i < T) word[q] = buf[i];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kMostRounds; ++q) {
+        const int i = base + q * 64;
+        if (q < rounds && i < T) {
+            out_keys[i] = word[q] >> 12;
+            out_pos[i] = (int32_t)(word[q] & 4095u);
+        }
+    }
+}
+
 // -------------------------------------------------------------- gradient
 constexpr int kSeg = 16;             // sorted positions of a wave
-constexpr int kSegWaves = 8;
-constexpr int kBlk = kSeg * kSegWaves;
+constexpr int kSumWaves = 8;
+constexpr int kBlk = kSeg * kSumWaves;
 constexpr int kCols = 256;           // columns of a workgroup: 4 per lane
 
 __device__ __forceinline__ void add4(float (&a)[4], const float4 v)
@@ -244,18 +368,23 @@ __device__ __forceinline__ void write_row(float *dW, int64_t key, int64_t d, int
 
 // One workgroup sums the runs of kBlk sorted positions over kCols columns;
 // wave w takes kSeg of them.  All row loads of a wave are issued before the
-// first is used.  The keys are uniform over the wave.
+// first is used.  The keys are uniform over the wave.  (Waves side by side over
+// 1024 columns of fewer positions read no faster, and left more partial rows.)
 template <typename IO, bool ACC>
-__global__ __launch_bounds__(64 * kSegWaves) void embed_sum_kernel(
-    const int64_t T, const int64_t V, const int64_t d, const uint32_t *__restrict__ skey,
-    const int32_t *__restrict__ spos, const IO *__restrict__ dout, const float scale,
-    float *__restrict__ dW, float *__restrict__ part)
+__global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(
+    const int64_t T, const int64_t V, const int64_t d, const int64_t first, const uint32_t n_cols,
+    const uint32_t *__restrict__ skey, const int32_t *__restrict__ spos,
+    const IO *__restrict__ dout, const float scale, float *__restrict__ dW,
+    float *__restrict__ part)
 {
-    __shared__ float4 head[kSegWaves][64], tail[kSegWaves][64];
+    __shared__ float4 head[kSumWaves][64], tail[kSumWaves][64];
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t blk = (int64_t)blockIdx.x * kBlk, base = blk + w * kSeg;
-    const int64_t col = (int64_t)blockIdx.y * kCols + lane * 4;
+    // (the column tiles of a block run next to each other: whole rows are read at a time)
+    const int64_t ib = first + blockIdx.x / n_cols;
+    const uint32_t ic = blockIdx.x % n_cols;
+    const int64_t blk = ib * kBlk, base = blk + w * kSeg;
+    const int64_t col = (int64_t)ic * kCols + lane * 4;
     const int nc = d - col >= 4 ? 4 : d > col ? (int)(d - col) : 0;
     const int n = T - base >= kSeg ? kSeg : T > base ? (int)(T - base) : 0;
 
@@ -307,17 +436,17 @@ __global__ __launch_bounds__(64 * kSegWaves) void embed_sum_kernel(
     }
     __syncthreads();
 
-    // a run that begins in wave w and goes on, or (wave 0) the one that began
-    // before this workgroup: add the later waves' heads in order
-    const int64_t slot = (int64_t)blockIdx.x * 2;
+    // a run that begins in this wave and goes on, or (first waves) the one that
+    // began before this block: add the later waves' heads in order
+    const int64_t slot = ib * 2;
     if (has_tail) {
         const uint32_t k = skey[base + n - 1];
         const float4 t = tail[w][lane];
         float s[4] = {t.x, t.y, t.z, t.w};
         int j = w + 1;
-        for (; j < kSegWaves && blk + j * kSeg < T && skey[blk + j * kSeg] == k; ++j)
+        for (; j < kSumWaves && blk + j * kSeg < T && skey[blk + j * kSeg] == k; ++j)
             add4(s, head[j][lane]);
-        if (j == kSegWaves && blk + kBlk < T && skey[blk + kBlk] == k) {
+        if (j == kSumWaves && blk + kBlk < T && skey[blk + kBlk] == k) {
             if (nc > 0) {
                 Run<float, 4> r = round_run<float, 4>(s);
                 float *p = part + (slot + 1) * d + col;
@@ -331,7 +460,7 @@ __global__ __launch_bounds__(64 * kSegWaves) void embed_sum_kernel(
     if (w == 0 && n > 0 && prev == key[0] && key[0] < V) {
         const uint32_t k = key[0];
         float s[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < kSegWaves && blk + j * kSeg < T && skey[blk + j * kSeg] == k; ++j)
+        for (int j = 0; j < kSumWaves && blk + j * kSeg < T && skey[blk + j * kSeg] == k; ++j)
             add4(s, head[j][lane]);
         if (nc > 0) {
             Run<float, 4> r = round_run<float, 4>(s);
@@ -347,19 +476,22 @@ __global__ __launch_bounds__(64 * kSegWaves) void embed_sum_kernel(
 // The waves take every eighth of them; their sums are added in wave order.
 template <bool ACC>
 __global__ __launch_bounds__(512) void embed_join_kernel(
-    const int64_t T, const int64_t V, const int64_t d, const uint32_t *__restrict__ skey,
-    const float scale, const float *__restrict__ part, float *__restrict__ dW)
+    const int64_t T, const int64_t V, const int64_t d, const int64_t first,
+    const uint32_t n_cols, const uint32_t *__restrict__ skey, const float scale, const float *__restrict__ part,
+    float *__restrict__ dW)
 {
     __shared__ float4 sum[8][64];
-    const int64_t blk = (int64_t)blockIdx.x * kBlk, end = blk + kBlk;
+    const int64_t ib = first + blockIdx.x / n_cols;
+    const uint32_t ic = blockIdx.x % n_cols;
+    const int64_t blk = ib * kBlk, end = blk + kBlk;
     const uint32_t k = skey[end - 1];  // (the grid has no last block: end < T)
     if (k >= V || skey[end] != k || (blk > 0 && skey[blk - 1] == k)) return;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t col = (int64_t)blockIdx.y * kCols + lane * 4;
+    const int64_t col = (int64_t)ic * kCols + lane * 4;
     const int nc = d - col >= 4 ? 4 : d > col ? (int)(d - col) : 0;
-    // blocks whose first key is still k: (blockIdx.x, hi]
-    int64_t lo = (int64_t)blockIdx.x + 1, hi = (T - 1) / kBlk;
+    // blocks whose first key is still k: (ib, hi]
+    int64_t lo = ib + 1, hi = (T - 1) / kBlk;
     while (lo < hi) {
         const int64_t mid = (lo + hi + 1) / 2;
         if (skey[mid * kBlk] == k) lo = mid;
@@ -367,7 +499,7 @@ __global__ __launch_bounds__(512) void embed_join_kernel(
     }
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     if (nc > 0) {
-        for (int64_t j = (int64_t)blockIdx.x + 1 + w; j <= hi; j += 8 * 4) {
+        for (int64_t j = ib + 1 + w; j <= hi; j += 8 * 4) {
             Run<float, 4> r[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -388,7 +520,7 @@ __global__ __launch_bounds__(512) void embed_join_kernel(
     __syncthreads();
     if (w != 0 || nc <= 0) return;
     Run<float, 4> r;
-    const float *p = part + ((int64_t)blockIdx.x * 2 + 1) * d + col;
+    const float *p = part + (ib * 2 + 1) * d + col;
     if (nc == 4) r.load(p);
     else r.load_part(p, nc);
     float a[4];
@@ -412,7 +544,8 @@ static EmbedPlan embed_plan(int64_t T, int64_t V, int64_t d)
     while (((uint64_t)V >> bits) != 0) ++bits;  // keys 0 .. V (at least one digit)
     p.passes = (bits + 8) / 9;
     p.bits = (bits + p.passes - 1) / p.passes;
-    p.n_tiles = (int)((T + kTile - 1) / kTile);
+    const int64_t tile = 1024 * tile_rounds(T);
+    p.n_tiles = (int)((T + tile - 1) / tile);
     p.n_blk = (T + kBlk - 1) / kBlk;
     size_t at = 256;
     for (int i = 0; i < 2; ++i) {
@@ -433,13 +566,19 @@ static hipError_t launch_embed_sum(const EmbedPlan &pl, int64_t T, int64_t V, in
                                    const uint32_t *skey, const int32_t *spos, const void *dout,
                                    float scale, float *dW, float *part, hipStream_t st)
 {
-    const unsigned by = (unsigned)((d + kCols - 1) / kCols);
-    hipLaunchKernelGGL((embed_sum_kernel<IO, ACC>), dim3((unsigned)pl.n_blk, by),
-                       dim3(64 * kSegWaves), 0, st, T, V, d, skey, spos, (const IO *)dout, scale,
-                       dW, part);
-    if (pl.n_blk > 1)
-        hipLaunchKernelGGL(embed_join_kernel<ACC>, dim3((unsigned)(pl.n_blk - 1), by), dim3(512),
-                           0, st, T, V, d, skey, scale, part, dW);
+    const int64_t cols = (d + kCols - 1) / kCols;
+    const int64_t most = ((int64_t)1 << 22) / cols;  // blocks of a launch
+    for (int64_t i = 0; i < pl.n_blk; i += most) {
+        const int64_t n = pl.n_blk - i < most ? pl.n_blk - i : most;
+        hipLaunchKernelGGL((embed_sum_kernel<IO, ACC>), dim3((unsigned)(n * cols)),
+                           dim3(64 * kSumWaves), 0, st, T, V, d, i, (uint32_t)cols, skey, spos,
+                           (const IO *)dout, scale, dW, part);
+    }
+    for (int64_t i = 0; i < pl.n_blk - 1; i += most) {
+        const int64_t n = pl.n_blk - 1 - i < most ? pl.n_blk - 1 - i : most;
+        hipLaunchKernelGGL(embed_join_kernel<ACC>, dim3((unsigned)(n * cols)), dim3(512), 0, st, T,
+                           V, d, i, (uint32_t)cols, skey, scale, part, dW);
+    }
     return hipGetLastError();
 }
 
@@ -447,22 +586,46 @@ static hipError_t launch_embed_bwd(int64_t T, int64_t V, int64_t d, int io, cons
                                    const void *dout, float scale, bool acc, float *dW, char *ws,
                                    hipStream_t st)
 {
-    if (!acc) {
-        const hipError_t e = launch_zero(dW, (size_t)V * (size_t)d * 4, st);
-        if (e != hipSuccess || T == 0) return e;
-    }
+    if (T == 0) return launch_zero(dW, (size_t)V * (size_t)d * 4, st);
     const EmbedPlan pl = embed_plan(T, V, d);
     uint32_t *keys[2] = {(uint32_t *)(ws + pl.off_keys[0]), (uint32_t *)(ws + pl.off_keys[1])};
     int32_t *pos[2] = {(int32_t *)(ws + pl.off_pos[0]), (int32_t *)(ws + pl.off_pos[1])};
     uint32_t *counts = (uint32_t *)(ws + pl.off_counts);
     const uint32_t *ik = nullptr;
     const int32_t *ip = nullptr;
-    for (int q = 0; q < pl.passes; ++q) {
-        hipLaunchKernelGGL(radix_count_kernel, dim3(pl.n_tiles), dim3(1024), 0, st, T, (uint32_t)V,
-                           ids, ik, q * pl.bits, 1 << pl.bits, counts);
-        hipLaunchKernelGGL(radix_scatter_kernel, dim3(pl.n_tiles), dim3(1024), 0, st, T,
-                           (uint32_t)V, ids, ik, ip, q * pl.bits, pl.bits, pl.n_tiles, counts,
-                           keys[q & 1], pos[q & 1]);
+    // slices of the fill: all of it beside the small sort; else as the launches last, a count
+    // about a third of a scatter
+    const bool small = T <= kSmallTokens && V <= kSmallVocab;
+    const int64_t all = acc ? 0 : V * d;
+    const int units = small ? 1 : 4 * pl.passes;
+    int64_t filled = 0;
+    int done = 0;
+    auto slice = [&](int weight) {
+        done += weight;
+        const int64_t to = done == units ? all : all / units * done;
+        Fill f{dW + filled, to - filled, 0};
+        const int64_t blocks = (f.n + 16383) / 16384;
+        f.blocks = (int)(blocks < 4096 ? blocks : 4096);
+        filled = to;
+        return f;
+    };
+    if (small) {
+        const Fill f = slice(1);
+        hipLaunchKernelGGL(small_sort_kernel, dim3(1 + f.blocks), dim3(1024), 0, st, (int)T,
+                           (uint32_t)V, ids, pl.passes, pl.bits, keys[0], pos[0], f);
+        ik = keys[0];
+        ip = pos[0];
+    }
+    for (int q = 0; !small && q < pl.passes; ++q) {
+        const Fill f1 = slice(1), f2 = slice(3);
+        const bool one = tile_rounds(T) == 1;
+        hipLaunchKernelGGL(one ? radix_count_kernel<1> : radix_count_kernel<4>,
+                           dim3(pl.n_tiles + f1.blocks), dim3(1024), 0, st, T, (uint32_t)V, ids,
+                           ik, q * pl.bits, 1 << pl.bits, pl.n_tiles, counts, f1);
+        hipLaunchKernelGGL(one ? radix_scatter_kernel<1> : radix_scatter_kernel<4>,
+                           dim3(pl.n_tiles + f2.blocks), dim3(1024), 0, st, T, (uint32_t)V, ids,
+                           ik, ip, q * pl.bits, pl.bits, pl.n_tiles, counts, keys[q & 1],
+                           pos[q & 1], f2);
         ik = keys[q & 1];
         ip = pos[q & 1];
     }
