@@ -22,9 +22,9 @@
 
 namespace naju {
 
-constexpr int kLogThreads = 512;
-constexpr int kLogTile = 8192;         // most tokens of a workgroup
-constexpr int kLogSmallTile = 2048;
+constexpr int kLogThreads = 1024;
+constexpr int kLogTile = 16384;        // most tokens of a workgroup
+constexpr int kLogSmallTile = 4096;
 constexpr int kLogRuns = kLogTile / (4 * kLogThreads);  // accesses of 4 tokens per thread
 constexpr int kCountBits = 20;         // a word: list place (12 bits) | count (20 bits)
 constexpr uint32_t kCountMask = (1u << kCountBits) - 1;
@@ -88,144 +88,156 @@ __device__ __forceinline__ float penalised(float x, uint32_t count, const Logits
 }
 
 template <typename IO>
-__global__ __launch_bounds__(kLogThreads) void logits_kernel(const LogitsArgs g,
-                                                             const IO *__restrict__ logits)
+__global__ __launch_bounds__(kLogThreads, 8) void logits_kernel(const LogitsArgs g,
+                                                                const IO *__restrict__ logits,
+                                                                const int64_t first)
 {
-    __shared__ __attribute__((aligned(16))) uint32_t word[kLogTile];
-    __shared__ uint16_t list[kLogTile];
+    // word[tile], then the list of touched tokens, at most H + nb of them
+    extern __shared__ __attribute__((aligned(16))) uint32_t word[];
+    uint16_t *list = (uint16_t *)(word + g.tile);
     __shared__ uint32_t n_list;
     __shared__ uint64_t wave_best[kLogThreads / 64];
     const int tid = threadIdx.x;
     const bool touched = g.H > 0 || g.nb > 0;
-    for (int64_t u = blockIdx.x; u < g.B * g.n_tiles; u += gridDim.x) {
-        const int64_t b = u / g.n_tiles, v0 = (u - b * g.n_tiles) * g.tile;
-        const int nv = g.V - v0 < g.tile ? (int)(g.V - v0) : g.tile;
-        const IO *row = logits + b * g.ld + v0;
-        const uint32_t *mrow = g.mask ? g.mask + b * ((g.V + 31) / 32) + v0 / 32 : nullptr;
-        // the tile's logits and mask words, in flight while the lists are scanned
-        Run<IO, 4> in[kLogRuns];
-        uint32_t allowed[kLogRuns];
+    const int64_t b = first + blockIdx.x / (uint32_t)g.n_tiles;
+    const int64_t v0 = (int64_t)(blockIdx.x % (uint32_t)g.n_tiles) * g.tile;
+    const int nv = g.V - v0 < g.tile ? (int)(g.V - v0) : g.tile;
+    const IO *row = logits + b * g.ld + v0;
+    const uint32_t *mrow = g.mask ? g.mask + b * ((g.V + 31) / 32) + v0 / 32 : nullptr;
+    // the first of the lists, then the tile's logits and mask words, all in flight while the
+    // lists are counted (loads return in order: the lists would wait behind the logits)
+    const int32_t *bi = g.bias_ids + b * g.nb, *h = g.history + b * g.H;
+    int32_t bias0 = tid < g.nb ? bi[tid] : -1;
+    Run<IO, 4> in[kLogRuns];
+    uint32_t allowed[kLogRuns];
 #pragma unroll
-        for (int i = 0; i < kLogRuns; ++i) {
-            const int c = (i * kLogThreads + tid) * 4, m = nv - c;
-            in[i].zero();
-            allowed[i] = ~0u;
-            if (m >= 4) in[i].load(row + c);
-            else if (m > 0) in[i].load_part(row + c, m);
-            if (mrow && m > 0) allowed[i] = mrow[c >> 5] >> (c & 31);
+    for (int i = 0; i < kLogRuns; ++i) {
+        const int c = (i * kLogThreads + tid) * 4;
+        in[i].zero();
+        allowed[i] = ~0u;
+        if (c + 4 <= nv) {
+            in[i].load(row + c);
+            if (mrow) allowed[i] = mrow[c >> 5];
         }
+    }
+    if (touched) {
+        for (int i = tid * 4; i < g.tile; i += kLogThreads * 4)
+            *(uint4 *)&word[i] = make_uint4(0, 0, 0, 0);
+        if (tid == 0) n_list = 0;
+        __syncthreads();
+        // bias list: the first pair that names a token has the highest mark
+        for (int j = tid; j < g.nb; j += kLogThreads) {
+            const int64_t v = (j == tid ? bias0 : bi[j]) - v0;
+            if (v >= 0 && v < nv) atomicMax(&word[v], (uint32_t)(kPlaces - j) << kCountBits);
+        }
+        __syncthreads();
+        for (int j = tid; j < g.nb; j += kLogThreads) {
+            const int64_t v = bi[j] - v0;
+            if (v >= 0 && v < nv && (word[v] >> kCountBits) == (uint32_t)(kPlaces - j))
+                list[atomicAdd(&n_list, 1u)] = (uint16_t)v;
+        }
+        // history: whoever counts a token first lists it
+        int64_t len = g.H;
+        if (g.lengths) {
+            len = g.lengths[b];
+            len = len < 0 ? 0 : len > g.H ? g.H : len;
+        }
+        for (int64_t i = (int64_t)tid * 4; i < len; i += kLogThreads * 4) {
+            Run<float, 4> r;
+            const int m = len - i < 4 ? (int)(len - i) : 4;
+            if (m == 4) r.load((const float *)h + i);
+            else r.load_part((const float *)h + i, m);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t v = (int32_t)r.w[q] - v0;
+                if (q < m && v >= 0 && v < nv)
+                    if (atomicAdd(&word[v], 1u) == 0) list[atomicAdd(&n_list, 1u)] = (uint16_t)v;
+            }
+        }
+        __syncthreads();
+        const int n = (int)n_list;
+        for (int i = tid; i < n; i += kLogThreads) {
+            const int v = list[i];
+            const uint32_t w = word[v];
+            float x = penalised(to_f(row[v]), w & kCountMask, g, b);
+            if (w >> kCountBits) x = x + g.bias[b * g.nb + (kPlaces - (w >> kCountBits))];
+            if (x != x) x = __uint_as_float(0x7fc00000u);
+            word[v] = ~__float_as_uint(x);  // (0 only for a NaN pattern that is not used)
+        }
+        __syncthreads();
+    }
+    // dense pass
+    float top = -__builtin_huge_valf();
+    int32_t at = -1;
+    float *out = g.out + b * g.V + v0;
+#pragma unroll
+    for (int i = 0; i < kLogRuns; ++i) {
+        const int c = (i * kLogThreads + tid) * 4;
+        if (c + 4 > nv) continue;
+        float x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[q] = in[i].get(q);
         if (touched) {
-            for (int i = tid * 4; i < g.tile; i += kLogThreads * 4)
-                *(uint4 *)&word[i] = make_uint4(0, 0, 0, 0);
-            if (tid == 0) n_list = 0;
-            __syncthreads();
-            // bias list: the first pair that names a token has the highest mark
-            const int32_t *bi = g.bias_ids + b * g.nb;
-            for (int j = tid; j < g.nb; j += kLogThreads) {
-                const int64_t v = bi[j] - v0;
-                if (v >= 0 && v < nv) atomicMax(&word[v], (uint32_t)(kPlaces - j) << kCountBits);
-            }
-            __syncthreads();
-            for (int j = tid; j < g.nb; j += kLogThreads) {
-                const int64_t v = bi[j] - v0;
-                if (v >= 0 && v < nv && (word[v] >> kCountBits) == (uint32_t)(kPlaces - j))
-                    list[atomicAdd(&n_list, 1u)] = (uint16_t)v;
-            }
-            // history: whoever counts a token first lists it
-            int64_t len = g.H;
-            if (g.lengths) {
-                len = g.lengths[b];
-                len = len < 0 ? 0 : len > g.H ? g.H : len;
-            }
-            const int32_t *h = g.history + b * g.H;
-            for (int64_t i = (int64_t)tid * 4; i < len; i += kLogThreads * 4) {
-                Run<float, 4> r;
-                const int m = len - i < 4 ? (int)(len - i) : 4;
-                if (m == 4) r.load((const float *)h + i);
-                else r.load_part((const float *)h + i, m);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t v = (int32_t)r.w[q] - v0;
-                    if (q < m && v >= 0 && v < nv)
-                        if (atomicAdd(&word[v], 1u) == 0) list[atomicAdd(&n_list, 1u)] = (uint16_t)v;
-                }
-            }
-            __syncthreads();
-            const int n = (int)n_list;
-            for (int i = tid; i < n; i += kLogThreads) {
-                const int v = list[i];
-                const uint32_t w = word[v];
-                float x = penalised(to_f(row[v]), w & kCountMask, g, b);
-                if (w >> kCountBits) x = x + g.bias[b * g.nb + (kPlaces - (w >> kCountBits))];
-                if (x != x) x = __uint_as_float(0x7fc00000u);
-                word[v] = ~__float_as_uint(x);  // (0 only for a NaN pattern that is not used)
-            }
-            __syncthreads();
+            const uint4 w = *(const uint4 *)&word[c];
+            x[0] = w.x ? __uint_as_float(~w.x) : x[0];
+            x[1] = w.y ? __uint_as_float(~w.y) : x[1];
+            x[2] = w.z ? __uint_as_float(~w.z) : x[2];
+            x[3] = w.w ? __uint_as_float(~w.w) : x[3];
         }
-        // dense pass
-        float top = -__builtin_huge_valf();
-        int32_t at = -1;
-        float *out = g.out + b * g.V + v0;
 #pragma unroll
-        for (int i = 0; i < kLogRuns; ++i) {
-            const int c = (i * kLogThreads + tid) * 4, m = nv - c < 4 ? nv - c : 4;
-            if (m <= 0) continue;
-            float x[4];
+        for (int q = 0; q < 4; ++q)
+            if (!((allowed[i] >> ((c & 31) + q)) & 1u)) x[q] = -__builtin_huge_valf();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[q] = in[i].get(q);
-            if (touched) {
-                const uint4 w = *(const uint4 *)&word[c];
-                x[0] = w.x ? __uint_as_float(~w.x) : x[0];
-                x[1] = w.y ? __uint_as_float(~w.y) : x[1];
-                x[2] = w.z ? __uint_as_float(~w.z) : x[2];
-                x[3] = w.w ? __uint_as_float(~w.w) : x[3];
+        for (int q = 0; q < 4; ++q)
+            if (x[q] > top) {
+                top = x[q];
+                at = c + q;
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (!((allowed[i] >> q) & 1u)) x[q] = -__builtin_huge_valf();
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (q < m && x[q] > top) {
-                    top = x[q];
-                    at = (int32_t)(v0 + c + q);
-                }
-            const Run<float, 4> o = round_run<float, 4>(x);
-            if (m == 4) o.store(out + c);
-            else o.store_part(out + c, m);
+        round_run<float, 4>(x).store(out + c);
+    }
+    // the last one to three tokens
+    if (tid < (nv & 3)) {
+        const int c = (nv & ~3) + tid;
+        float x = to_f(row[c]);
+        if (touched && word[c]) x = __uint_as_float(~word[c]);
+        if (mrow && !((mrow[c >> 5] >> (c & 31)) & 1u)) x = -__builtin_huge_valf();
+        if (x > top) {
+            top = x;
+            at = c;
         }
-        if (g.best) {
-            uint64_t k = best_key(top, at);
+        out[c] = x;
+    }
+    if (g.best) {
+        uint64_t k = best_key(top, at < 0 ? -1 : (int32_t)(v0 + at));
 #pragma unroll
-            for (int o = 32; o > 0; o >>= 1) {
-                const uint64_t x = __shfl_xor(k, o);
-                k = x > k ? x : k;
-            }
-            if ((tid & 63) == 0) wave_best[tid >> 6] = k;
-            __syncthreads();
-            if (tid == 0) {
-                for (int i = 1; i < kLogThreads / 64; ++i) k = wave_best[i] > k ? wave_best[i] : k;
-                if (g.n_tiles == 1) {
+        for (int o = 32; o > 0; o >>= 1) {
+            const uint64_t x = __shfl_xor(k, o);
+            k = x > k ? x : k;
+        }
+        if ((tid & 63) == 0) wave_best[tid >> 6] = k;
+        __syncthreads();
+        if (tid == 0) {
+            for (int i = 1; i < kLogThreads / 64; ++i) k = wave_best[i] > k ? wave_best[i] : k;
+            if (g.n_tiles == 1) {
+                g.best[b] = key_index(k);
+            } else {
+                // the last tile of the row to report reads the row's key and clears
+                // the record for the next call.  Only the record's own words pass
+                // between workgroups, all by agent-scope atomics, so their order
+                // (the wait) is enough: a release here would write every dirty line
+                // of the L2 back first (243 us against 65 us at 256 x 131072)
+                RowBest *rb = (RowBest *)g.ws + b;
+                __hip_atomic_fetch_max(&rb->key, k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                wait_mem();
+                const uint32_t d = add_agent(&rb->done, 1u);
+                if (d + 1 == (uint32_t)g.n_tiles) {
+                    k = __hip_atomic_exchange(&rb->key, (uint64_t)0, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+                    st_agent(&rb->done, 0u);
                     g.best[b] = key_index(k);
-                } else {
-                    // the last tile of the row to report reads the row's key and clears
-                    // the record for the next call.  Only the record's own words pass
-                    // between workgroups, all by agent-scope atomics, so their order
-                    // (the wait) is enough: a release here would write every dirty line
-                    // of the L2 back first (243 us against 65 us at 256 x 131072)
-                    RowBest *rb = (RowBest *)g.ws + b;
-                    __hip_atomic_fetch_max(&rb->key, k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    wait_mem();
-                    const uint32_t d = add_agent(&rb->done, 1u);
-                    if (d + 1 == (uint32_t)g.n_tiles) {
-                        k = __hip_atomic_exchange(&rb->key, (uint64_t)0, __ATOMIC_RELAXED,
-                                                  __HIP_MEMORY_SCOPE_AGENT);
-                        st_agent(&rb->done, 0u);
-                        g.best[b] = key_index(k);
-                    }
                 }
             }
         }
-        __syncthreads();  // (word, list and wave_best are reused)
     }
 }
 
@@ -234,10 +246,23 @@ static size_t logits_ws_bytes(int64_t rows) { return align256(sizeof(RowBest) * 
 template <typename IO>
 static hipError_t launch_logits(const LogitsArgs &g, const void *logits, hipStream_t st)
 {
-    const int64_t units = g.B * g.n_tiles;
-    const unsigned grid = (unsigned)(units < (1 << 22) ? units : 1 << 22);
-    hipLaunchKernelGGL(logits_kernel<IO>, dim3(grid), dim3(kLogThreads), 0, st, g,
-                       (const IO *)logits);
+    size_t lds = 0;
+    if (g.H > 0 || g.nb > 0) {
+        const int64_t most = g.H + g.nb;
+        lds = (size_t)g.tile * 4 + (size_t)(most < g.tile ? most : g.tile) * 2;
+    }
+    // (above 64 KB a kernel has to ask for its LDS)
+    if (lds > (64 << 10)) {
+        const hipError_t e = hipFuncSetAttribute(
+            (const void *)logits_kernel<IO>, hipFuncAttributeMaxDynamicSharedMemorySize, 128 << 10);
+        if (e != hipSuccess) return e;
+    }
+    const int64_t most = ((int64_t)1 << 21) / g.n_tiles + 1;  // rows of a launch
+    for (int64_t r = 0; r < g.B; r += most) {
+        const int64_t rows = g.B - r < most ? g.B - r : most;
+        hipLaunchKernelGGL(logits_kernel<IO>, dim3((unsigned)(rows * g.n_tiles)), dim3(kLogThreads),
+                           lds, st, g, (const IO *)logits, r);
+    }
     return hipGetLastError();
 }
 
