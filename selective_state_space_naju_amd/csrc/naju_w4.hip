@@ -359,16 +359,22 @@ static hipError_t launch_w4_t(const W4Args &g, hipStream_t st)
 {
     constexpr int per = (kW4Waves / WK) * NT * 16;
     constexpr int64_t unit = 128 * WK * D;  // inputs of a turn of the ring
-    constexpr int64_t budget = 78 << 10;    // two workgroups on a CU
     const int64_t rows = g.R < RT * 16 ? g.R : RT * 16;
+    const int64_t wgs = (g.N + per - 1) / per * ((g.R + RT * 16 - 1) / (RT * 16));
+    // two workgroups on a CU, or one where there are not more than that
+    const int64_t budget = (wgs <= device_cu_count() ? 150 : 78) << 10;
     // LDS of `s` staged inputs: the waves' blocks; P rows of x; per group P sums and `per`
     // scales and zeros
     auto bytes = [&](int64_t s) {
         return 1024 * kW4Waves + P * s * 2 + s / G * (P * 4 + per * (Z ? 3 : 2));
     };
-    const int64_t all = (g.K + unit - 1) / unit * unit;
-    int64_t stage = unit;
-    while (stage < all && bytes(stage + unit) <= budget) stage += unit;
+    // all inputs at once if they fit, else whole turns of the ring
+    int64_t stage = (g.K + 127) / 128 * 128;
+    if (stage == 0) stage = 128;
+    if (bytes(stage) > budget) {
+        stage = unit;
+        while (bytes(stage + unit) <= budget) stage += unit;
+    }
     int64_t lds = bytes(stage);
     const int64_t red = WK > 1 ? kW4Waves * RT * NT * 256 * 4 : 0;
     if (lds < red) lds = red;
@@ -392,6 +398,9 @@ template <int G, bool Z> static hipError_t launch_w4_z(const W4Args &g, hipStrea
     if (g.R <= 4)
         return split ? launch_w4_t<1, 4, G, 4, 1, 4, Z>(g, st)
                      : launch_w4_t<1, 4, G, 1, 1, 4, Z>(g, st);
+    if (g.R <= 8)
+        return split ? launch_w4_t<1, 8, G, 4, 1, 4, Z>(g, st)
+                     : launch_w4_t<1, 8, G, 1, 1, 4, Z>(g, st);
     if (g.R <= 16)
         return split ? launch_w4_t<1, 16, G, 4, 1, 4, Z>(g, st)
                      : launch_w4_t<1, 16, G, 1, 1, 4, Z>(g, st);
