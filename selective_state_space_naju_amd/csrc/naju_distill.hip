@@ -12,6 +12,10 @@
 // The rows are long (tens of thousands of logits) and the entries few, so a
 // workgroup takes a row, streams it with 16-byte accesses and keeps one entry
 // per thread; statistics and sums are fp32, each rounded once on output.
+//
+// Bound by the bytes of the logits.  16384 x 32000 bf16: loss 219 us (4.8 TB/s;
+// 5.9 at 32768 logits a row), gradient 437 us, both in one call 423 us (5.0 TB/s,
+// a large copy's rate).
 #include <math.h>
 
 #include "naju_device.h"
@@ -474,7 +478,8 @@ struct DistillArgs {
 };
 
 // Short rows take workgroups of two waves: the rows, not the logits, are then what there are
-// many of (65536 x 1000 fp32, loss and gradient: 367 us with eight waves a row).
+// many of (65536 x 1000 fp32, loss and gradient: 367 us with eight waves a row, 195 us with
+// two).
 constexpr int kSmallBS = 128, kLargeBS = 512;
 template <typename IO> static bool short_rows(const DistillArgs &a)
 {

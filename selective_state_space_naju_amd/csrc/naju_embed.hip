@@ -11,6 +11,10 @@
 // partial row per block in the workspace, and a last kernel adds those in
 // order.  Sums are fp32.  dW is dense: rows of tokens that do not occur are
 // zero-filled (kept, when accumulating).
+//
+// Bound by the bytes of dout and dW: 65536 x 2048 fp32 over 100003 rows take
+// 345 us (1356 MB, 3.9 TB/s; a copy reaches 4.8), 16384 x 768 bf16 over 50000
+// rows 62 us, of which the sums are 13.
 #include "naju_device.h"
 #include "naju_host.h"
 #include "naju_launch.h"
@@ -94,7 +98,7 @@ __device__ __forceinline__ uint32_t key_of(const int32_t *ids, const uint32_t *k
 // The zero fill of dW needs nothing from the sort, whose kernels leave most of
 // the device idle: each launch of the sort carries workgroups that fill a slice.
 // (16384 x 768 tokens over 50000 rows: 72 us with the fill in front of the
-// sort; the fill alone is 21 us, the sort 27 us.)
+// sort, 62 us beside it; the fill alone is 21 us, the sort 27 us.)
 struct Fill {
     float *p;       // null: nothing to fill
     int64_t n;      // floats of this launch's slice

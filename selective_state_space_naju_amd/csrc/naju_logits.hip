@@ -14,7 +14,8 @@
 // counted there, the tokens that were touched are listed, their values are
 // computed once each into their words, and the dense pass that follows only
 // selects between a word and the logit.  It reads every logit and writes every
-// result once: the bytes bound it.
+// result once.  256 x 131072 bf16 with every constraint: 54 us (3.9 TB/s); the
+// dense pass alone is 35 us, the rest is the lists' latency between barriers.
 #include "naju_device.h"
 #include "naju_host.h"
 #include "naju_launch.h"
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(kLogThreads, 8) void logits_kernel(const LogitsArgs
                 // the record for the next call.  Only the record's own words pass
                 // between workgroups, all by agent-scope atomics, so their order
                 // (the wait) is enough: a release here would write every dirty line
-                // of the L2 back first (243 us against 65 us at 256 x 131072)
+                // of the L2 back first (243 us against 80 us at 256 x 131072)
                 RowBest *rb = (RowBest *)g.ws + b;
                 __hip_atomic_fetch_max(&rb->key, k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                 wait_mem();

@@ -20,6 +20,9 @@
 // products cover 32 consecutive inputs, so a product never spans two groups.
 // The order of the 8 inputs inside a quarter is that of the unpacking; x is
 // staged in LDS in the same order.
+//
+// 4096 -> 131072, groups of 128: one row 53 us (5.2 TB/s of codes), 32 rows
+// 82 us, where unpacking and the LDS reads of x come to more than the codes.
 #include "naju_device.h"
 #include "naju_host.h"
 #include "naju_launch.h"
