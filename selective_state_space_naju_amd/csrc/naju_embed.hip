@@ -84,7 +84,9 @@ static hipError_t launch_embed_fwd(int64_t T, int64_t V, int64_t d, const int32_
 // digits, then every tile ranks its keys (in its own order) behind the smaller
 // digits of all tiles and the equal digits of the tiles before it.
 constexpr int kDigits = 512;  // most values of a digit
-// keys of a tile: 1024 while that leaves a tile few others to look at, else 4096
+// keys of a tile: 1024 while that leaves a tile few others to look at, else 4096 (tiles of 1024
+// and 4096: gradient of 16384 x 768 over 50000 rows 54 and 56 us, of 65536 x 2048 fp32 over
+// 100003 rows 374 and 360 us)
 static int tile_rounds(int64_t T) { return T <= 16384 ? 1 : 4; }
 
 __device__ __forceinline__ uint32_t key_of(const int32_t *ids, const uint32_t *keys, int64_t i,

@@ -329,7 +329,10 @@ naju_status_t naju_logits_process(int64_t rows, int64_t vocab, int32_t io, const
     LogitsArgs g{};
     g.B = rows;
     g.V = vocab;
-    g.tile = rows * ((vocab + kLogTile - 1) / kLogTile) >= 512 ? kLogTile : kLogSmallTile;
+    // small tiles only where large ones leave most CUs idle (2048 tokens of history, large and
+    // small, us: 1 x 32000 8.1 and 6.3, 8 x 50001 8.1 and 7.3, 16 x 131072 9.5 and 12.6,
+    // 256 x 131072 43 and 97)
+    g.tile = rows * ((vocab + kLogTile - 1) / kLogTile) >= 64 ? kLogTile : kLogSmallTile;
     g.n_tiles = (vocab + g.tile - 1) / g.tile;
     g.ld = ld;
     g.history = history;

@@ -396,8 +396,10 @@ static hipError_t launch_w4_t(const W4Args &g, hipStream_t st)
 
 template <int G, bool Z> static hipError_t launch_w4_z(const W4Args &g, hipStream_t st)
 {
-    // few outputs: the waves of a workgroup split the inputs of a tile
-    const bool split = g.N < 16 * 8 * 512;
+    // few outputs: the waves of a workgroup split the inputs of a tile (4096 inputs, split and
+    // not, us: 14336 outputs, one row 9.9 and 15.7, 32 rows 28 and 46; 32000 outputs, one row
+    // 19.1 and 18.0, 32 rows 53 and 48; 131072 outputs, one row 69 and 53, 32 rows 191 and 93)
+    const bool split = g.N < 24576;
     if (g.R <= 4)
         return split ? launch_w4_t<1, 4, G, 4, 1, 4, Z>(g, st)
                      : launch_w4_t<1, 4, G, 1, 1, 4, Z>(g, st);
