@@ -22,7 +22,7 @@
 // staged in LDS in the same order.
 //
 // 4096 -> 131072, groups of 128: one row 53 us (5.2 TB/s of codes), 32 rows
-// 82 us, where unpacking and the LDS reads of x come to more than the codes.
+// 80 us, where unpacking and the LDS reads of x come to more than the codes.
 #include "naju_device.h"
 #include "naju_host.h"
 #include "naju_launch.h"
@@ -211,15 +211,34 @@ __global__ __launch_bounds__(kW4Threads, 4) void w4_kernel(const W4Args g, const
         // stage x[r0 ..][s0 .. s0 + stage), and its sums over the groups; zeros past the inputs
         const int64_t avail = (g.K - s0 + 127) / 128 * 128;
         const int runs = (int)(avail < stage ? avail : stage) / 8;
-        // (rows of 512 inputs are dealt out to the waves, 2 RT of them in flight)
+        // Rows of 512 inputs are dealt out to the waves, F of them in flight.  Where the waves
+        // split the inputs, a stage is most of a call: four rows, and the first scales and zeros
+        // asked for before them (5 x 4100 -> 7001: 13.9 -> 13.0 us; elsewhere the registers cost
+        // more: 16 x 4096 -> 131072 68 -> 72 us).
+        constexpr bool kAhead = WK > 1;
+        constexpr int F = RT == 1 && kAhead ? 4 : 2 * RT;
+        const int g0 = (int)(s0 / G), sets = (runs * 8 / G + 7) / 8;
+        Run<bf16, 8> sv;
+        Run<uint8_t, 8> zv;
+        auto ask = [&](int i) {
+            sv.zero();
+            zv.zero();
+            const int m = i / sets, c = (i - m * sets) * 8;
+            const int64_t at = (n0 + m) * g.ng + g0 + c;
+            if (i < outs * sets && g.ng - g0 - c >= 8) {
+                sv.load(g.scales + at);
+                if (Z) zv.load(g.zeros + at);
+            }
+        };
+        if (kAhead) ask(tid);
         const int64_t left = g.K - s0;
         const int parts = (int)by_rows.d * ((runs + 63) / 64);
         const bf16 *src = g.x + r0 * g.K + s0;
-        for (int p0 = w; p0 < parts; p0 += kW4Waves * 2 * RT) {
-            Run<bf16, 8> v[2 * RT];
-            int m[2 * RT], c[2 * RT];
+        for (int p0 = w; p0 < parts; p0 += kW4Waves * F) {
+            Run<bf16, 8> v[F];
+            int m[F], c[F];
 #pragma unroll
-            for (int i = 0; i < 2 * RT; ++i) {
+            for (int i = 0; i < F; ++i) {
                 const int p = p0 + i * kW4Waves < parts ? p0 + i * kW4Waves : p0;
                 const int cb = (int)fdiv((uint32_t)p, by_rows);
                 m[i] = p - cb * (int)by_rows.d;
@@ -231,7 +250,7 @@ __global__ __launch_bounds__(kW4Threads, 4) void w4_kernel(const W4Args g, const
                 else v[i].zero();
             }
 #pragma unroll
-            for (int i = 0; i < 2 * RT; ++i) {
+            for (int i = 0; i < F; ++i) {
                 if (p0 + i * kW4Waves >= parts) break;  // (uniform)
                 float sum = 0.f;
 #pragma unroll
@@ -250,24 +269,16 @@ __global__ __launch_bounds__(kW4Threads, 4) void w4_kernel(const W4Args g, const
             }
         }
         // the outputs' scales and zeros, 8 groups a thread; none past the last group
-        const int g0 = (int)(s0 / G), sets = (runs * 8 / G + 7) / 8;
         for (int i = tid; i < outs * sets; i += kW4Threads) {
+            if (!kAhead || i != tid) ask(i);
             const int m = i / sets, c = (i - m * sets) * 8;
             const int64_t at = (n0 + m) * g.ng + g0 + c;
             const int left = (int)(g.ng - g0) - c;
-            Run<bf16, 8> v;
-            Run<uint8_t, 8> zv;
-            v.zero();
-            zv.zero();
-            if (left >= 8) {
-                v.load(g.scales + at);
-                if (Z) zv.load(g.zeros + at);
-            }
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 if (c + q >= groups) continue;
                 const bool alone = left < 8 && q < left;
-                sl[(c + q) * NR + m] = alone ? g.scales[at + q] : v.get_raw(q);
+                sl[(c + q) * NR + m] = alone ? g.scales[at + q] : sv.get_raw(q);
                 if (Z)
                     zl[(c + q) * NR + m] =
                         alone ? g.zeros[at + q] : (uint8_t)(zv.w[q / 4] >> (8 * (q % 4)));

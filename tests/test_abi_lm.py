@@ -147,3 +147,18 @@ def test_w4_refusals(lib):
     expect(quant(W=None), nb.EINVAL, "W is NULL")
     assert lin(R=0, x=None, y=None) == nb.OK
     assert quant(K=0, W=None) == nb.OK
+
+
+def test_binding_refuses_tensors_in_host_memory(lib):
+    import torch
+    ids, W = torch.zeros(3, dtype=torch.int32), torch.zeros(5, 8)
+    x, t = torch.zeros(3, 5), torch.zeros(3, 2)
+    t_ids, g = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3)
+    q, s = torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.bfloat16)
+    for call in (lambda: nb.embed_fwd(ids, W), lambda: nb.embed_bwd(ids, torch.zeros(3, 8), 5),
+                 lambda: nb.distill_fwd(x, t_ids, t), lambda: nb.distill_fwd_bwd(x, t_ids, t, g),
+                 lambda: nb.distill_bwd(x, t_ids, t, g, g), lambda: nb.logits_process(x),
+                 lambda: nb.w4_linear(torch.zeros(2, 32, dtype=torch.bfloat16), q, s, 32),
+                 lambda: nb.w4_quantize(W)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
