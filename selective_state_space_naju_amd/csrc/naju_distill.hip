@@ -256,7 +256,7 @@ __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
     __syncthreads();
     const MaxSum ts = join_maxsum<BS / 64>(ent_ms);
     // no valid entry: no loss to descend; weight 0: a row that does not count
-    const bool some = ts.m != kNegInf && gr != 0.f;
+    const bool some = !(ts.s == 0.f) && gr != 0.f;  // (a list of NaN has the sum NaN)
     const float f = some ? gr * tau : 0.f;
     ids[tid] = e.id;
     ps[tid] = e.id >= 0 ? exp_nat(e.t - base_of(ts.m)) / ts.s : 0.f;
@@ -415,7 +415,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
     for (int o = 32; o > 0; o >>= 1) term += __shfl_xor(term, o);
     if (lane == 0) sum[w] = term;
     // the dense part of the gradient: f q_v (a row of -inf alone has q = 0)
-    const bool some = ts.m != kNegInf && gr != 0.f;
+    const bool some = !(ts.s == 0.f) && gr != 0.f;  // (a list of NaN has the sum NaN)
     const float f = some ? gr * tau : 0.f;
     const float fq = m == kNegInf ? 0.f : f / s;
     int c1 = c0;

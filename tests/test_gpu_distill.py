@@ -198,6 +198,17 @@ def test_distill_nan_stays_in_its_row():
     assert not nb.distill_bwd(x, ids, t, lse, g)[1:].any()
 
 
+def test_distill_a_list_of_nan_reaches_loss_and_gradient():
+    x = torch.randn(2, 4000, device=dev())
+    ids, one = i32([[5, 77], [9, -1]]), torch.ones(2, device=dev())
+    t = torch.tensor([[float("nan")] * 2, [0.5, 0.0]], device=dev())
+    loss, grad = nb.distill_fwd_bwd(x, ids, t, one)
+    _, lse = nb.distill_fwd(x, ids, t)
+    for d in (grad, nb.distill_bwd(x, ids, t, lse, one)):
+        assert torch.isnan(d[0, [5, 77]]).all() and torch.isfinite(d[1]).all()
+    assert torch.isnan(loss[0]) and torch.isfinite(loss[1])
+
+
 def test_distill_gradient_against_differences():
     """Central differences of the device's own loss, fp32 logits: the quotient's error is the
     loss error (below 1e-6 here) over 2 eps, plus the third derivative times eps^2 / 6."""
