@@ -368,7 +368,10 @@ naju_status_t naju_embed_bwd(int64_t tokens, int64_t vocab, int64_t d_model, int
  *   logits    [rows][ld] io, the first vocab of every row's ld >= vocab elements
  *   t_ids     [rows][k] int32;  t_logits [rows][k] fp32;  k <= 512
  *   temperature  > 0, finite
- *   loss, lse [rows] fp32 (written)
+ *   loss, lse [rows] fp32 (written); lse is infinite where it leaves fp32 (a row of
+ *             nothing but fp32's lowest value at temperatures below 1)
+ * Finite logits and teacher values may lie anywhere in their types' ranges: a
+ * maximum is taken off before a difference is scaled.
  * rows, vocab <= 2^30.
  */
 naju_status_t naju_distill_fwd(int64_t rows, int64_t vocab, int64_t k, int32_t io,
@@ -380,7 +383,9 @@ naju_status_t naju_distill_fwd(int64_t rows, int64_t vocab, int64_t k, int32_t i
  * Its gradient for the upstream gradient g of each row's loss:
  *     dlogits_v = g tau ([any valid entry] exp(x_v - lse) - sum_{j : i_j = v} p_j)
  * A row with g == 0 gets zeros, whatever it holds.
- *   lse       [rows] fp32 from naju_distill_fwd on the same inputs
+ *   lse       [rows] fp32 from naju_distill_fwd on the same inputs (where it is
+ *             larger than 16384, too coarse to form exp(x_v - lse) from, it is formed
+ *             again from the row)
  *   g         [rows] fp32
  *   dlogits   [rows][ld_d] io: the first vocab elements of every row are written,
  *             the others are not touched

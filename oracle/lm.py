@@ -36,7 +36,8 @@ def distill(logits, t_ids, t_logits, tau, g=None):
         for r in range(R):
             x = np.asarray(logits[r], dtype=np.float64) / tau
             top = x.max() if np.isfinite(x.max()) else 0.0
-            lse[r] = top + np.log(np.exp(x - top).sum())
+            log_sum = np.log(np.exp(x - top).sum())
+            lse[r] = top + log_sum
             use = [j for j, i in enumerate(t_ids[r]) if 0 <= i < V and t_logits[r, j] != -np.inf]
             if not use:
                 continue
@@ -45,7 +46,8 @@ def distill(logits, t_ids, t_logits, tau, g=None):
             e = np.exp(t - t.max())
             p = e / e.sum()
             logp = t - t.max() - np.log(e.sum())
-            logq = np.where(x == -np.inf, -np.inf, x - lse[r])
+            # (x - lse would lose the sum's logarithm where the logits are huge)
+            logq = np.where(x == -np.inf, -np.inf, x - top - log_sum)
             terms = np.where(p == 0, 0.0, p * (logp - logq[idx]))
             loss[r] = tau * tau * terms.sum()
             if g is not None and g[r] != 0:

@@ -29,45 +29,48 @@ constexpr int kMostEntries = 512;  // entries of a row: one per thread of a larg
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLn2 = 0.6931471805599453f;
 
-// running maximum and sum of exp(. - maximum)
+// Maximum of some logits, and the sum of exp((. - maximum) / tau) over them.
+// The maximum is kept as it was read and taken off before the difference is
+// scaled: scaled by itself, a logit near the type's lowest or largest value
+// would leave fp32's range.  c2 = log2(e) / tau.
 struct MaxSum {
     float m, s;
 };
 
 __device__ __forceinline__ float exp_nat(float d) { return ex2(d * kLog2e); }
-// the exponent base of a row or list without any finite value is 0, not -inf
+// what is taken off where there is no value above -inf is 0, not -inf
 __device__ __forceinline__ float base_of(float m) { return m == kNegInf ? 0.f : m; }
 
-__device__ __forceinline__ MaxSum wave_maxsum(MaxSum a)
+__device__ __forceinline__ MaxSum wave_maxsum(MaxSum a, float c2)
 {
     float M = a.m;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor(M, o));
-    float s = a.s * exp_nat(a.m - base_of(M));
+    float s = a.s * ex2((a.m - base_of(M)) * c2);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
     return {M, s};
 }
 
-template <int kWaves> __device__ __forceinline__ MaxSum join_maxsum(const MaxSum *w)
+template <int kWaves> __device__ __forceinline__ MaxSum join_maxsum(const MaxSum *w, float c2)
 {
     float M = w[0].m;
 #pragma unroll
     for (int i = 1; i < kWaves; ++i) M = fmaxf(M, w[i].m);
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) s += w[i].s * exp_nat(w[i].m - base_of(M));
+    for (int i = 0; i < kWaves; ++i) s += w[i].s * ex2((w[i].m - base_of(M)) * c2);
     return {M, s};
 }
 
 // One teacher entry per thread.
 struct Entry {
     int id;      // -1: not valid
-    float t;     // t / tau, -inf if not valid
+    float t;     // -inf if not valid
 };
 
 __device__ __forceinline__ Entry load_entry(const int32_t *t_ids, const float *t_logits, int k,
-                                            int64_t V, float inv_tau)
+                                            int64_t V)
 {
     Entry e{-1, kNegInf};
     if ((int)threadIdx.x < k) {
@@ -75,14 +78,15 @@ __device__ __forceinline__ Entry load_entry(const int32_t *t_ids, const float *t
         const float t = t_logits[threadIdx.x];
         if (id >= 0 && id < V && t != kNegInf) {
             e.id = id;
-            e.t = t * inv_tau;
+            e.t = t;
         }
     }
     return e;
 }
-__device__ __forceinline__ MaxSum entry_maxsum(const Entry &e)
+__device__ __forceinline__ MaxSum entry_maxsum(const Entry &e, float c2)
 {
-    return wave_maxsum({e.t, e.id >= 0 ? exp_nat(e.t - base_of(e.t)) : 0.f});
+    // (1, or NaN for an infinite or NaN entry)
+    return wave_maxsum({e.t, e.id >= 0 ? ex2((e.t - base_of(e.t)) * c2) : 0.f}, c2);
 }
 
 // elements between p and the 16-byte boundary before it
@@ -97,9 +101,9 @@ template <> __device__ __forceinline__ bf16 neg_inf_raw<bf16>() { return 0xff80;
 
 // ------------------------------------------------------------------ loss
 // Reads the row once, kLossRuns accesses per thread in flight, with a running
-// maximum and sum per thread in base 2.  Accesses start at a 16-byte boundary;
-// one that would leave the row is moved inside it, and what it holds of its
-// neighbours is taken for -inf.
+// maximum and sum per thread.  Accesses start at a 16-byte boundary; one that
+// would leave the row is moved inside it, and what it holds of its neighbours is
+// taken for -inf.
 constexpr int kLossRuns = 4;
 
 template <typename IO, int BS>
@@ -116,9 +120,9 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
     const float c2 = inv_tau * kLog2e;
     for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
         const IO *row = logits + r * ld;
-        const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
+        const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V);
         const float at = e.id >= 0 ? to_f(row[e.id]) : 0.f;
-        float m = kNegInf, s = 0.f;  // of x in base 2
+        float m = kNegInf, s = 0.f;
         if (V >= n) {
             for (int64_t c0 = -past_boundary(row); c0 < V; c0 += per) {
                 Run<IO, n> v[kLossRuns];
@@ -137,7 +141,7 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
                             if (in + j < c || in + j >= c + n) v[i].set_raw(j, neg_inf_raw<IO>());
                     }
                 }
-                float top = kNegInf;
+                float top = m;
 #pragma unroll
                 for (int i = 0; i < kLossRuns; ++i) {
                     if (c0 + i * (BS * n) < V) {
@@ -145,51 +149,38 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
                         for (int j = 0; j < n; ++j) top = fmaxf(top, v[i].get(j));
                     }
                 }
-                top = fmaxf(m, top * c2);
                 const float b = base_of(top);
-                s *= ex2(m - b);
+                s *= ex2((m - b) * c2);
                 m = top;
 #pragma unroll
                 for (int i = 0; i < kLossRuns; ++i) {
                     if (c0 + i * (BS * n) < V) {
                         v[i].repack();
 #pragma unroll
-                        for (int j = 0; j < n; ++j) s += ex2(fmaf(v[i].get(j), c2, -b));
+                        for (int j = 0; j < n; ++j) s += ex2((v[i].get(j) - b) * c2);
                     }
                 }
             }
         } else if (tid < V) {  // (shorter than an access)
-            m = to_f(row[tid]) * c2;
+            m = to_f(row[tid]);
             s = m == kNegInf ? 0.f : fabsf(m) < -kNegInf ? 1.f : __builtin_nanf("");
         }
-        // over the wave, then over the workgroup
-        float top = m;
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-        s *= ex2(m - base_of(top));
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-        const MaxSum es = entry_maxsum(e);
+        const MaxSum rs = wave_maxsum({m, s}, c2);
+        const MaxSum es = entry_maxsum(e, c2);
         if (lane == 0) {
-            row_ms[w] = {top, s};
+            row_ms[w] = rs;
             ent_ms[w] = es;
         }
         __syncthreads();
-        const MaxSum ts = join_maxsum<BS / 64>(ent_ms);
-        m = row_ms[0].m;
-#pragma unroll
-        for (int i = 1; i < BS / 64; ++i) m = fmaxf(m, row_ms[i].m);
-        const float b = base_of(m);
-        s = 0.f;
-#pragma unroll
-        for (int i = 0; i < BS / 64; ++i) s += row_ms[i].s * ex2(row_ms[i].m - b);
-        const float log2_s = log2f(s);
+        const MaxSum ts = join_maxsum<BS / 64>(ent_ms, c2), row_s = join_maxsum<BS / 64>(row_ms, c2);
+        const float b = base_of(row_s.m), log2_s = log2f(row_s.s);
         float term = 0.f;
         if (e.id >= 0) {
-            const float gap = e.t - base_of(ts.m);
-            const float p = exp_nat(gap) / ts.s;
-            const float logq = at == kNegInf ? kNegInf : (fmaf(at, c2, -b) - log2_s) * kLn2;
-            if (!(p == 0.f)) term = p * ((gap - logf(ts.s)) - logq);  // 0 log 0 = 0; NaN goes on
+            const float gap = (e.t - base_of(ts.m)) * c2;  // (in base 2, as log2 q)
+            const float p = ex2(gap) / ts.s;
+            const float log2_q = at == kNegInf ? kNegInf : (at - b) * c2 - log2_s;
+            // 0 log 0 = 0; NaN goes on
+            if (!(p == 0.f)) term = p * (((gap - log2f(ts.s)) - log2_q) * kLn2);
         }
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) term += __shfl_xor(term, o);
@@ -199,7 +190,7 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
             float t = 0.f;
             for (int i = 0; i < BS / 64; ++i) t += sum[i];
             loss[r] = tau * tau * t;
-            lse[r] = m == kNegInf ? kNegInf : (m + log2_s) * kLn2;
+            lse[r] = row_s.m == kNegInf ? kNegInf : fmaf(b, inv_tau, log2_s * kLn2);
         }
         // (the next row writes row_ms and ent_ms: every thread has read them by now)
     }
@@ -212,6 +203,12 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
 // the first entry that names each.  The accesses are laid out from a 16-byte
 // boundary of the gradient's row at or before its start (rows of an odd
 // vocabulary start anywhere).
+//
+// q_v is exp(x_v - lse), with the rounding of lse in it: |lse| 2^-24 relative,
+// up to kFineLse a quarter of a bf16 rounding.  A row beyond it (logits near the
+// type's lowest or largest value have no usable lse at all) has its maximum and
+// sum formed again, by every workgroup of the row.
+constexpr float kFineLse = 16384.f;
 
 template <typename IO, int NV, int BS>
 __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
@@ -222,10 +219,11 @@ __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
 {
     constexpr int n = kPer16<IO>;
     constexpr int chunk = BS * n * NV;
-    __shared__ MaxSum ent_ms[BS / 64];
+    __shared__ MaxSum row_ms[BS / 64], ent_ms[BS / 64];
     __shared__ int ids[BS];
     __shared__ float ps[BS];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const float c2 = inv_tau * kLog2e;
     const int64_t r = blockIdx.x / (unsigned)n_chunks;
     const int part = (int)(blockIdx.x - (unsigned)r * (unsigned)n_chunks);
     const IO *row = logits + r * ld;
@@ -235,7 +233,7 @@ __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
     const int64_t c0 = (int64_t)part * chunk - past_boundary(out);
     const bool is_last = part == n_chunks - 1;
     const int64_t lo = c0 > 0 ? c0 : 0, hi = is_last ? V : c0 + chunk;
-    const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
+    const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V);
     const float L = lse[r], gr = g[r];
     Run<IO, n> v[NV];
     if (V >= n) {
@@ -251,46 +249,67 @@ __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
     }
     const bool mine = e.id >= lo && e.id < hi;
     const float at = mine ? to_f(row[e.id]) : 0.f;
-    const MaxSum es = entry_maxsum(e);
+    const MaxSum es = entry_maxsum(e, c2);
     if (lane == 0) ent_ms[w] = es;
     __syncthreads();
-    const MaxSum ts = join_maxsum<BS / 64>(ent_ms);
+    const MaxSum ts = join_maxsum<BS / 64>(ent_ms, c2);
     // no valid entry: no loss to descend; weight 0: a row that does not count
     const bool some = !(ts.s == 0.f) && gr != 0.f;  // (a list of NaN has the sum NaN)
     const float f = some ? gr * tau : 0.f;
     ids[tid] = e.id;
-    ps[tid] = e.id >= 0 ? exp_nat(e.t - base_of(ts.m)) / ts.s : 0.f;
-    const float fq = L == kNegInf ? 0.f : f, base = L == kNegInf ? 0.f : L;
-    auto dense = [&](float s) { return fq * exp_nat(fmaf(s, inv_tau, -base)); };
-    if (V >= n) {
-        IO *out_c0 = out + c0;
-        const int64_t left = V - c0;  // elements from c0 to the row's end
+    ps[tid] = e.id >= 0 ? ex2((e.t - base_of(ts.m)) * c2) / ts.s : 0.f;
+    float dense_at;  // the dense part at this thread's entry
+    if (fabsf(L) <= kFineLse || L != L) {
+        auto dense = [&](float x) { return f * exp_nat(fmaf(x, inv_tau, -L)); };
+        if (V >= n) {
+            IO *out_c0 = out + c0;
+            const int64_t left = V - c0;  // elements from c0 to the row's end
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * BS + tid) * n;
-            float d[n];
+            for (int i = 0; i < NV; ++i) {
+                const int c = (i * BS + tid) * n;
+                float d[n];
 #pragma unroll
-            for (int j = 0; j < n; ++j) d[j] = dense(v[i].get(j));
-            Run<IO, n> o = round_run<IO, n>(d);
-            if (!some) o.zero();
-            if (c0 + c >= 0 && c + n <= left) {
-                o.store(out_c0 + c);
-            } else if (c0 + c > -n && c < left) {
-                // the row's first or last access, moved inside it: its own elements
-                const int in = c0 + c < 0 ? (int)-c0 : (int)(left - n);
+                for (int j = 0; j < n; ++j) d[j] = dense(v[i].get(j));
+                Run<IO, n> o = round_run<IO, n>(d);
+                if (!some) o.zero();
+                if (c0 + c >= 0 && c + n <= left) {
+                    o.store(out_c0 + c);
+                } else if (c0 + c > -n && c < left) {
+                    // the row's first or last access, moved inside it: its own elements
+                    const int in = c0 + c < 0 ? (int)-c0 : (int)(left - n);
 #pragma unroll
-                for (int j = 0; j < n; ++j)
-                    if (in + j >= c && in + j < c + n) out_c0[in + j] = o.get_raw(j);
+                    for (int j = 0; j < n; ++j)
+                        if (in + j >= c && in + j < c + n) out_c0[in + j] = o.get_raw(j);
+                }
             }
+            const int64_t rest = c0 + chunk + tid;
+            if (is_last && tid < n && rest < V) {
+                const float d = dense(to_f(row[rest]));
+                out[rest] = from_f<IO>(some ? d : 0.f);
+            }
+        } else if (tid < V) {  // (shorter than an access)
+            const float d = dense(to_f(row[tid]));
+            out[tid] = from_f<IO>(some ? d : 0.f);
         }
-        const int64_t rest = c0 + chunk + tid;
-        if (is_last && tid < n && rest < V) {
-            const float d = dense(to_f(row[rest]));
-            out[rest] = from_f<IO>(some ? d : 0.f);
+        dense_at = dense(at);
+    } else {  // (uniform)
+        MaxSum rs{kNegInf, 0.f};
+#pragma unroll 1
+        for (uint32_t c = tid; c < (uint32_t)V; c += BS) rs.m = fmaxf(rs.m, to_f(row[c]));
+#pragma unroll 1
+        for (uint32_t c = tid; c < (uint32_t)V; c += BS) rs.s += ex2((to_f(row[c]) - base_of(rs.m)) * c2);
+        rs = wave_maxsum(rs, c2);
+        if (lane == 0) row_ms[w] = rs;
+        __syncthreads();
+        rs = join_maxsum<BS / 64>(row_ms, c2);
+        const float base = base_of(rs.m), fq = rs.m == kNegInf ? 0.f : f / rs.s;
+        auto dense = [&](float x) { return fq * ex2((x - base) * c2); };
+#pragma unroll 1
+        for (uint32_t c = (uint32_t)lo + tid; c < (uint32_t)hi; c += BS) {
+            const float d = dense(to_f(row[c]));
+            out[c] = from_f<IO>(some ? d : 0.f);
         }
-    } else if (tid < V) {  // (shorter than an access)
-        const float d = dense(to_f(row[tid]));
-        out[tid] = from_f<IO>(some ? d : 0.f);
+        dense_at = dense(at);
     }
     // the dense stores are done before an element is written again
     wait_mem();
@@ -303,19 +322,35 @@ __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
                 first = first && j >= tid;
                 p += ps[j];
             }
-        if (first) out[e.id] = from_f<IO>(dense(at) - f * p);
+        if (first) out[e.id] = from_f<IO>(dense_at - f * p);
     }
 }
 
 // ------------------------------------------------- loss and gradient at once
 // The row stays in registers between its statistics and its gradient, NV
 // accesses per thread: every logit is read once and every gradient written
-// once.  Exponents are formed in base 2 with the maximum of the wave, so one
-// barrier joins the row's and the list's statistics; q is exp2(x - m) over the
-// row's sum, with no rounded lse in between.  Places past the row hold -inf,
-// which adds nothing.
-
+// once.  Exponents are formed with the maximum of the wave, so one barrier joins
+// the row's and the list's statistics; q is exp((s - m) / tau) over the row's
+// sum, with no rounded lse in between.  Places past the row hold -inf, which
+// adds nothing.
 //
+// (s - m) c2 is formed as one multiply-add, s c - b with b = m c rounded; what
+// that rounding took, m c - b, is the same for every logit and comes off the sum.
+// (Subtracted first, an operation more per logit, 8192 x 50001 bf16 takes 413 us
+// in place of 400.)  c is c2 unless m c2 would pass 2^30, or fp32's range: there it
+// is made smaller.  Numbers of that size lie 64 or more apart in units of 1 / c,
+// so either way all but the largest weigh nothing, and b's rounding, up to 64,
+// leaves the exponential in range.
+struct Exponent {
+    float m, c, b, rest;
+    __device__ __forceinline__ Exponent(float max, float c2)
+        : m(base_of(max)), c(fabsf(m) * c2 <= 0x1p30f ? c2 : 0x1p30f / fabsf(m)), b(m * c),
+          rest(fmaf(m, c, -b))
+    {
+    }
+    __device__ __forceinline__ float operator()(float s) const { return fmaf(s, c, -b); }
+};
+
 // The waves per SIMD that the launch bounds ask for keep the row's packed words
 // (4 NV registers) and little else live, so that several workgroups share a CU
 // and one loads while another computes.
@@ -337,7 +372,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
     const int64_t r = blockIdx.x;
     const IO *row = logits + r * ld;
     IO *out = dlogits + r * ldd;
-    const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V, inv_tau);
+    const Entry e = load_entry(t_ids + r * k, t_logits + r * k, k, V);
     const float gr = g[r];
     // accesses from the 16-byte boundary `before` elements ahead of the gradient's row, moved
     // into the row at its ends: no load waits on a branch
@@ -351,7 +386,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
         v[i].load_at(row, (uint32_t)in * (uint32_t)sizeof(IO));
     }
     const float at = e.id >= 0 ? to_f(row[e.id]) : 0.f;
-    const MaxSum es = entry_maxsum(e);
+    const MaxSum es = entry_maxsum(e, c2);
     // what a moved access holds of its neighbours is taken for -inf
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -363,7 +398,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
                 if (in + j < c || in + j >= c + n) v[i].set_raw(j, neg_inf_raw<IO>());
         }
     }
-    // the row, in base 2: maximum of the wave, sum of exp2(x - maximum)
+    // maximum of the wave, sum of exp((. - maximum) / tau)
     float top = kNegInf;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -374,40 +409,36 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-    const float m_wave = base_of(top) * c2;
+    const Exponent xw(top, c2);
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (i * per < V + before) {
             v[i].repack();
 #pragma unroll
-            for (int j = 0; j < n; ++j) s += ex2(fmaf(v[i].get(j), c2, -m_wave));
+            for (int j = 0; j < n; ++j) s += ex2(xw(v[i].get(j)));
             v[i].repack();
         }
     }
+    s *= ex2(-xw.rest);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
     if (lane == 0) {
-        row_ms[w] = {top == kNegInf ? kNegInf : m_wave, s};
+        row_ms[w] = {top, s};
         ent_ms[w] = es;
     }
     __syncthreads();
-    const MaxSum ts = join_maxsum<BS / 64>(ent_ms);
-    float m = row_ms[0].m;
-#pragma unroll
-    for (int i = 1; i < (BS / 64); ++i) m = fmaxf(m, row_ms[i].m);
-    const float b = base_of(m);
-    s = 0.f;
-#pragma unroll
-    for (int i = 0; i < (BS / 64); ++i) s += row_ms[i].s * ex2(row_ms[i].m - b);
+    const MaxSum ts = join_maxsum<BS / 64>(ent_ms, c2), row_s = join_maxsum<BS / 64>(row_ms, c2);
+    const float m = row_s.m;
+    const Exponent xr(m, c2);
     // the entries: their probabilities and their terms of the loss
-    const float log2_s = log2f(s), log_t = logf(ts.s);
+    const float log2_s = log2f(row_s.s), log2_t = log2f(ts.s);
     float p = 0.f, term = 0.f;
     if (e.id >= 0) {
-        const float gap = e.t - base_of(ts.m);
-        p = exp_nat(gap) / ts.s;
-        const float logq = at == kNegInf ? kNegInf : (fmaf(at, c2, -b) - log2_s) * kLn2;
-        if (!(p == 0.f)) term = p * ((gap - log_t) - logq);
+        const float gap = (e.t - base_of(ts.m)) * c2;  // (in base 2, as log2 q)
+        p = ex2(gap) / ts.s;
+        const float log2_q = at == kNegInf ? kNegInf : (at - xr.m) * c2 - log2_s;
+        if (!(p == 0.f)) term = p * (((gap - log2_t) - log2_q) * kLn2);
     }
     ids[tid] = e.id;
     ps[tid] = p;
@@ -417,7 +448,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
     // the dense part of the gradient: f q_v (a row of -inf alone has q = 0)
     const bool some = !(ts.s == 0.f) && gr != 0.f;  // (a list of NaN has the sum NaN)
     const float f = some ? gr * tau : 0.f;
-    const float fq = m == kNegInf ? 0.f : f / s;
+    const float fq = m == kNegInf ? 0.f : f / row_s.s * ex2(-xr.rest);
     int c1 = c0;
     asm volatile("" : "+v"(c1));  // (offsets formed anew, not kept since the loads)
 #pragma unroll
@@ -426,7 +457,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
             const int c = i * (int)per + c1;
             float d[n];
 #pragma unroll
-            for (int j = 0; j < n; ++j) d[j] = fq * ex2(fmaf(v[i].get(j), c2, -b));
+            for (int j = 0; j < n; ++j) d[j] = fq * ex2(xr(v[i].get(j)));
             Run<IO, n> o = round_run<IO, n>(d);
             if (!some) o.zero();
             if (c >= 0 && c <= last) {
@@ -446,7 +477,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
         float t = 0.f;
         for (int i = 0; i < (BS / 64); ++i) t += sum[i];
         loss[r] = tau * tau * t;
-        lse[r] = m == kNegInf ? kNegInf : (m + log2_s) * kLn2;
+        lse[r] = m == kNegInf ? kNegInf : fmaf(m, inv_tau, log2_s * kLn2);
     }
     if (some && e.id >= 0) {
         float all = 0.f;
@@ -457,7 +488,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
                 all += ps[j];
             }
         if (first) {
-            const float q = m == kNegInf ? 0.f : ex2(fmaf(at, c2, -b)) / s;
+            const float q = m == kNegInf ? 0.f : ex2((at - xr.m) * c2) / row_s.s;
             out[e.id] = from_f<IO>(f * (q - all));
         }
     }

@@ -1,0 +1,14 @@
+"""Pins of oracle/lm.py's distillation at the ends of the logits' range and for rows of NaN."""
+import numpy as np
+
+from oracle import lm
+
+
+def test_distill_of_a_row_of_one_value_is_uniform_whatever_the_value():
+    ids, t = np.array([[3, 4]]), np.zeros((1, 2))
+    for v in (0.0, 5.0, float(np.finfo(np.float32).min), float(np.finfo(np.float32).max)):
+        loss, _, grad = lm.distill(np.full((1, 10), v), ids, t, 1.0, np.ones(1))
+        assert np.isclose(loss[0], np.log(5.0))  # log(1/2) - log(1/10)
+        want = np.full(10, 0.1)
+        want[[3, 4]] -= 0.5
+        assert np.allclose(grad[0], want)
