@@ -47,7 +47,9 @@ def distill(logits, t_ids, t_logits, tau, g=None):
             p = e / e.sum()
             logp = t - t.max() - np.log(e.sum())
             # (x - lse would lose the sum's logarithm where the logits are huge)
-            logq = np.where(x == -np.inf, -np.inf, x - top - log_sum)
+            logq = x - top - log_sum
+            if not np.isnan(log_sum):  # (NaN makes the whole row NaN)
+                logq[x == -np.inf] = -np.inf
             terms = np.where(p == 0, 0.0, p * (logp - logq[idx]))
             loss[r] = tau * tau * terms.sum()
             if g is not None and g[r] != 0:

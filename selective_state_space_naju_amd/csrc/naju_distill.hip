@@ -32,7 +32,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Maximum of some logits, and the sum of exp((. - maximum) / tau) over them.
 // The maximum is kept as it was read and taken off before the difference is
 // scaled: scaled by itself, a logit near the type's lowest or largest value
-// would leave fp32's range.  c2 = log2(e) / tau.
+// would leave fp32's range.  c2 = log2(e) / tau.  The maximum passes NaN over, the
+// sum does not: a row of -inf alone is the one whose sum is 0, and a row with NaN
+// has the sum NaN, whatever its maximum.
 struct MaxSum {
     float m, s;
 };
@@ -178,7 +180,8 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
         if (e.id >= 0) {
             const float gap = (e.t - base_of(ts.m)) * c2;  // (in base 2, as log2 q)
             const float p = ex2(gap) / ts.s;
-            const float log2_q = at == kNegInf ? kNegInf : (at - b) * c2 - log2_s;
+            const float log2_q =
+                at == kNegInf && log2_s == log2_s ? kNegInf : (at - b) * c2 - log2_s;
             // 0 log 0 = 0; NaN goes on
             if (!(p == 0.f)) term = p * (((gap - log2f(ts.s)) - log2_q) * kLn2);
         }
@@ -190,7 +193,7 @@ __global__ __launch_bounds__(BS) void distill_loss_kernel(
             float t = 0.f;
             for (int i = 0; i < BS / 64; ++i) t += sum[i];
             loss[r] = tau * tau * t;
-            lse[r] = row_s.m == kNegInf ? kNegInf : fmaf(b, inv_tau, log2_s * kLn2);
+            lse[r] = fmaf(b, inv_tau, log2_s * kLn2);
         }
         // (the next row writes row_ms and ent_ms: every thread has read them by now)
     }
@@ -302,7 +305,7 @@ __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
         if (lane == 0) row_ms[w] = rs;
         __syncthreads();
         rs = join_maxsum<BS / 64>(row_ms, c2);
-        const float base = base_of(rs.m), fq = rs.m == kNegInf ? 0.f : f / rs.s;
+        const float base = base_of(rs.m), fq = rs.s == 0.f ? 0.f : f / rs.s;
         auto dense = [&](float x) { return fq * ex2((x - base) * c2); };
 #pragma unroll 1
         for (uint32_t c = (uint32_t)lo + tid; c < (uint32_t)hi; c += BS) {
@@ -429,15 +432,15 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
     }
     __syncthreads();
     const MaxSum ts = join_maxsum<BS / 64>(ent_ms, c2), row_s = join_maxsum<BS / 64>(row_ms, c2);
-    const float m = row_s.m;
-    const Exponent xr(m, c2);
+    const Exponent xr(row_s.m, c2);
     // the entries: their probabilities and their terms of the loss
     const float log2_s = log2f(row_s.s), log2_t = log2f(ts.s);
     float p = 0.f, term = 0.f;
     if (e.id >= 0) {
         const float gap = (e.t - base_of(ts.m)) * c2;  // (in base 2, as log2 q)
         p = ex2(gap) / ts.s;
-        const float log2_q = at == kNegInf ? kNegInf : (at - xr.m) * c2 - log2_s;
+        const float log2_q =
+            at == kNegInf && log2_s == log2_s ? kNegInf : (at - xr.m) * c2 - log2_s;
         if (!(p == 0.f)) term = p * (((gap - log2_t) - log2_q) * kLn2);
     }
     ids[tid] = e.id;
@@ -448,7 +451,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
     // the dense part of the gradient: f q_v (a row of -inf alone has q = 0)
     const bool some = !(ts.s == 0.f) && gr != 0.f;  // (a list of NaN has the sum NaN)
     const float f = some ? gr * tau : 0.f;
-    const float fq = m == kNegInf ? 0.f : f / row_s.s * ex2(-xr.rest);
+    const float fq = row_s.s == 0.f ? 0.f : f / row_s.s * ex2(-xr.rest);
     int c1 = c0;
     asm volatile("" : "+v"(c1));  // (offsets formed anew, not kept since the loads)
 #pragma unroll
@@ -477,7 +480,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
         float t = 0.f;
         for (int i = 0; i < (BS / 64); ++i) t += sum[i];
         loss[r] = tau * tau * t;
-        lse[r] = m == kNegInf ? kNegInf : fmaf(m, inv_tau, log2_s * kLn2);
+        lse[r] = fmaf(xr.m, inv_tau, log2_s * kLn2);
     }
     if (some && e.id >= 0) {
         float all = 0.f;
@@ -488,7 +491,7 @@ __global__ __launch_bounds__(BS, NV <= 8 ? 6 : NV <= 16 ? 4 : 2) void distill_st
                 all += ps[j];
             }
         if (first) {
-            const float q = m == kNegInf ? 0.f : ex2((at - xr.m) * c2) / row_s.s;
+            const float q = row_s.s == 0.f ? 0.f : ex2((at - xr.m) * c2) / row_s.s;
             out[e.id] = from_f<IO>(f * (q - all));
         }
     }
