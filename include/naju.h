@@ -367,7 +367,7 @@ naju_status_t naju_embed_bwd(int64_t tokens, int64_t vocab, int64_t d_model, int
  * and tau == 1 the loss is the cross entropy of a hard label.  No workspace.
  *   logits    [rows][ld] io, the first vocab of every row's ld >= vocab elements
  *   t_ids     [rows][k] int32;  t_logits [rows][k] fp32;  k <= 512
- *   temperature  > 0, finite
+ *   temperature  > 0, finite, with a finite reciprocal (5e-39 and more)
  *   loss, lse [rows] fp32 (written); lse is infinite where it leaves fp32 (a row of
  *             nothing but fp32's lowest value at temperatures below 1)
  * Finite logits and teacher values may lie anywhere in their types' ranges: a

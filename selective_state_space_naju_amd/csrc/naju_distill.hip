@@ -614,6 +614,9 @@ static naju_status_t check_distill(int64_t R, int64_t V, int64_t k, int32_t io, 
                     kMostEntries);
     if (!(tau > 0.f) || !(tau < __builtin_huge_valf()))
         return fail(NAJU_EINVAL, "temperature must be positive and finite");
+    // (exponents are scaled by it, and 0 times infinity would be NaN)
+    if (!(1.f / tau * kLog2e < __builtin_huge_valf()))
+        return fail(NAJU_EINVAL, "temperature is too small for its reciprocal");
     if (R == 0 || V == 0) return NAJU_OK;
     if (ld < V) return fail(NAJU_EINVAL, "row stride of logits %lld is less than vocab %lld",
                             (long long)ld, (long long)V);
