@@ -522,7 +522,9 @@ def embed_fwd(ids, W, scale=1.0):
 
 def embed_bwd(ids, dout, vocab, scale=1.0, *, dW=None, ws=None):
     """dW = naju_embed_bwd(ids, dout, vocab, scale), fp32 [vocab, d_model].  With dW given the
-    gradient is added to it (rows of tokens that do not occur are not touched)."""
+    gradient is added to it (rows of tokens that do not occur are not touched).  Without ws
+    every call takes scratch of its own from torch's allocator: token counts vary from batch to
+    batch, and calls from several host threads must not sort in one another's lists."""
     d = dout.shape[-1]
     dt, dev = dout.dtype, dout.device
     io, st = _io_of(dout), _stream(dev)
@@ -533,11 +535,13 @@ def embed_bwd(ids, dout, vocab, scale=1.0, *, dW=None, ws=None):
     if dW is None:
         dW = torch.empty((vocab, d), dtype=torch.float32, device=dev)
     T = ids.numel()
-    ws = ws or _cached_workspace(
-        "embed_bwd", (T, vocab, d),
-        lambda: lib().naju_embed_bwd_workspace_bytes(T, vocab, d), dev, st)
+    if ws is None:
+        nbytes = lib().naju_embed_bwd_workspace_bytes(T, vocab, d)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        nbytes, scratch = ws.nbytes, ws.tensor
     check(lib().naju_embed_bwd(T, vocab, d, io, _p(ids), _p(dout), float(scale),
-                               int(accumulate), _p(dW), ws.tensor.data_ptr(), ws.nbytes, st))
+                               int(accumulate), _p(dW), _p(scratch), nbytes, st))
     return dW
 
 
