@@ -497,12 +497,21 @@ def mixer_bwd(xn, W_u, W_z, conv_w, W_a, a_bias, W_b, b_bias, W_B, W_C, D, W_out
 
 
 # ------------------------------------------------- around the mixer layer
-def _cached_workspace(kind, sizes, nbytes, dev, stream) -> Workspace:
-    """Cached workspace per (device, stream, kind, sizes); nbytes() is asked once."""
-    key = (dev.index, stream, kind) + sizes
-    ws = _ws_cache.get(key)
-    if ws is None:
-        ws = _ws_cache[key] = Workspace(nbytes(), dev)
+def _logits_records(R, dev, stream) -> Workspace:
+    """naju_logits_process's zero-filled records of R rows.  Calls leave them zero, so one buffer
+    per stream serves them all and is replaced by a larger one as rows grow (the allocator hands
+    the old one out in stream order).  A call under graph capture has records of its own, with
+    their fill in the graph: replays come in any order, and on any stream."""
+    if torch.cuda.is_current_stream_capturing():
+        return Workspace(lib().naju_logits_workspace_bytes(R), dev)
+    key = (dev.index, stream, "logits")
+    rows, ws = _ws_cache.get(key, (-1, None))
+    if R > rows:
+        rows = 1 << max(8, (R - 1).bit_length())
+        nbytes = lib().naju_logits_workspace_bytes(rows)
+        ws = Workspace(nbytes, dev)
+        if nbytes > 0:  # (else the call refuses that many rows)
+            _ws_cache[key] = (rows, ws)
     return ws
 
 
@@ -649,8 +658,7 @@ def logits_process(logits, history=None, lengths=None, repetition=None, presence
     _opt(mask, "mask", (R, (V + 31) // 32), torch.int32, dev)
     out = torch.empty((R, V), dtype=torch.float32, device=dev)
     best = torch.empty((R,), dtype=torch.int32, device=dev)
-    ws = ws or _cached_workspace("logits", (R,),
-                                 lambda: lib().naju_logits_workspace_bytes(R), dev, st)
+    ws = ws or _logits_records(R, dev, st)
     check(lib().naju_logits_process(R, V, io, _p(logits), ld, _p(history), H, _p(lengths),
                                     _p(repetition), _p(presence), _p(frequency), _p(bias_ids),
                                     _p(bias), nb, _p(mask), _p(out), _p(best), ws.tensor.data_ptr(),
