@@ -199,17 +199,24 @@ class Workspace:
 _ws_cache: dict = {}
 
 
+def _cached_workspace(key, nbytes, dev) -> Workspace:
+    """The workspace kept for key, made at its first use.  One made under graph capture is not
+    kept: its zero fill is a node of that graph and has not run for anybody else."""
+    ws = _ws_cache.get(key)
+    if ws is None:
+        ws = Workspace(nbytes(), dev)
+        if not torch.cuda.is_current_stream_capturing():
+            _ws_cache[key] = ws
+    return ws
+
+
 def workspace(op: int, dims: Dims, device) -> Workspace:
     """Cached workspace per (device, stream, op, dims): a workspace is only ever
     reused by calls with the same layout, on one stream."""
     dev = torch.device(device)
     key = (dev.index, torch.cuda.current_stream(dev).cuda_stream, op, dims.batch, dims.seqlen,
            dims.d_inner, dims.d_state, dims.d_conv, dims.io)
-    ws = _ws_cache.get(key)
-    if ws is None:
-        ws = Workspace(workspace_bytes(op, dims), dev)
-        _ws_cache[key] = ws
-    return ws
+    return _cached_workspace(key, lambda: workspace_bytes(op, dims), dev)
 
 
 def _io_of(t: torch.Tensor) -> int:
@@ -437,10 +444,8 @@ def mixer_fwd(xn, W_u, W_z, conv_w, W_a, a_bias, W_b, b_bias, W_B, W_C, D, W_out
     if ws is None:
         d = torch.device(dev)
         key = (d.index, torch.cuda.current_stream(d).cuda_stream, "mixer", Bt, L, dm, Di, N)
-        ws = _ws_cache.get(key)
-        if ws is None:
-            ws = Workspace(int(lib().naju_mixer_workspace_bytes(ctypes.byref(dims), dm)), d)
-            _ws_cache[key] = ws
+        ws = _cached_workspace(
+            key, lambda: int(lib().naju_mixer_workspace_bytes(ctypes.byref(dims), dm)), d)
     check(lib().naju_mixer_fwd(ctypes.byref(dims), dm, _p(xn), _p(res), _p(W_u), _p(W_z),
                                _p(conv_w), _p(conv_state), _p(W_a), _p(a_bias), _p(W_b),
                                _p(b_bias), _p(W_B), _p(W_C), _p(D), _p(W_out), _p(out), ws.ptr,
@@ -479,10 +484,8 @@ def mixer_bwd(xn, W_u, W_z, conv_w, W_a, a_bias, W_b, b_bias, W_B, W_C, D, W_out
     if ws is None:
         d = torch.device(dev)
         key = (d.index, torch.cuda.current_stream(d).cuda_stream, "mixer_bwd", Bt, L, dm, Di, N)
-        ws = _ws_cache.get(key)
-        if ws is None:
-            ws = Workspace(int(lib().naju_mixer_bwd_workspace_bytes(ctypes.byref(dims), dm)), d)
-            _ws_cache[key] = ws
+        ws = _cached_workspace(
+            key, lambda: int(lib().naju_mixer_bwd_workspace_bytes(ctypes.byref(dims), dm)), d)
     check(lib().naju_mixer_bwd(ctypes.byref(dims), dm, _p(xn), _p(W_u), _p(W_z), _p(conv_w),
                                _p(conv_state), _p(W_a), _p(a_bias), _p(W_b), _p(b_bias),
                                _p(W_B), _p(W_C), _p(D), _p(W_out), _p(d_out), _p(g["dxn"]),
