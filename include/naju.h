@@ -44,7 +44,8 @@
  *            memory; it uses only the caller's workspace.
  *  Stream    `stream` is a hipStream_t (NULL = the default stream).  Every call
  *            only enqueues work on that stream and returns; nothing is
- *            synchronised.
+ *            synchronised.  The stream and every device pointer belong to the
+ *            calling thread's current device.
  *  Workspace `ws` of at least naju_workspace_bytes(op, dims) bytes, zero-filled
  *            before its first use (naju_workspace_init, or any zero fill).
  *            Each call leaves it in a reusable state when its work completes,

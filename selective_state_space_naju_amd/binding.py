@@ -10,6 +10,8 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import threading
 
@@ -170,11 +172,32 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _stream(dev) -> int:
     """The current stream's handle on dev (a device of tensors), without building a stream
     object: 4 us less a call, which single-token calls notice."""
-    if dev.type != "cuda":
+    index = dev.index
+    if index is None:  # (no device of a GPU's tensor)
         raise ValueError("tensors must be on a GPU, got %s" % dev)
     if _raw_stream is None:
         return torch.cuda.current_stream(dev).cuda_stream
-    return _raw_stream(dev.index)
+    return _raw_stream(index)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _on_its_device(fn):
+    """An entry point that runs with its first tensor's device current.  The library launches on
+    the current device, and the default stream's handle is 0 on every device: called from another
+    one, a kernel would run there, on memory that is not its own."""
+    first = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        t = args[0] if args else kw.get(first)
+        device = t.get_device() if t is not None else -1  # (-1 in host memory)
+        if device < 0 or device == _current_device():
+            return fn(*args, **kw)
+        with torch.cuda.device(device):
+            return fn(*args, **kw)
+    return call
 
 
 class Workspace:
@@ -190,10 +213,14 @@ class Workspace:
         return ctypes.c_void_p(self.tensor.data_ptr())
 
     def error_flags(self) -> int:
-        out = ctypes.c_uint32(0)
-        check(lib().naju_workspace_check(self.ptr, self.nbytes, stream_handle(self.tensor.device),
-                                         ctypes.byref(out)))
-        return int(out.value)
+        return _error_flags(self.tensor, self.nbytes)
+
+
+@_on_its_device
+def _error_flags(ws: torch.Tensor, nbytes: int) -> int:
+    out = ctypes.c_uint32(0)
+    check(lib().naju_workspace_check(_p(ws), nbytes, stream_handle(ws.device), ctypes.byref(out)))
+    return int(out.value)
 
 
 _ws_cache: dict = {}
@@ -249,6 +276,7 @@ def _opt(t, name, shape, dtype, device):
 
 
 # ------------------------------------------------------------------ entry points
+@_on_its_device
 def scan_fwd(h, a, b, B, C, D, x0=None, *, return_ckpt=False, ws=None, check_errors=False):
     """y, x_final (, ckpt) = naju_scan_fwd(h, a, b, B, C, D, x0).
 
@@ -279,6 +307,7 @@ def scan_fwd(h, a, b, B, C, D, x0=None, *, return_ckpt=False, ws=None, check_err
     return (y, xf, ck) if return_ckpt else (y, xf)
 
 
+@_on_its_device
 def block_fwd(u, z, conv_w, a, b, B, C, D, x0=None, conv_state=None, *, return_ckpt=False,
               ws=None, check_errors=False):
     """y, x_final, conv_state_out (, ckpt) = naju_block_fwd(...) (check_errors: as for
@@ -311,6 +340,7 @@ def block_fwd(u, z, conv_w, a, b, B, C, D, x0=None, conv_state=None, *, return_c
     return (y, xf, cso, ck) if return_ckpt else (y, xf, cso)
 
 
+@_on_its_device
 def scan_bwd(h, a, b, B, C, D, dy, x0=None, dx_final=None, ckpt=None, *, want_dx0=True,
              ws=None):
     """Gradients of naju_scan_fwd: dict(dh, da, db, dB, dC, dD, dx0)."""
@@ -340,6 +370,7 @@ def scan_bwd(h, a, b, B, C, D, dy, x0=None, dx_final=None, ckpt=None, *, want_dx
     return out
 
 
+@_on_its_device
 def block_bwd(u, z, conv_w, a, b, B, C, D, dy, x0=None, dx_final=None, conv_state=None,
               ckpt=None, *, want_dx0=True, want_dconv_state=True, ws=None):
     """Gradients of naju_block_fwd: dict(du, dz, dconv_w, dconv_state, da, db, dB, dC, dD, dx0)."""
@@ -375,6 +406,7 @@ def block_bwd(u, z, conv_w, a, b, B, C, D, dy, x0=None, dx_final=None, conv_stat
     return out
 
 
+@_on_its_device
 def scan_step(h, a, b, B, C, D, x):
     """y = naju_scan_step(h, a, b, B, C, D, x); x ([Bt, Di, N] fp32) is updated in place."""
     Bt, Di = h.shape
@@ -394,6 +426,7 @@ def scan_step(h, a, b, B, C, D, x):
     return y
 
 
+@_on_its_device
 def block_step(u, z, conv_w, conv_state, a, b, B, C, D, x):
     """y = naju_block_step(...); x and conv_state ([Bt, K-1, Di]) are updated in place."""
     Bt, Di = u.shape
@@ -416,6 +449,7 @@ def block_step(u, z, conv_w, conv_state, a, b, B, C, D, x):
     return y
 
 
+@_on_its_device
 def mixer_fwd(xn, W_u, W_z, conv_w, W_a, a_bias, W_b, b_bias, W_B, W_C, D, W_out, res=None,
               conv_state=None, *, ws=None):
     """out = naju_mixer_fwd(...): the mixer layer around the block scan (bf16)."""
@@ -453,6 +487,7 @@ def mixer_fwd(xn, W_u, W_z, conv_w, W_a, a_bias, W_b, b_bias, W_B, W_C, D, W_out
     return out
 
 
+@_on_its_device
 def mixer_bwd(xn, W_u, W_z, conv_w, W_a, a_bias, W_b, b_bias, W_B, W_C, D, W_out, d_out,
               conv_state=None, *, fwd_ws=None, ws=None):
     """Gradients of naju_mixer_fwd for upstream d_out (the residual's is d_out); fwd_ws:
@@ -518,13 +553,15 @@ def _logits_records(R, dev, stream) -> Workspace:
     return ws
 
 
+@_on_its_device
 def embed_fwd(ids, W, scale=1.0):
     """out = naju_embed_fwd(ids, W, scale): scale * W[ids], zeros where an id lies outside
     the vocabulary.  ids: int32 of any shape; W [vocab, d_model]; out ids.shape + (d_model,)."""
     V, d = W.shape
     dt, dev = W.dtype, W.device
     io, st = _io_of(W), _stream(dev)
-    _req(W, "W", (V, d), dt, dev)
+    if not W.is_contiguous():
+        raise ValueError("W must be contiguous")
     _req(ids, "ids", ids.shape, torch.int32, dev)
     out = torch.empty(tuple(ids.shape) + (d,), dtype=dt, device=dev)
     check(lib().naju_embed_fwd(ids.numel(), V, d, io, _p(ids), _p(W), float(scale), _p(out),
@@ -532,6 +569,7 @@ def embed_fwd(ids, W, scale=1.0):
     return out
 
 
+@_on_its_device
 def embed_bwd(ids, dout, vocab, scale=1.0, *, dW=None, ws=None):
     """dW = naju_embed_bwd(ids, dout, vocab, scale), fp32 [vocab, d_model].  With dW given the
     gradient is added to it (rows of tokens that do not occur are not touched).  Without ws
@@ -557,6 +595,14 @@ def embed_bwd(ids, dout, vocab, scale=1.0, *, dW=None, ws=None):
     return dW
 
 
+def _row_stride(t, name, R, V) -> int:
+    """The distance of a matrix's contiguous rows."""
+    rows, cols = t.stride()
+    if (V > 1 and cols != 1) or (R > 1 and rows < V):
+        raise ValueError("%s must have contiguous rows that do not overlap" % name)
+    return rows if R > 1 else V
+
+
 def _req_rows(t, name, shape, dtype, device) -> int:
     """A matrix of contiguous rows, any distance apart; returns that distance."""
     if t is None:
@@ -567,10 +613,7 @@ def _req_rows(t, name, shape, dtype, device) -> int:
         raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
     if t.device != device:
         raise ValueError("%s must be on %s" % (name, device))
-    R, V = shape
-    if (V > 1 and t.stride(1) != 1) or (R > 1 and t.stride(0) < V):
-        raise ValueError("%s must have contiguous rows that do not overlap" % name)
-    return t.stride(0) if R > 1 else V
+    return _row_stride(t, name, *shape)
 
 
 def _distill_args(logits, t_ids, t_logits, temperature):
@@ -582,7 +625,7 @@ def _distill_args(logits, t_ids, t_logits, temperature):
     k = t_ids.shape[1]
     dt, dev = logits.dtype, logits.device
     io, st = _io_of(logits), _stream(dev)
-    ld = _req_rows(logits, "logits", (R, V), dt, dev)
+    ld = _row_stride(logits, "logits", R, V)
     _req(t_ids, "t_ids", (R, k), torch.int32, dev)
     _req(t_logits, "t_logits", (R, k), torch.float32, dev)
     return R, dev, st, (R, V, k, io, _p(logits), ld, _p(t_ids), _p(t_logits), float(temperature))
@@ -596,6 +639,7 @@ def _distill_grad_out(logits, g, dlogits):
     return dlogits, _req_rows(dlogits, "dlogits", (R, V), logits.dtype, logits.device)
 
 
+@_on_its_device
 def distill_fwd(logits, t_ids, t_logits, temperature=1.0):
     """loss, lse = naju_distill_fwd(...), fp32 [rows] each.  logits [rows, vocab] (contiguous
     rows, any row stride); t_ids int32 and t_logits fp32 [rows, k]: the teacher's top logits
@@ -607,6 +651,7 @@ def distill_fwd(logits, t_ids, t_logits, temperature=1.0):
     return loss, lse
 
 
+@_on_its_device
 def distill_bwd(logits, t_ids, t_logits, lse, g, temperature=1.0, *, dlogits=None):
     """dlogits = naju_distill_bwd(...) for the upstream gradient g [rows] of the loss and the
     lse that distill_fwd returned; dlogits: a tensor to write (contiguous rows, any stride)."""
@@ -617,6 +662,7 @@ def distill_bwd(logits, t_ids, t_logits, lse, g, temperature=1.0, *, dlogits=Non
     return dlogits
 
 
+@_on_its_device
 def distill_fwd_bwd(logits, t_ids, t_logits, g, temperature=1.0, *, dlogits=None):
     """loss, dlogits = naju_distill_fwd_bwd(...): both in one pass over the logits, for row
     weights g that are known before the loss."""
@@ -629,6 +675,7 @@ def distill_fwd_bwd(logits, t_ids, t_logits, g, temperature=1.0, *, dlogits=None
     return loss, dlogits
 
 
+@_on_its_device
 def logits_process(logits, history=None, lengths=None, repetition=None, presence=None,
                    frequency=None, bias_ids=None, bias=None, mask=None, *, ws=None):
     """out, best = naju_logits_process(...): penalties for the tokens of each row's history
@@ -643,7 +690,7 @@ def logits_process(logits, history=None, lengths=None, repetition=None, presence
         raise ValueError("logits: the vocabulary is empty")
     dt, dev = logits.dtype, logits.device
     io, st = _io_of(logits), _stream(dev)
-    ld = _req_rows(logits, "logits", (R, V), dt, dev)
+    ld = _row_stride(logits, "logits", R, V)
     H = nb = 0
     if history is not None:
         H = history.shape[-1]
@@ -669,6 +716,7 @@ def logits_process(logits, history=None, lengths=None, repetition=None, presence
     return out, best
 
 
+@_on_its_device
 def w4_quantize(W, group=64, *, zeros=False):
     """qweight, scales, zeros = naju_w4_quantize(W): weights W [d_in, d_out] (fp32 or bf16) as
     4-bit codes with one bf16 scale per `group` inputs of an output.  zeros=False: codes around
@@ -686,6 +734,7 @@ def w4_quantize(W, group=64, *, zeros=False):
     return qw, scales, z
 
 
+@_on_its_device
 def w4_linear(x, qweight, scales, group, zeros=None, bias=None, res=None):
     """y = naju_w4_linear(x, ...), bf16 [rows, d_out]: x bf16 [rows, d_in], qweight uint8
     [d_out, d_in / 2], scales bf16 and zeros uint8 (None: 8) [d_out, ceil(d_in / group)], bias
