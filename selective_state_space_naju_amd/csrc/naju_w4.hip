@@ -450,7 +450,10 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(
             hi = fmaxf(hi, v);
         }
         // codes -7 .. 7 around 8 without zeros, 0 .. 15 between the extremes with them
-        const bf16 sb = from_f<bf16>(zeros ? (hi - lo) / 15.f : fmaxf(hi, -lo) / 7.f);
+        // (divided first where the difference would leave fp32)
+        const float span = hi - lo;
+        const float step = span < __builtin_huge_valf() ? span / 15.f : hi / 15.f - lo / 15.f;
+        const bf16 sb = from_f<bf16>(zeros ? step : fmaxf(hi, -lo) / 7.f);
         const float s = to_f(sb);
         float z = 8.f;
         if (zeros) z = s > 0.f ? fminf(fmaxf(rintf(-lo / s), 0.f), 15.f) : 8.f;
