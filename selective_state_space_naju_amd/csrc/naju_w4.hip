@@ -368,20 +368,30 @@ __global__ __launch_bounds__(kW4Threads, 4) void w4_kernel(const W4Args g, const
     }
 }
 
-template <int RT, int P, int G, int WK, int NT, int D, bool Z>
+// LDS of `s` staged inputs: the waves' blocks; P rows of x; per group P sums, and scales and
+// zeros of the workgroup's outputs
+constexpr int64_t w4_lds(int P, int G, int WK, int NT, bool Z, int64_t s)
+{
+    const int per = (kW4Waves / WK) * NT * 16;
+    return 1024 * kW4Waves + P * s * 2 + s / G * (P * 4 + per * (Z ? 3 : 2));
+}
+constexpr int64_t kHalfLds = 80 << 10;
+
+// DEPTH: blocks whose codes a wave holds, or half of them where a turn of that many would not
+// leave a CU room for a second workgroup (groups of 32 with zeros, four and two, us: 64 x 4096 ->
+// 131072 268 and 250, 64 x 1000 -> 33000 46 and 38, 16 x 4096 -> 16384 27 and 22)
+template <int RT, int P, int G, int WK, int NT, int DEPTH, bool Z>
 static hipError_t launch_w4_t(const W4Args &g, hipStream_t st)
 {
     constexpr int per = (kW4Waves / WK) * NT * 16;
+    constexpr int D = w4_lds(P, G, WK, NT, Z, 128 * WK * DEPTH) <= kHalfLds ? DEPTH : DEPTH / 2;
     constexpr int64_t unit = 128 * WK * D;  // inputs of a turn of the ring
+    static_assert(w4_lds(P, G, WK, NT, Z, unit) <= kHalfLds, "two workgroups share a CU");
     const int64_t rows = g.R < RT * 16 ? g.R : RT * 16;
     const int64_t wgs = (g.N + per - 1) / per * ((g.R + RT * 16 - 1) / (RT * 16));
     // two workgroups on a CU, or one where there are not more than that
-    const int64_t budget = (wgs <= device_cu_count() ? 150 : 78) << 10;
-    // LDS of `s` staged inputs: the waves' blocks; P rows of x; per group P sums and `per`
-    // scales and zeros
-    auto bytes = [&](int64_t s) {
-        return 1024 * kW4Waves + P * s * 2 + s / G * (P * 4 + per * (Z ? 3 : 2));
-    };
+    const int64_t budget = wgs <= device_cu_count() ? 150 << 10 : kHalfLds;
+    auto bytes = [](int64_t s) { return w4_lds(P, G, WK, NT, Z, s); };
     // all inputs at once if they fit, else whole turns of the ring
     int64_t stage = (g.K + 127) / 128 * 128;
     if (stage == 0) stage = 128;

@@ -41,6 +41,7 @@ CASES = [  # rows, d_in, d_out, group, zeros, bias and residual
     (16, 9002, 33, 128, True, False),
     (32, 5010, 100, 64, False, True),
     (64, 2502, 47, 32, True, False),
+    (16, 3002, 20000, 32, True, True),
     # one output less than the rule's border
     (4, 260, 24575, 64, True, False),
     (64, 260, 24575, 64, False, False),
