@@ -77,10 +77,15 @@ __device__ __forceinline__ Entry load_entry(const int32_t *t_ids, const float *t
     Entry e{-1, kNegInf};
     if ((int)threadIdx.x < k) {
         const int id = t_ids[threadIdx.x];
-        const float t = t_logits[threadIdx.x];
-        if (id >= 0 && id < V && t != kNegInf) {
-            e.id = id;
-            e.t = t;
+        if (id >= 0 && id < V) {
+            // (kept behind the id: with both asked for at once the rows' loads of a CU's workgroups
+            // fall together, 16384 x 32000 bf16 loss and gradient 437 us in place of 430)
+            asm volatile("");
+            const float t = t_logits[threadIdx.x];
+            if (t != kNegInf) {
+                e.id = id;
+                e.t = t;
+            }
         }
     }
     return e;
