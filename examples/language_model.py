@@ -11,8 +11,9 @@ Serving (one token per call for every sequence): embedding of the last tokens, p
     4-bit weights around the block's decode step, 4-bit output layer, penalties and a grammar mask
     on the logits, the best allowed token.
 
-The teacher is a fixed table: for each token, the k most likely next ones and their logits.  Norms
-and the output layer's products are plain torch; everything else goes through the library.
+The teacher is a fixed table: for each token, the k most likely next ones and their logits.  Norms,
+the training step's output layer, the updates, and the decode step's convolution that the gates are
+projected from are plain torch; everything else goes through the library.
 """
 from __future__ import annotations
 

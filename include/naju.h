@@ -457,7 +457,8 @@ naju_status_t naju_logits_process(int64_t rows, int64_t vocab, int32_t io, const
  *   y         [rows][d_out] bf16 (written)
  * d_in even, at most 2^24; d_out <= 2^26; group 32, 64 or 128 (the last group of a
  * row may be shorter).  Any number of rows up to 2^20; the weights are read once
- * for every 64 of them.  An infinite or NaN x makes its row of y NaN or infinite.
+ * for every 64 of them.  An infinite or NaN x makes its row of y NaN or infinite, and
+ * so does a group of inputs whose magnitudes add up to more than 2e36.
  */
 naju_status_t naju_w4_linear(int64_t rows, int64_t d_in, int64_t d_out, int64_t group,
                              const void *x, const uint8_t *qweight, const void *scales,

@@ -13,9 +13,9 @@
 // workgroup takes a row, streams it with 16-byte accesses and keeps one entry
 // per thread; statistics and sums are fp32, each rounded once on output.
 //
-// Bound by the bytes of the logits.  16384 x 32000 bf16: loss 219 us (4.8 TB/s;
-// 5.9 at 32768 logits a row), gradient 437 us, both in one call 423 us (5.0 TB/s,
-// a large copy's rate).
+// Bound by the bytes of the logits.  16384 x 32000 bf16, kernel times: loss 179 us
+// (5.9 TB/s of reads), gradient 413 us, both in one call 426 us (4.9 TB/s; a large
+// copy reaches 4.8).
 #include <math.h>
 
 #include "naju_device.h"
@@ -344,8 +344,8 @@ __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
 //
 // (s - m) c2 is formed as one multiply-add, s c - b with b = m c rounded; what
 // that rounding took, m c - b, is the same for every logit and comes off the sum.
-// (Subtracted first, an operation more per logit, 8192 x 50001 bf16 takes 413 us
-// in place of 400.)  c is c2 unless m c2 would pass 2^30, or fp32's range: there it
+// (Subtracted first, an operation more per logit, 8192 x 50001 bf16 takes 3 %
+// longer.)  c is c2 unless m c2 would pass 2^30, or fp32's range: there it
 // is made smaller.  Numbers of that size lie 64 or more apart in units of 1 / c,
 // so either way all but the largest weigh nothing, and b's rounding, up to 64,
 // leaves the exponential in range.
@@ -517,7 +517,7 @@ struct DistillArgs {
 };
 
 // Short rows take workgroups of two waves: the rows, not the logits, are then what there are
-// many of (65536 x 1000 fp32, loss and gradient: 367 us with eight waves a row, 195 us with
+// many of (65536 x 1000 fp32, loss and gradient: 367 us with eight waves a row, 184 us with
 // two).
 constexpr int kSmallBS = 128, kLargeBS = 512;
 template <typename IO> static bool short_rows(const DistillArgs &a)
@@ -559,8 +559,8 @@ template <typename IO> static hipError_t launch_grad(const DistillArgs &a, hipSt
 {
     if (short_rows<IO>(a)) return launch_grad_t<IO, 4, kSmallBS>(a, st);
     // eight accesses a thread amortise the entries' part of a workgroup; few rows are cut finer
-    // (eight and two, us, 131072 bf16 logits: 1 row 8.9 and 7.0, 64 rows 11.8 and 11.7, 128 rows
-    // 17.8 and 19.3, 256 rows 27.2 and 28.8)
+    // (eight and two, us, 131072 bf16 logits: 1 row 9.2 and 7.4, 64 rows 13.9 and 13.6, 128 rows
+    // 18.8 and 19.0, 256 rows 31.1 and 31.3)
     constexpr int64_t per = kLargeBS * kPer16<IO>;
     return a.R * ((a.V + 8 * per - 1) / (8 * per)) >= 512 ? launch_grad_t<IO, 8, kLargeBS>(a, st)
                                                           : launch_grad_t<IO, 2, kLargeBS>(a, st);

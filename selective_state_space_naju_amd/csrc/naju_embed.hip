@@ -13,8 +13,8 @@
 // zero-filled (kept, when accumulating).
 //
 // Bound by the bytes of dout and dW: 65536 x 2048 fp32 over 100003 rows take
-// 345 us (1356 MB, 3.9 TB/s; a copy reaches 4.8), 16384 x 768 bf16 over 50000
-// rows 62 us, of which the sums are 13.
+// 343 us (1356 MB, 4.0 TB/s; a copy reaches 4.8), 16384 x 768 bf16 over 50000
+// rows 61 us, of which the sums are 14.
 #include "naju_device.h"
 #include "naju_host.h"
 #include "naju_launch.h"
@@ -123,9 +123,11 @@ static hipError_t launch_embed_fwd(int64_t T, int64_t V, int64_t d, const int32_
 // digits, then every tile ranks its keys (in its own order) behind the smaller
 // digits of all tiles and the equal digits of the tiles before it.
 constexpr int kDigits = 512;  // most values of a digit
-// keys of a tile: 1024 while that leaves a tile few others to look at, else 4096 (tiles of 1024
-// and 4096: gradient of 16384 x 768 over 50000 rows 54 and 56 us, of 65536 x 2048 fp32 over
-// 100003 rows 374 and 360 us)
+// keys of a tile: 1024 while that leaves a tile few others to look at, else 4096 (sort and fill
+// with tiles of 1024 and 4096: 16384 tokens, 50000 x 768 rows 38 and 43 us; 65536 tokens, 100003 x
+// 2048 rows 148 and 146 us).  Every tile reads the counts of all, so the sort grows with the
+// square of the tokens in the end: a pass takes 25 us at 2^18 tokens, 76 us at 2^20, 526 us at
+// 2^22.
 static int tile_rounds(int64_t T) { return T <= 16384 ? 1 : 4; }
 
 __device__ __forceinline__ uint32_t key_of(const int32_t *ids, const uint32_t *keys, int64_t i,
@@ -139,7 +141,7 @@ __device__ __forceinline__ uint32_t key_of(const int32_t *ids, const uint32_t *k
 // The zero fill of dW needs nothing from the sort, whose kernels leave most of
 // the device idle: each launch of the sort carries workgroups that fill a slice.
 // (16384 x 768 tokens over 50000 rows: 72 us with the fill in front of the
-// sort, 62 us beside it; the fill alone is 21 us, the sort 27 us.)
+// sort, 61 us beside it; the fill alone is 21 us, the sort 27 us.)
 struct Fill {
     float *p;       // null: nothing to fill
     int64_t n;      // floats of this launch's slice

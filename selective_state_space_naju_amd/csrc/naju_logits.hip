@@ -14,8 +14,9 @@
 // counted there, the tokens that were touched are listed, their values are
 // computed once each into their words, and the dense pass that follows only
 // selects between a word and the logit.  It reads every logit and writes every
-// result once.  256 x 131072 bf16 with every constraint: 54 us (3.9 TB/s); the
-// dense pass alone is 35 us, the rest is the lists' latency between barriers.
+// result once.  256 x 131072 bf16 with 4096 tokens of history, 300 biases and a
+// mask: 50 us (4.2 TB/s); the dense pass alone is 35 us, the rest is the lists'
+// latency between barriers.
 #include "naju_device.h"
 #include "naju_host.h"
 #include "naju_launch.h"
@@ -329,9 +330,9 @@ naju_status_t naju_logits_process(int64_t rows, int64_t vocab, int32_t io, const
     LogitsArgs g{};
     g.B = rows;
     g.V = vocab;
-    // small tiles only where large ones leave most CUs idle (2048 tokens of history, large and
-    // small, us: 1 x 32000 8.1 and 6.3, 8 x 50001 8.1 and 7.3, 16 x 131072 9.5 and 12.6,
-    // 256 x 131072 43 and 97)
+    // small tiles only where large ones leave most CUs idle (2048 tokens of history, 16 biases and
+    // a mask, large and small, us: 1 x 32000 7.6 and 7.4, 8 x 50001 8.7 and 7.4, 16 x 131072 9.6
+    // and 12.6, 256 x 131072 48 and 108)
     g.tile = rows * ((vocab + kLogTile - 1) / kLogTile) >= 64 ? kLogTile : kLogSmallTile;
     g.n_tiles = (vocab + g.tile - 1) / g.tile;
     g.ld = ld;

@@ -21,8 +21,9 @@
 // The order of the 8 inputs inside a quarter is that of the unpacking; x is
 // staged in LDS in the same order.
 //
-// 4096 -> 131072, groups of 128: one row 53 us (5.2 TB/s of codes), 32 rows
-// 80 us, where unpacking and the LDS reads of x come to more than the codes.
+// 4096 -> 131072, groups of 128: one row 51 us (5.3 TB/s of codes), 32 rows
+// 79 us and 64 rows 157 us, where unpacking and the LDS reads of x come to more
+// than the codes.
 #include "naju_device.h"
 #include "naju_host.h"
 #include "naju_launch.h"
@@ -214,7 +215,7 @@ __global__ __launch_bounds__(kW4Threads, 4) void w4_kernel(const W4Args g, const
         // Rows of 512 inputs are dealt out to the waves, F of them in flight.  Where the waves
         // split the inputs, a stage is most of a call: four rows, and the first scales and zeros
         // asked for before them (5 x 4100 -> 7001: 13.9 -> 13.0 us; elsewhere the registers cost
-        // more: 16 x 4096 -> 131072 68 -> 72 us).
+        // more: 16 x 4096 -> 131072 took 6 % longer).
         constexpr bool kAhead = WK > 1;
         constexpr int F = RT == 1 && kAhead ? 4 : 2 * RT;
         const int g0 = (int)(s0 / G), sets = (runs * 8 / G + 7) / 8;
@@ -417,9 +418,14 @@ static hipError_t launch_w4_t(const W4Args &g, hipStream_t st)
 
 template <int G, bool Z> static hipError_t launch_w4_z(const W4Args &g, hipStream_t st)
 {
-    // few outputs: the waves of a workgroup split the inputs of a tile (4096 inputs, split and
-    // not, us: 14336 outputs, one row 9.9 and 15.7, 32 rows 28 and 46; 32000 outputs, one row
-    // 19.1 and 18.0, 32 rows 53 and 48; 131072 outputs, one row 69 and 53, 32 rows 191 and 93)
+    // few outputs: the waves of a workgroup split the inputs of a tile (4096 inputs, groups of
+    // 128, split and not, us:
+    //   rows    14336 outputs    24576          32000          131072
+    //    1      11 and 15        17 and 17      20 and 17      65 and 51
+    //    8      14 and 18        22 and 20      26 and 20      92 and 63
+    //   16      19 and 21        29 and 23      35 and 24      124 and 65
+    //   32      29 and 40        47 and 43      55 and 44      202 and 78
+    //   64      42 and 49        62 and 51      63 and 53      228 and 157)
     const bool split = g.N < 24576;
     if (g.R <= 4)
         return split ? launch_w4_t<1, 4, G, 4, 1, 4, Z>(g, st)
