@@ -267,7 +267,7 @@ __global__ __launch_bounds__(BS, 6) void distill_grad_kernel(
     ids[tid] = e.id;
     ps[tid] = e.id >= 0 ? ex2((e.t - base_of(ts.m)) * c2) / ts.s : 0.f;
     float dense_at;  // the dense part at this thread's entry
-    if (fabsf(L) <= kFineLse || L != L) {
+    if (fabsf(L) <= kFineLse || L != L || !some) {
         auto dense = [&](float x) { return f * exp_nat(fmaf(x, inv_tau, -L)); };
         if (V >= n) {
             IO *out_c0 = out + c0;

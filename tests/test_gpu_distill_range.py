@@ -16,7 +16,7 @@ import numpy as np
 import pytest
 import torch
 
-from gpu_helpers import f32_dev, to_dev
+from gpu_helpers import dev, to_dev
 from oracle import lm
 from selective_state_space_naju_amd import binding as nb
 from selective_state_space_naju_amd import inputs
@@ -98,3 +98,21 @@ def test_distill_at_the_ends_of_the_range(io, V, tau):
                             ("loss (joint)", got[3], loss, b_loss),
                             ("gradient (joint)", got[4], grad, b_grad)):
         check(name, a, ref, b)
+
+
+@pytest.mark.parametrize("io,V", [("bf16", 40), ("bf16", 70001), ("f32", 20000)])
+def test_distill_rows_of_weight_zero_whatever_they_hold(io, V):
+    """Padding: zeros, from logits and an lse of any kind, and nothing in the rows beside them."""
+    x = torch.randn(7, V, device=dev())
+    for r, v in enumerate((-np.inf, np.nan, -3.4e38, 3e4, np.inf)):
+        x[r] = v
+    x = to_dev(x.cpu().numpy(), io)
+    ids = torch.zeros(7, 2, dtype=torch.int32, device=dev())
+    ids[:, 1] = V - 1
+    t = torch.zeros(7, 2, device=dev())
+    g = torch.tensor([0.0] * 6 + [1.0], device=dev())
+    lse = nb.distill_fwd(x, ids, t)[1]
+    lse[5] = 1e30
+    grad, joint = nb.distill_bwd(x, ids, t, lse, g), nb.distill_fwd_bwd(x, ids, t, g)[1]
+    for d in (grad, joint):
+        assert not d[:6].any() and d[6].any() and torch.isfinite(d).all()
