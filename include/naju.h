@@ -478,6 +478,58 @@ naju_status_t naju_w4_quantize(int64_t d_in, int64_t d_out, int64_t group, int32
                                const void *W, uint8_t *qweight, void *scales, uint8_t *zeros,
                                void *stream);
 
+/*
+ * ---- The rest of a layer: norms, a second token mixer, the update ----
+ * The conventions of the section above hold.
+ */
+
+/*
+ * The norms before and after a block, with the block's gate and residual scale.
+ * Per token, over d_model channels:
+ *     n  = y / sqrt(mean y^2 + eps) * w_post      (y itself without w_post)
+ *     x' = x + scale * n * SiLU(z)                (without scale, z: 1)
+ *     xn = x' / sqrt(mean x'^2 + eps) * w_pre
+ * in fp32, each output rounded once (xn is formed from the unrounded x').
+ *   x         [tokens][d_model] x_io  the residual stream
+ *   y         [tokens][d_model] io    the block's output, or NULL: x' = x, and z,
+ *             scale, w_post and x_new are NULL too
+ *   z         [tokens][d_model] io    gate pre-activation, or NULL
+ *   scale, w_post, w_pre  [d_model] fp32, each may be NULL (w_pre: no xn)
+ *   x_new     [tokens][d_model] x_io (written)
+ *   xn        [tokens][d_model] io (written), or NULL with w_pre
+ * io BF16 with x_io BF16 or F32, or both F32.  d_model 4 to 16384.  eps >= 0.
+ * Squares are summed as they are: a row whose sum of squares leaves fp32 (values
+ * of 1e17 and more) has the norm 0, a row that holds NaN or infinity has NaN.
+ */
+naju_status_t naju_res_norm_fwd(int64_t tokens, int64_t d_model, int32_t io, int32_t x_io,
+                                const void *x, const void *y, const void *z, const float *scale,
+                                const float *w_post, const float *w_pre, float eps, void *x_new,
+                                void *xn, void *stream);
+
+/*
+ * Its gradients, for the gradients dxn of xn and dx_new of x':
+ *   dx     [tokens][d_model] g_io   of x' with what reached it through xn, which is
+ *          the gradient of x too (written)
+ *   dy, dz [tokens][d_model] io     (written; with y, z)
+ *   dscale, dw_post, dw_pre  [d_model] fp32 (written), each may be NULL; sums over
+ *          the tokens in a fixed order, zeros for no tokens
+ *   dxn    [tokens][d_model] g_io, with w_pre;  dx_new  [tokens][d_model] g_io or
+ *          NULL (= zeros), one of the two at least
+ *   x_new  [tokens][d_model] x_io   x' (with w_pre)
+ *   y, z, scale, w_post, w_pre, eps as in the forward call
+ *   g_io   F32, or BF16 where io is BF16
+ *   ws     naju_res_norm_bwd_workspace_bytes() bytes, 256-byte aligned (no initial
+ *          contents needed; not used when tokens == 0)
+ */
+size_t naju_res_norm_bwd_workspace_bytes(int64_t tokens, int64_t d_model);
+naju_status_t naju_res_norm_bwd(int64_t tokens, int64_t d_model, int32_t io, int32_t x_io,
+                                int32_t g_io, const void *dxn, const void *dx_new,
+                                const void *x_new, const void *y, const void *z,
+                                const float *scale, const float *w_post, const float *w_pre,
+                                float eps, void *dx, void *dy, void *dz, float *dscale,
+                                float *dw_post, float *dw_pre, void *ws, size_t ws_bytes,
+                                void *stream);
+
 /* Thread-local description of the last non-OK status ("" if none). */
 const char *naju_last_error(void);
 

@@ -33,6 +33,7 @@ EXPORTS = ("naju_workspace_bytes", "naju_ckpt_bytes", "naju_workspace_init",
            "naju_scan_fwd_noalloc", "naju_embed_fwd", "naju_embed_bwd_workspace_bytes",
            "naju_embed_bwd", "naju_distill_fwd", "naju_distill_bwd", "naju_distill_fwd_bwd",
            "naju_logits_workspace_bytes", "naju_logits_process", "naju_w4_linear", "naju_w4_quantize",
+           "naju_res_norm_fwd", "naju_res_norm_bwd_workspace_bytes", "naju_res_norm_bwd",
            "naju_last_error", "naju_version")
 
 
@@ -120,6 +121,13 @@ def lib() -> ctypes.CDLL:
         L.naju_w4_linear.restype = st
         L.naju_w4_quantize.argtypes = [i64, i64, i64, i32] + [vp] * 5
         L.naju_w4_quantize.restype = st
+        L.naju_res_norm_fwd.argtypes = [i64, i64, i32, i32] + [vp] * 6 + [f32] + [vp] * 3
+        L.naju_res_norm_fwd.restype = st
+        L.naju_res_norm_bwd_workspace_bytes.argtypes = [i64, i64]
+        L.naju_res_norm_bwd_workspace_bytes.restype = sz
+        L.naju_res_norm_bwd.argtypes = ([i64, i64, i32, i32, i32] + [vp] * 8 + [f32] + [vp] * 7 +
+                                        [sz, vp])
+        L.naju_res_norm_bwd.restype = st
         L.naju_last_error.argtypes = []
         L.naju_last_error.restype = ctypes.c_char_p
         L.naju_version.argtypes = []
@@ -246,12 +254,16 @@ def workspace(op: int, dims: Dims, device) -> Workspace:
     return _cached_workspace(key, lambda: workspace_bytes(op, dims), dev)
 
 
-def _io_of(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
+def _code(dtype: torch.dtype) -> int:
+    if dtype == torch.float32:
         return F32
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return BF16
-    raise TypeError("activations must be float32 or bfloat16, got %s" % t.dtype)
+    raise TypeError("activations must be float32 or bfloat16, got %s" % dtype)
+
+
+def _io_of(t: torch.Tensor) -> int:
+    return _code(t.dtype)
 
 
 def _req(t, name, shape, dtype, device):
@@ -756,3 +768,77 @@ def w4_linear(x, qweight, scales, group, zeros=None, bias=None, res=None):
     check(lib().naju_w4_linear(R, K, N, group, _p(x), _p(qweight), _p(scales), _p(zeros),
                                _p(bias), _p(res), _p(y), st))
     return y
+
+
+# ------------------------------------------- the rest of a layer and of its training step
+def _scratch(nbytes, dev):
+    """Scratch of one call's own, from torch's allocator (in stream order; under graph capture
+    from the graph's pool): calls from several threads, streams or graphs do not share it."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def _norm_args(x, y, z, scale, w_post, w_pre, like):
+    """Checks what both directions of the norms take; returns tokens, d_model, device, stream and
+    the type of the block's side (y's, or `like`'s where there is no y)."""
+    if x.dim() < 1:
+        raise ValueError("x must have a dimension of channels")
+    dev, d = x.device, x.shape[-1]
+    st = _stream(dev)
+    if y is None and (z is not None or scale is not None or w_post is not None):
+        raise ValueError("z, scale and w_post need y")
+    io_dt = y.dtype if y is not None else like
+    for nm, t in (("y", y), ("z", z)):
+        _opt(t, nm, x.shape, io_dt, dev)
+    for nm, t in (("scale", scale), ("w_post", w_post), ("w_pre", w_pre)):
+        _opt(t, nm, (d,), torch.float32, dev)
+    return (x.numel() // d if d else 0), d, dev, st, io_dt
+
+
+@_on_its_device
+def res_norm_fwd(x, y=None, z=None, *, scale=None, w_post=None, w_pre=None, eps=1e-6, dtype=None):
+    """x_new, xn = naju_res_norm_fwd(...): x_new = x + scale * norm(y) * w_post * SiLU(z) and
+    xn = norm(x_new) * w_pre over the last dimension.  x [..., d_model] fp32 or bf16 (contiguous);
+    y, z of its shape in the block's type; the vectors fp32 [d_model].  Without w_post y is taken
+    as it is, without y x_new is x itself, without w_pre xn is None.  dtype: the block's type (xn)
+    where there is no y (default: x's)."""
+    T, d, dev, st, io_dt = _norm_args(x, y, z, scale, w_post, w_pre, dtype or x.dtype)
+    _req(x, "x", x.shape, x.dtype, dev)
+    if dtype is not None and dtype != io_dt:
+        raise TypeError("dtype: y has the block's type, %s" % io_dt)
+    io, x_io = _code(io_dt), _io_of(x)
+    if y is None and w_pre is None:
+        raise ValueError("neither y nor w_pre is given: nothing to compute")
+    x_new = torch.empty_like(x) if y is not None else None
+    xn = torch.empty(x.shape, dtype=io_dt, device=dev) if w_pre is not None else None
+    check(lib().naju_res_norm_fwd(T, d, io, x_io, _p(x), _p(y), _p(z), _p(scale), _p(w_post),
+                                  _p(w_pre), float(eps), _p(x_new), _p(xn), st))
+    return (x if y is None else x_new), xn
+
+
+@_on_its_device
+def res_norm_bwd(dxn, dx_new, x_new, y=None, z=None, *, scale=None, w_post=None, w_pre=None,
+                 eps=1e-6, dtype=None, ws=None):
+    """Gradients of naju_res_norm_fwd for the gradients dxn of xn (with w_pre) and dx_new of x_new
+    (or None), both fp32 or both bf16: dict(dx, dy, dz, dscale, dw_post, dw_pre), None where the
+    forward call had no such input.  x_new, y, z, the vectors and dtype as in the forward call; x_new
+    is what that call returned."""
+    T, d, dev, st, io_dt = _norm_args(x_new, y, z, scale, w_post, w_pre, dtype or x_new.dtype)
+    _req(x_new, "x_new", x_new.shape, x_new.dtype, dev)
+    io, x_io = _code(io_dt), _io_of(x_new)
+    if (dxn is None) != (w_pre is None):
+        raise ValueError("dxn and w_pre go together")
+    if dxn is None and dx_new is None:
+        raise ValueError("neither dxn nor dx_new is given: no gradient to pass on")
+    g_dt = (dxn if dxn is not None else dx_new).dtype
+    _opt(dxn, "dxn", x_new.shape, g_dt, dev)
+    _opt(dx_new, "dx_new", x_new.shape, g_dt, dev)
+    out = {"dx": torch.empty(x_new.shape, dtype=g_dt, device=dev)}
+    for nm, t in (("dy", y), ("dz", z), ("dscale", scale), ("dw_post", w_post), ("dw_pre", w_pre)):
+        out[nm] = torch.empty_like(t) if t is not None else None
+    nbytes = lib().naju_res_norm_bwd_workspace_bytes(T, d) if ws is None else ws.nbytes
+    scratch = _scratch(nbytes, dev) if ws is None else ws.tensor
+    check(lib().naju_res_norm_bwd(T, d, io, x_io, _code(g_dt), _p(dxn), _p(dx_new), _p(x_new),
+                                  _p(y), _p(z), _p(scale), _p(w_post), _p(w_pre), float(eps),
+                                  _p(out["dx"]), _p(out["dy"]), _p(out["dz"]), _p(out["dscale"]),
+                                  _p(out["dw_post"]), _p(out["dw_pre"]), _p(scratch), nbytes, st))
+    return out

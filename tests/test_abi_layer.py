@@ -1,0 +1,102 @@
+"""CPU checks of the entry points of the rest of a layer: argument validation
+through the C ABI and the binding (no call here touches a GPU), and pins of
+their fp64 definitions."""
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer
+from selective_state_space_naju_amd import binding as nb
+
+FAKE = 0x100000  # a 256-byte aligned non-null address; never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(nb.LIB_PATH):
+        pytest.fail("libnaju.so is not built (run __graft_entry__.build())")
+    return nb.lib()
+
+
+def expect(status, want, text=""):
+    assert status == want, nb.last_error()
+    assert text in nb.last_error(), nb.last_error()
+
+
+def test_res_norm_fwd_refusals(lib):
+    def call(T=10, d=64, io=nb.BF16, xio=nb.F32, x=FAKE, y=FAKE, z=FAKE, s=FAKE, wo=FAKE, wi=FAKE,
+             eps=1e-6, new=FAKE, xn=FAKE):
+        return lib.naju_res_norm_fwd(T, d, io, xio, x, y, z, s, wo, wi, eps, new, xn, None)
+    expect(call(T=-1), nb.EINVAL, "negative size")
+    expect(call(T=2 ** 41), nb.EINVAL, "too large")
+    expect(call(io=3), nb.EINVAL, "io dtype")
+    expect(call(xio=7), nb.EINVAL, "io dtype")
+    expect(call(io=nb.F32, xio=nb.BF16), nb.EUNSUPPORTED, "fp32")
+    for d in (1, 3, 16385):
+        expect(call(d=d), nb.EUNSUPPORTED, "d_model")
+    for eps in (-1.0, float("nan"), float("inf")):
+        expect(call(eps=eps), nb.EINVAL, "eps")
+    expect(call(x=None), nb.EINVAL, "x is NULL")
+    expect(call(x=FAKE + 2), nb.EINVAL, "aligned")
+    expect(call(y=None, new=None), nb.EINVAL, "need y")
+    expect(call(new=None), nb.EINVAL, "go together")
+    expect(call(xn=None), nb.EINVAL, "go together")
+    expect(call(y=FAKE + 1), nb.EINVAL, "aligned")
+    expect(call(s=FAKE + 2), nb.EINVAL, "aligned")
+    expect(call(y=None, z=None, s=None, wo=None, wi=None, new=None, xn=None), nb.EINVAL,
+           "nothing to compute")
+    assert call(T=0, x=None) == nb.OK
+    assert call(d=0, x=None) == nb.OK
+
+
+def test_res_norm_bwd_refusals(lib):
+    def call(T=10, d=64, io=nb.BF16, xio=nb.F32, gio=nb.F32, dxn=FAKE, dnew=FAKE, x=FAKE, y=FAKE,
+             z=FAKE, s=FAKE, wo=FAKE, wi=FAKE, eps=1e-6, dx=FAKE, dy=FAKE, dz=FAKE, ds=FAKE,
+             dwo=FAKE, dwi=FAKE, ws=FAKE, wsb=1 << 40):
+        return lib.naju_res_norm_bwd(T, d, io, xio, gio, dxn, dnew, x, y, z, s, wo, wi, eps, dx,
+                                     dy, dz, ds, dwo, dwi, ws, wsb, None)
+    expect(call(d=-1), nb.EINVAL, "negative size")
+    expect(call(gio=2), nb.EINVAL, "io dtype")
+    expect(call(io=nb.F32, gio=nb.BF16), nb.EUNSUPPORTED, "fp32")
+    expect(call(d=2), nb.EUNSUPPORTED, "d_model")
+    expect(call(dxn=None), nb.EINVAL, "go together")
+    expect(call(dxn=None, wi=None, dwi=None, dnew=None), nb.EINVAL, "no gradient")
+    expect(call(s=None), nb.EINVAL, "dscale needs")
+    expect(call(wo=None), nb.EINVAL, "dw_post needs")
+    expect(call(wi=None, dxn=None), nb.EINVAL, "dw_pre needs")
+    expect(call(x=None), nb.EINVAL, "x_new is NULL")
+    for k in ("dx", "dy", "dz"):
+        expect(call(**{k: None}), nb.EINVAL, k + " is NULL")
+        expect(call(**{k: FAKE + 1}), nb.EINVAL, "aligned")
+    expect(call(ws=None), nb.EWORKSPACE, "workspace is NULL")
+    expect(call(wsb=64), nb.EWORKSPACE, "needs")
+    expect(call(ws=FAKE + 16), nb.EINVAL, "256-byte")
+    assert call(d=0, ws=None) == nb.OK
+    assert call(T=0, ds=None, dwo=None, dwi=None, dxn=None, dnew=None, ws=None) == nb.OK
+    size = lib.naju_res_norm_bwd_workspace_bytes
+    assert size(16384, 768) >= 512 * 3 * 768 * 4
+    assert size(-1, 768) == 0 and size(10, 3) == 0
+
+
+def test_binding_refuses_what_does_not_fit(lib):
+    x, w = torch.zeros(3, 8), torch.ones(8)
+    with pytest.raises(ValueError, match="GPU"):
+        nb.res_norm_fwd(x, w_pre=w)
+    with pytest.raises(ValueError, match="GPU"):
+        nb.res_norm_bwd(x, None, x, w_pre=w)
+
+
+# ------------------------------------------------------------- pins of the definitions
+def test_norm_definitions():
+    """A norm without weight brings any row to unit mean square; the gradient of a norm is
+    perpendicular to its input where eps is 0; SiLU(0) = 0 leaves the residual."""
+    rng = np.random.default_rng(1)
+    x, y, d = rng.standard_normal((3, 4, 50))
+    new, xn = layer.res_norm_fwd(x, y, np.zeros_like(y), w_pre=np.ones(50), eps=0.0)
+    assert np.array_equal(new, x)
+    assert np.allclose((xn * xn).mean(1), 1.0, rtol=1e-12)
+    g = layer.res_norm_bwd(d, None, x, w_pre=np.ones(50), eps=0.0)
+    assert np.abs((g["dx"] * x).sum(1)).max() < 1e-12
+    assert np.allclose(g["dw_pre"], (d * xn).sum(0))
