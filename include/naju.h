@@ -530,6 +530,46 @@ naju_status_t naju_res_norm_bwd(int64_t tokens, int64_t d_model, int32_t io, int
                                 float *dw_post, float *dw_pre, void *ws, size_t ws_bytes,
                                 void *stream);
 
+/*
+ * One AdamW step over a list of tensors.  Per element, with t the step's number:
+ *     g = grad_scale g
+ *     m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *     p = p - lr weight_decay p
+ *           - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32.  state_bits 32: m, v fp32.  state_bits 8: m and the square root of v as
+ * 8-bit floats (e4m3: 4 exponent bits of bias 7, 3 mantissa bits, no infinities),
+ * each times the fp32 scale of its 256 consecutive elements (the tensor's last block
+ * may be shorter).  A scale is its block's largest magnitude / 448 (0 below 2^-120,
+ * and the block then holds zeros); values are rounded to nearest even; p is formed
+ * from the unrounded m and v.  Zeros (codes and scales) are the states of a first
+ * step.  A NaN gradient makes its element NaN, one that is infinite or has an infinite
+ * square its block's states.
+ *   tensors   host array, read during the call only
+ *   step      number of this step, from 1; or step_dev, a device int32 that holds it
+ *             (a captured graph then reads it at every replay; it is not advanced)
+ *   lr_dev    device fp32 that holds the learning rate, or NULL (= lr)
+ *   grad_scale  device fp32 (of a clipped norm, say), or NULL (= 1)
+ *   g_io      type of every tensor's gradient
+ * Two tensors whose p overlap are refused; the other outputs must not overlap.
+ * An output may be its own input (NULL says so); otherwise outputs must not alias inputs.
+ */
+typedef struct {
+    int64_t n;               /* elements; 0: the tensor is skipped */
+    float *p;                /* [n] fp32 parameters */
+    const void *g;           /* [n] g_io gradient */
+    void *m, *v;             /* [n] fp32 or e4m3 states */
+    float *m_scale, *v_scale; /* [ceil(n / 256)] with 8-bit states */
+    float *p_out;            /* where results go; NULL: in place */
+    void *m_out, *v_out;
+    float *m_scale_out, *v_scale_out;
+    void *copy;              /* [n] bf16: the new p rounded (written), or NULL */
+} naju_adamw_tensor_t;
+naju_status_t naju_adamw_step(int64_t n_tensors, const naju_adamw_tensor_t *tensors,
+                              int32_t g_io, int32_t state_bits, double lr, double beta1,
+                              double beta2, double eps, double weight_decay, int64_t step,
+                              const int32_t *step_dev, const float *lr_dev,
+                              const float *grad_scale, void *stream);
+
 /* Thread-local description of the last non-OK status ("" if none). */
 const char *naju_last_error(void);
 

@@ -9,6 +9,7 @@ fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import inspect
@@ -34,6 +35,7 @@ EXPORTS = ("naju_workspace_bytes", "naju_ckpt_bytes", "naju_workspace_init",
            "naju_embed_bwd", "naju_distill_fwd", "naju_distill_bwd", "naju_distill_fwd_bwd",
            "naju_logits_workspace_bytes", "naju_logits_process", "naju_w4_linear", "naju_w4_quantize",
            "naju_res_norm_fwd", "naju_res_norm_bwd_workspace_bytes", "naju_res_norm_bwd",
+           "naju_adamw_step",
            "naju_last_error", "naju_version")
 
 
@@ -47,6 +49,14 @@ class Dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("d_inner", ctypes.c_int64), ("d_state", ctypes.c_int64),
                 ("d_conv", ctypes.c_int32), ("io", ctypes.c_int32)]
+
+
+_ADAMW_FIELDS = ("p", "g", "m", "v", "m_scale", "v_scale", "p_out", "m_out", "v_out",
+                 "m_scale_out", "v_scale_out", "copy")
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64)] + [(k, ctypes.c_void_p) for k in _ADAMW_FIELDS]
 
 
 _lib = None
@@ -128,6 +138,10 @@ def lib() -> ctypes.CDLL:
         L.naju_res_norm_bwd.argtypes = ([i64, i64, i32, i32, i32] + [vp] * 8 + [f32] + [vp] * 7 +
                                         [sz, vp])
         L.naju_res_norm_bwd.restype = st
+        f64 = ctypes.c_double
+        L.naju_adamw_step.argtypes = ([i64, ctypes.POINTER(AdamwTensor), i32, i32] + [f64] * 5 +
+                                      [i64, vp, vp, vp, vp])
+        L.naju_adamw_step.restype = st
         L.naju_last_error.argtypes = []
         L.naju_last_error.restype = ctypes.c_char_p
         L.naju_version.argtypes = []
@@ -842,3 +856,90 @@ def res_norm_bwd(dxn, dx_new, x_new, y=None, z=None, *, scale=None, w_post=None,
                                   _p(out["dx"]), _p(out["dy"]), _p(out["dz"]), _p(out["dscale"]),
                                   _p(out["dw_post"]), _p(out["dw_pre"]), _p(scratch), nbytes, st))
     return out
+
+
+_dtype_of, _shape_of = torch.Tensor.dtype.__get__, torch.Tensor.shape.__get__
+
+
+def _one_value(t, name, dtype, dev):
+    if t.numel() != 1 or t.dtype != dtype or t.device != dev:
+        raise ValueError("%s must be one %s on %s" % (name, dtype, dev))
+    return t.data_ptr()
+
+
+def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
+               weight_decay=0.01, *, m_scale=None, v_scale=None, grad_scale=None, copies=None,
+               out=None):
+    """naju_adamw_step over lists of tensors, all on one device: params fp32; grads of their
+    shapes, all fp32 or all bf16; states m, v fp32, or float8_e4m3fn with m_scale, v_scale (fp32
+    [ceil(n / 256)]; v then holds the root of the second moment).  Updated in place, or with out
+    (a dict of lists p, m, v and, for 8-bit states, m_scale, v_scale) written there.  step: its
+    number from 1, or an int32 tensor that holds it; lr: a number or an fp32 tensor; grad_scale:
+    an fp32 tensor or None; copies: bf16 tensors that receive the new parameters, or None."""
+    n = len(params)
+    if n == 0:
+        return
+    dev = params[0].device
+    if dev.index is not None and dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return adamw_step(params, grads, m, v, step, lr, beta1, beta2, eps, weight_decay,
+                              m_scale=m_scale, v_scale=v_scale, grad_scale=grad_scale,
+                              copies=copies, out=out)
+    st = _stream(dev)
+    s_dt = m[0].dtype if len(m) else torch.float32
+    if s_dt not in (torch.float32, torch.float8_e4m3fn):
+        raise TypeError("states must be float32 or float8_e4m3fn, got %s" % s_dt)
+    eight = s_dt == torch.float8_e4m3fn
+    if eight != (m_scale is not None) or eight != (v_scale is not None):
+        raise ValueError("m_scale and v_scale go with 8-bit states")
+    g_dt = grads[0].dtype if len(grads) else torch.float32
+    io = _code(g_dt)
+    f32 = torch.float32
+    # the fields that are given: place in the table, name, tensors, type, whether of a scale's shape
+    lists = [(1, "p", params, f32, False), (2, "g", grads, g_dt, False), (3, "m", m, s_dt, False),
+             (4, "v", v, s_dt, False)]
+    if eight:
+        lists += [(5, "m_scale", m_scale, f32, True), (6, "v_scale", v_scale, f32, True)]
+    if out is not None:
+        names = ("p", "m", "v", "m_scale", "v_scale")[:5 if eight else 3]
+        if set(out) != set(names):
+            raise ValueError("out: expected the lists %s" % ", ".join(names))
+        lists += [(7 + i, k + "_out", out[k], (f32, s_dt, s_dt, f32, f32)[i], i > 2)
+                  for i, k in enumerate(names)]
+    if copies is not None:
+        lists.append((12, "copy", copies, torch.bfloat16, False))
+    # Checks over all tensors at once, property by property: 0.2 us a tensor, where checking
+    # tensor by tensor takes a microsecond.
+    T = torch.Tensor
+    sizes = list(map(T.numel, params))
+    blocks = [(k + 255) // 256 for k in sizes] if eight else None
+    every, types, counts = [], [], []
+    for _, k, ts, dt, of_blocks in lists:
+        if len(ts) != n:
+            raise ValueError("%s: expected %d tensors, got %d" % (k, n, len(ts)))
+        every += ts
+        types += [dt] * n
+        counts += blocks if of_blocks else sizes
+    fits = (list(map(_dtype_of, every)) == types and set(map(T.get_device, every)) == {dev.index}
+            and all(map(T.is_contiguous, every)) and list(map(T.numel, every)) == counts
+            and list(map(_shape_of, grads)) == list(map(_shape_of, params)))
+    if not fits:  # which one, and what is wrong with it
+        for _, k, ts, dt, of_blocks in lists:
+            for i, t in enumerate(ts):
+                shape = (blocks[i],) if of_blocks else params[i].shape if k == "g" else t.shape
+                _req(t, "%s[%d]" % (k, i), shape, dt, dev)
+                if t.numel() != (blocks if of_blocks else sizes)[i]:
+                    raise ValueError("%s[%d]: expected %d elements, got %d" %
+                                     (k, i, sizes[i], t.numel()))
+    addresses = array.array("Q", map(T.data_ptr, every))
+    table = array.array("Q", bytes(8 * 13 * n))
+    table[0::13] = array.array("Q", sizes)
+    for j, field in enumerate(lists):
+        table[field[0]::13] = addresses[j * n:(j + 1) * n]
+    table = ctypes.cast(table.buffer_info()[0], ctypes.POINTER(AdamwTensor)), table
+    step_dev = _one_value(step, "step", torch.int32, dev) if torch.is_tensor(step) else None
+    lr_dev = _one_value(lr, "lr", f32, dev) if torch.is_tensor(lr) else None
+    gs = _one_value(grad_scale, "grad_scale", f32, dev) if grad_scale is not None else None
+    check(lib().naju_adamw_step(n, table[0], io, 8 if eight else 32, 0.0 if lr_dev else float(lr),
+                                beta1, beta2, eps, weight_decay, 0 if step_dev else int(step),
+                                step_dev, lr_dev, gs, st))

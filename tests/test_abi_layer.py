@@ -100,3 +100,61 @@ def test_norm_definitions():
     g = layer.res_norm_bwd(d, None, x, w_pre=np.ones(50), eps=0.0)
     assert np.abs((g["dx"] * x).sum(1)).max() < 1e-12
     assert np.allclose(g["dw_pre"], (d * xn).sum(0))
+
+
+def test_adamw_refusals(lib):
+    def tensor(**kw):
+        t = dict(n=1000, p=FAKE, g=FAKE * 2, m=FAKE * 3, v=FAKE * 4, m_scale=FAKE * 5,
+                 v_scale=FAKE * 6)
+        t.update(kw)
+        return nb.AdamwTensor(**{k: v for k, v in t.items() if v is not None})
+
+    def call(*ts, n=None, io=nb.F32, bits=32, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, wd=0.1, step=1,
+             step_dev=None, lr_dev=None, gs=None):
+        table = (nb.AdamwTensor * max(1, len(ts)))(*ts)
+        return lib.naju_adamw_step(len(ts) if n is None else n, table, io, bits, lr, b1, b2, eps,
+                                   wd, step, step_dev, lr_dev, gs, None)
+    expect(call(n=-1), nb.EINVAL, "negative size")
+    expect(call(n=2 ** 25), nb.EINVAL, "too large")
+    expect(call(tensor(), io=5), nb.EINVAL, "io dtype")
+    expect(call(tensor(), bits=16), nb.EUNSUPPORTED, "state_bits")
+    for kw in (dict(b1=1.0), dict(b2=-0.1), dict(b1=float("nan"))):
+        expect(call(tensor(), **kw), nb.EINVAL, "beta")
+    expect(call(tensor(), eps=-1.0), nb.EINVAL, "eps")
+    expect(call(tensor(), lr=float("inf")), nb.EINVAL, "lr")
+    expect(call(tensor(), wd=float("nan")), nb.EINVAL, "weight_decay")
+    expect(call(tensor(), step=0), nb.EINVAL, "steps count from 1")
+    for k in ("step_dev", "lr_dev", "gs"):
+        expect(call(tensor(), **{k: FAKE + 2}), nb.EINVAL, "aligned")
+    for k in ("p", "g", "m", "v"):
+        expect(call(tensor(**{k: None})), nb.EINVAL, k + " is NULL")
+        expect(call(tensor(**{k: FAKE + 2})), nb.EINVAL, "aligned")
+    expect(call(tensor(n=-1)), nb.EINVAL, "elements")
+    expect(call(tensor(n=2 ** 43)), nb.EINVAL, "elements")
+    expect(call(tensor(m_scale=None), bits=8), nb.EINVAL, "m_scale is NULL")
+    expect(call(tensor(copy=FAKE + 1)), nb.EINVAL, "aligned")
+    # the same parameter twice, and two that overlap by one element
+    expect(call(tensor(), tensor()), nb.EINVAL, "overlap")
+    expect(call(tensor(p=FAKE + 4 * 999), tensor(p=2 * FAKE + 64), tensor()), nb.EINVAL, "overlap")
+    assert call() == nb.OK
+    assert call(tensor(n=0, p=None, g=None, m=None, v=None)) == nb.OK
+
+
+def test_adamw_binding_refusals(lib):
+    p = [torch.zeros(5)]
+    with pytest.raises(ValueError, match="GPU"):
+        nb.adamw_step(p, p, p, p, 1, 1e-3)
+    nb.adamw_step([], [], [], [], 1, 1e-3)
+
+
+def test_adamw_definition():
+    """One step from zero states moves every parameter by lr against its gradient's sign; zero
+    gradients leave weight decay alone; the 8-bit type's values."""
+    p, g = np.array([1.0, 2.0, 3.0]), np.array([0.5, -2.0, 1e-3])
+    q, m, v = layer.adamw(p, g, 0 * p, 0 * p, 1, 0.1, weight_decay=0.0, eps=0.0)
+    assert np.allclose(q, p - 0.1 * np.sign(g), rtol=1e-12)
+    q, _, _ = layer.adamw(p, 0 * g, 0 * p, 0 * p, 3, 0.1, weight_decay=0.5)
+    assert np.allclose(q, p * 0.95)
+    vals = layer.e4m3_values()
+    t = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(vals, t) and vals[-1] == 448
