@@ -531,6 +531,67 @@ naju_status_t naju_res_norm_bwd(int64_t tokens, int64_t d_model, int32_t io, int
                                 void *stream);
 
 /*
+ * Linear attention with a decay for each head, over sequences:
+ *     S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ *   q         [batch][seqlen][heads][d_key] io, k [..][kv_heads][d_key], v
+ *             [..][kv_heads][d_value]; ldq, ldk, ldv: elements from one token to
+ *             the next (parts of a joint projection), a multiple of 16 bytes; heads
+ *             h of q read the key and value of head h / (heads / kv_heads)
+ *   log_decay [heads] fp32, at most 0 (-inf: only the token itself); a constant of
+ *             the head, to which there is no gradient
+ *   state     [batch][heads][d_key][d_value] fp32 before the first token, or NULL
+ *             (= zeros);  state_out  after the last (written), or NULL; may be state
+ *   lengths   [batch] int32 (taken into [0, seqlen]) or NULL (= seqlen): tokens of a
+ *             row; what lies behind them is not read, and o is zero there
+ *   o         [batch][seqlen][heads][d_value] io (written)
+ *   ws        naju_linattn_fwd_workspace_bytes() bytes, 256-byte aligned (no initial
+ *             contents needed; 0 bytes: may be NULL)
+ * d_key, d_value multiples of 8 from 8 to 256; q, k, v, o (and the gradients) 16-byte
+ * aligned.  Sums and states are fp32.  A NaN or infinite input reaches its own row's
+ * head from up to 63 tokens before it on.
+ */
+size_t naju_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
+                                        int64_t kv_heads, int64_t d_key, int64_t d_value);
+naju_status_t naju_linattn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads,
+                               int64_t d_key, int64_t d_value, int32_t io, const void *q,
+                               int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                               const float *log_decay, const float *state, const int32_t *lengths,
+                               float scale, void *o, float *state_out, void *ws, size_t ws_bytes,
+                               void *stream);
+
+/*
+ * Its gradients, for the gradients dout of o and dstate_out of the last state (NULL:
+ * zeros).  dout [batch][seqlen][heads][d_value] io; what lies behind a row's length
+ * is not read.
+ *   dq, dk, dv  [batch][seqlen][heads or kv_heads][d] io, contiguous (written, zero
+ *             behind a row's length; those of a shared head are summed in fp32 over
+ *             its readers)
+ *   dstate    [batch][heads][d_key][d_value] fp32 (written), or NULL
+ *   ws        naju_linattn_bwd_workspace_bytes() bytes, as for the forward
+ */
+size_t naju_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
+                                        int64_t kv_heads, int64_t d_key, int64_t d_value);
+naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads,
+                               int64_t d_key, int64_t d_value, int32_t io, const void *q,
+                               int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                               const float *log_decay, const float *state, const int32_t *lengths,
+                               float scale, const void *dout, const float *dstate_out, void *dq,
+                               void *dk, void *dv, float *dstate, void *ws, size_t ws_bytes,
+                               void *stream);
+
+/*
+ * One token of it for every batch row: q [batch][heads][d_key], k, v
+ * [batch][kv_heads][..], o [batch][heads][d_value], contiguous.
+ *   state     as above, 16-byte aligned, read;  state_out  written, state itself for a
+ *             step in place, or another buffer that keeps the state before the token
+ * No workspace.
+ */
+naju_status_t naju_linattn_step(int64_t batch, int64_t heads, int64_t kv_heads, int64_t d_key,
+                                int64_t d_value, int32_t io, const void *q, const void *k,
+                                const void *v, const float *log_decay, const float *state,
+                                float scale, void *o, float *state_out, void *stream);
+
+/*
  * One AdamW step over a list of tensors.  Per element, with t the step's number:
  *     g = grad_scale g
  *     m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2

@@ -35,7 +35,8 @@ EXPORTS = ("naju_workspace_bytes", "naju_ckpt_bytes", "naju_workspace_init",
            "naju_embed_bwd", "naju_distill_fwd", "naju_distill_bwd", "naju_distill_fwd_bwd",
            "naju_logits_workspace_bytes", "naju_logits_process", "naju_w4_linear", "naju_w4_quantize",
            "naju_res_norm_fwd", "naju_res_norm_bwd_workspace_bytes", "naju_res_norm_bwd",
-           "naju_adamw_step",
+           "naju_adamw_step", "naju_linattn_fwd_workspace_bytes", "naju_linattn_fwd",
+           "naju_linattn_bwd_workspace_bytes", "naju_linattn_bwd", "naju_linattn_step",
            "naju_last_error", "naju_version")
 
 
@@ -142,6 +143,16 @@ def lib() -> ctypes.CDLL:
         L.naju_adamw_step.argtypes = ([i64, ctypes.POINTER(AdamwTensor), i32, i32] + [f64] * 5 +
                                       [i64, vp, vp, vp, vp])
         L.naju_adamw_step.restype = st
+        for name in ("naju_linattn_fwd_workspace_bytes", "naju_linattn_bwd_workspace_bytes"):
+            getattr(L, name).argtypes = [i64] * 6
+            getattr(L, name).restype = sz
+        lin = [i64] * 6 + [i32] + [vp, i64] * 3 + [vp] * 3 + [f32]
+        L.naju_linattn_fwd.argtypes = lin + [vp, vp, vp, sz, vp]
+        L.naju_linattn_fwd.restype = st
+        L.naju_linattn_bwd.argtypes = lin + [vp] * 7 + [sz, vp]
+        L.naju_linattn_bwd.restype = st
+        L.naju_linattn_step.argtypes = [i64] * 5 + [i32] + [vp] * 5 + [f32] + [vp] * 3
+        L.naju_linattn_step.restype = st
         L.naju_last_error.argtypes = []
         L.naju_last_error.restype = ctypes.c_char_p
         L.naju_version.argtypes = []
@@ -943,3 +954,119 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
     check(lib().naju_adamw_step(n, table[0], io, 8 if eight else 32, 0.0 if lr_dev else float(lr),
                                 beta1, beta2, eps, weight_decay, 0 if step_dev else int(step),
                                 step_dev, lr_dev, gs, st))
+
+
+def _req_tokens(t, name, shape, dtype, device) -> int:
+    """A tensor [batch, tokens, heads, d] whose tokens' heads are contiguous and whose tokens lie
+    any one distance apart (a part of a joint projection); returns that distance."""
+    if t is None:
+        raise ValueError("%s is required" % name)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
+    if t.dtype != dtype:
+        raise TypeError("%s: expected %s, got %s" % (name, dtype, t.dtype))
+    if t.device != device:
+        raise ValueError("%s must be on %s" % (name, device))
+    B, L, H, d = shape
+    if t.is_contiguous():
+        return H * d
+    sb, sl, sh, sd = t.stride()
+    if L == 1:
+        sl = sb if B > 1 else H * d
+    if sd != 1 or (H > 1 and sh != d) or sl < H * d or (B > 1 and sb != L * sl):
+        raise ValueError("%s: a token's heads must be contiguous and tokens equally far apart"
+                         % name)
+    return sl
+
+
+def _linattn_args(q, k, v, log_decay, state, lengths, scale):
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v must be [batch, tokens, heads, d]")
+    B, L, H, dk = q.shape
+    Hk, dv = k.shape[2], v.shape[3]
+    dt, dev = q.dtype, q.device
+    io, st = _io_of(q), _stream(dev)
+    ldq = _req_tokens(q, "q", (B, L, H, dk), dt, dev)
+    ldk = _req_tokens(k, "k", (B, L, Hk, dk), dt, dev)
+    ldv = _req_tokens(v, "v", (B, L, Hk, dv), dt, dev)
+    _req(log_decay, "log_decay", (H,), torch.float32, dev)
+    _opt(state, "state", (B, H, dk, dv), torch.float32, dev)
+    _opt(lengths, "lengths", (B,), torch.int32, dev)
+    sizes = (B, L, H, Hk, dk, dv)
+    return sizes, dt, dev, st, sizes + (
+        io, _p(q), ldq, _p(k), ldk, _p(v), ldv, _p(log_decay), _p(state), _p(lengths),
+        dk ** -0.5 if scale is None else float(scale))
+
+
+def _linattn_scratch(nbytes, ws, dev):
+    if ws is not None:
+        return ws.tensor.data_ptr(), ws.nbytes, ws
+    scratch = _scratch(nbytes, dev) if nbytes > 0 else None
+    return _p(scratch), nbytes, scratch
+
+
+@_on_its_device
+def linattn_fwd(q, k, v, log_decay, state=None, lengths=None, scale=None, *, state_out=None,
+                ws=None):
+    """o, state_out = naju_linattn_fwd(...): S_t = exp(log_decay) S_{t-1} + k_t v_t^T and o_t =
+    scale S_t^T q_t over the tokens of each row.  q [batch, tokens, heads, d_key], k and v
+    [batch, tokens, kv_heads, ..] (heads a multiple of kv_heads; tokens any equal distance apart);
+    log_decay fp32 [heads], at most 0; state fp32 [batch, heads, d_key, d_value] or None (zeros);
+    lengths int32 [batch] or None; scale: d_key ** -0.5 if None.  state_out: a tensor to write, state
+    itself among them."""
+    (B, L, H, Hk, dk, dv), dt, dev, st, args = _linattn_args(q, k, v, log_decay, state, lengths,
+                                                              scale)
+    o = torch.empty((B, L, H, dv), dtype=dt, device=dev)
+    if state_out is None:
+        state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    else:
+        _req(state_out, "state_out", (B, H, dk, dv), torch.float32, dev)
+    nbytes = lib().naju_linattn_fwd_workspace_bytes(B, L, H, Hk, dk, dv) if ws is None else 0
+    p, nbytes, keep = _linattn_scratch(nbytes, ws, dev)
+    check(lib().naju_linattn_fwd(*args, _p(o), _p(state_out), p, nbytes, st))
+    return o, state_out
+
+
+@_on_its_device
+def linattn_bwd(q, k, v, log_decay, do, state=None, dstate=None, lengths=None, scale=None, *,
+                ws=None):
+    """Gradients of naju_linattn_fwd for the gradients do of o and dstate of the last state (or
+    None): dict(dq, dk, dv, dstate), contiguous; dstate is that of the state before the first
+    token."""
+    (B, L, H, Hk, dk, dv), dt, dev, st, args = _linattn_args(q, k, v, log_decay, state, lengths,
+                                                              scale)
+    _req(do, "do", (B, L, H, dv), dt, dev)
+    _opt(dstate, "dstate", (B, H, dk, dv), torch.float32, dev)
+    out = {"dq": torch.empty((B, L, H, dk), dtype=dt, device=dev),
+           "dk": torch.empty((B, L, Hk, dk), dtype=dt, device=dev),
+           "dv": torch.empty((B, L, Hk, dv), dtype=dt, device=dev),
+           "dstate": torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)}
+    nbytes = lib().naju_linattn_bwd_workspace_bytes(B, L, H, Hk, dk, dv) if ws is None else 0
+    p, nbytes, keep = _linattn_scratch(nbytes, ws, dev)
+    check(lib().naju_linattn_bwd(*args, _p(do), _p(dstate), _p(out["dq"]), _p(out["dk"]),
+                                 _p(out["dv"]), _p(out["dstate"]), p, nbytes, st))
+    return out
+
+
+@_on_its_device
+def linattn_step(q, k, v, log_decay, state, scale=None, *, state_out=None):
+    """o = naju_linattn_step(...): one token, q [batch, heads, d_key], k and v [batch, kv_heads, ..].
+    state fp32 [batch, heads, d_key, d_value] is updated in place, or with state_out kept and the
+    new one written there."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [batch, heads, d]")
+    B, H, dk = q.shape
+    Hk, dv = k.shape[1], v.shape[2]
+    dt, dev = q.dtype, q.device
+    io, st = _io_of(q), _stream(dev)
+    _req(q, "q", (B, H, dk), dt, dev)
+    _req(k, "k", (B, Hk, dk), dt, dev)
+    _req(v, "v", (B, Hk, dv), dt, dev)
+    _req(log_decay, "log_decay", (H,), torch.float32, dev)
+    _req(state, "state", (B, H, dk, dv), torch.float32, dev)
+    _opt(state_out, "state_out", (B, H, dk, dv), torch.float32, dev)
+    o = torch.empty((B, H, dv), dtype=dt, device=dev)
+    check(lib().naju_linattn_step(B, H, Hk, dk, dv, io, _p(q), _p(k), _p(v), _p(log_decay),
+                                  _p(state), dk ** -0.5 if scale is None else float(scale), _p(o),
+                                  _p(state if state_out is None else state_out), st))
+    return o

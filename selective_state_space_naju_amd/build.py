@@ -21,7 +21,7 @@ SOURCES = ["naju_api.hip", "naju_fwd.hip", "naju_fwd_mfma.hip", "naju_fwd_mfma64
            "naju_bwd_mfma.hip",
            "naju_step.hip", "naju_mixer.hip", "naju_embed.hip",
            "naju_distill.hip", "naju_logits.hip", "naju_w4.hip",
-           "naju_norm.hip", "naju_adamw.hip"]
+           "naju_norm.hip", "naju_adamw.hip", "naju_linattn.hip"]
 ARCH = os.environ.get("NAJU_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,1053 @@
+// naju_linattn.hip -- linear attention with a decay for each head: chunked for
+// prompts and training (forward and gradients), recurrent for single tokens.
+//
+//     S_t = l S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   l = exp(log_decay)
+// Over a chunk of tokens that the state S enters, i and j counted from 0:
+//     O_i = scale ( sum_{j <= i} l^{i-j} (q_i . k_j) v_j + l^{i+1} S^T q_i )
+//     S'  = l^T S + sum_j l^{T-1-j} k_j v_j^T
+// so all of it is matrix products; powers of l are formed from differences of
+// positions and never exceed 1 for l <= 1.
+//
+// The gradients are the same walk with other operands.  With G = dO:
+//     dq_i = scale sum_{j <= i} l^{i-j} (G_i . v_j) k_j + ...   (G, v, k), state S^T
+//     dv_j = scale sum_{i >= j} l^{i-j} (k_j . q_i) G_i + ...   (k, q, G), back in time
+//     dk_j = scale sum_{i >= j} l^{i-j} (v_j . G_i) q_i + ...   (v, G, q), back in time
+// where the state walking back is M <- l (M + scale q_t G_t^T), from the gradient of
+// the last state to that of the first: it enters a chunk already decayed, so its
+// powers of l are one lower than the forward walk's (`late` 0 in place of 1).
+//
+// One workgroup walks one head of one batch row over a stretch of chunks, for 64 or
+// 128 of the value columns, with its part of the state in the accumulators of its
+// four waves from chunk to chunk.  A wave owns 16 CT columns: the state's tiles come
+// out of the matrix instruction with a column in each lane and four rows in its
+// registers, which is also the layout of an operand, so the product with q reads the
+// state from registers.  Scores are shared through LDS.  Where heads and rows are too
+// few for the CUs the sequence is cut into segments: their own contributions to the
+// state first, the entering states from those, then the walk over all segments at
+// once.
+//
+// bf16: v_mfma_f32_16x16x32_bf16 with fp32 sums; scores and state enter products as
+// bf16 hi + lo (2^-16), the decayed values of the state's sum in three bf16 parts
+// (fp32's precision: the state is an fp32 output).  fp32: v_mfma_f32_16x16x4_f32.
+#include <math.h>
+
+#include "naju_device.h"
+#include "naju_host.h"
+#include "naju_launch.h"
+#include "naju_vec.h"
+
+namespace naju {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kLinMost = 256;      // elements of a head's keys or values
+constexpr int kLinThreads = 256;
+
+// One walk.  The names are the forward's: q reads, k and v are summed into the state.
+struct LinJob {
+    const void *q, *k, *v;
+    void *o;
+    const float *enter;      // states entering the segments, or the first; null: zeros
+    float *leave;            // segments' contributions, or the last state; may be null
+    int64_t ldq, ldk, ldv, ldo;         // elements from token to token
+    int64_t enter_bh, enter_seg, leave_bh, leave_seg;
+    int enter_r, enter_c, leave_r, leave_c;  // element (row, column) of a state
+    int D1, D2;              // rows (q's and k's elements) and columns (v's) of the state
+    int gq, gk, gv;          // heads that share one of q, k, v
+    float s_row, s_pair, s_tok;         // scales of S^T q, of the scores, of k v^T
+    int late;
+    int back;                // 1: from each row's last token to its first
+    int out_f32;             // o is fp32 whatever the io type
+};
+
+struct LinArgs {
+    LinJob job[3];
+    const float *log_decay;
+    const int32_t *lengths;
+    int B, H, slices, nseg, seg;        // seg: tokens of a segment
+    int64_t L;
+};
+
+// ------------------------------------------------------- operands of the products
+// 8 elements of a row (or column) of an operand in a lane: the lane's row is l % 16, its slots
+// 8 (l / 16) .. + 7 of 32.  Both operands of a product take the same elements in the same slots.
+template <typename T> struct Frag;
+
+template <> struct Frag<bf16> {
+    bf16x8 f;
+    __device__ __forceinline__ void row(const bf16 *p) { f = *(const bf16x8 *)p; }
+    // Transposed: element j of the lane is column `col` of the lane of row 4 (j % 4) + 16 (j / 4)
+    // behind its first.  ds_read_tr16_b64: lane i of 16 hands in row i / 4 (of four) and columns
+    // 4 (i % 4) .. + 3 of its choice, and receives column i of all four rows.
+    __device__ __forceinline__ void cols(const bf16 *p, int stride)
+    {
+        typedef __attribute__((address_space(3))) s16x4 lds4;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds4 *)(__attribute__((address_space(3))) const bf16 *)p);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds4 *)(__attribute__((address_space(3))) const bf16 *)(p + 16 * stride));
+        const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
+        f = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const u32x4 w = __builtin_bit_cast(u32x4, f);
+        return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+};
+template <> struct Frag<float> {
+    float f[8];
+    __device__ __forceinline__ void row(const float *p)
+    {
+        const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = a[i];
+            f[4 + i] = b[i];
+        }
+    }
+    // (no transposing read for 32-bit elements: the lane reads its own column)
+    __device__ __forceinline__ void cols(const float *p, int stride)
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = p[4 * j * stride];
+    }
+    __device__ __forceinline__ float get(int i) const { return f[i]; }
+};
+
+__device__ __forceinline__ f32x4 mma(const Frag<bf16> &a, const Frag<bf16> &b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.f, b.f, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(const Frag<float> &a, const Frag<float> &b, f32x4 c)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.f[j], b.f[j], c, 0, 0, 0);
+    return c;
+}
+
+// fp32 values as an operand: P bf16 parts whose sum holds 8 P bits (the first ones cut off, the
+// last one rounded), or fp32 as they are
+template <typename T, int P> struct Parts;
+template <int P> struct Parts<bf16, P> {
+    Frag<bf16> p[P];
+    __device__ __forceinline__ void set(const float (&v)[8])
+    {
+        float r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = v[i];
+#pragma unroll
+        for (int n = 0; n < P; ++n) {
+            if (n == P - 1) {
+                Run<bf16, 8> w = round_run<bf16, 8>(r);
+                p[n].f = __builtin_bit_cast(bf16x8, w.w);
+            } else {
+                u32x4 h;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t b0 = __float_as_uint(r[2 * i]);
+                    const uint32_t b1 = __float_as_uint(r[2 * i + 1]);
+                    h[i] = __builtin_amdgcn_perm(b1, b0, 0x07060302u);
+                    r[2 * i] -= __uint_as_float(b0 & 0xffff0000u);
+                    r[2 * i + 1] -= __uint_as_float(b1 & 0xffff0000u);
+                }
+                p[n].f = __builtin_bit_cast(bf16x8, h);
+            }
+        }
+    }
+};
+template <int P> struct Parts<float, P> {
+    Frag<float> p[1];
+    __device__ __forceinline__ void set(const float (&v)[8])
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[0].f[i] = v[i];
+    }
+};
+template <typename T, int P>
+__device__ __forceinline__ f32x4 mma(const Parts<T, P> &a, const Frag<T> &b, f32x4 c)
+{
+    constexpr int n = sizeof(T) == 2 ? P : 1;
+#pragma unroll
+    for (int i = n - 1; i >= 0; --i) c = mma(a.p[i], b, c);
+    return c;
+}
+template <typename T, int P>
+__device__ __forceinline__ f32x4 mma(const Frag<T> &a, const Parts<T, P> &b, f32x4 c)
+{
+    constexpr int n = sizeof(T) == 2 ? P : 1;
+#pragma unroll
+    for (int i = n - 1; i >= 0; --i) c = mma(a, b.p[i], c);
+    return c;
+}
+
+// A tile of rows on its way from HBM to LDS: 16 bytes at a time, zeros behind the sequence's
+// and the head's ends.
+template <typename T, int ROWS, int COLS> struct Stage {
+    static constexpr int E = 16 / (int)sizeof(T);
+    static constexpr int kPerRow = COLS / E;
+    static constexpr int N = ROWS * kPerRow / kLinThreads;  // accesses of a thread
+    static_assert(ROWS * kPerRow % kLinThreads == 0, "whole accesses");
+    static constexpr int kStride = COLS + E;  // (rows lie 16 bytes further in the banks)
+    u32x4 r[N];
+
+    // tokens n0 .. of a row with `len` of them; D: elements of a row from column c0 on
+    __device__ __forceinline__ void fetch(const T *p, int64_t ld, int64_t n0, int64_t len,
+                                          bool back, int D, int tid)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = tid + i * kLinThreads, row = at / kPerRow, col = at % kPerRow * E;
+            int64_t n = n0 + row;
+            n = n < len ? n : len - 1;
+            const int64_t t = back ? len - 1 - n : n;
+            const int c = col < D ? col : 0;
+            r[i] = *(const u32x4 *)(p + t * ld + c);
+        }
+    }
+    __device__ __forceinline__ void put(T *lds, int64_t n0, int64_t len, int D, int tid) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = tid + i * kLinThreads, row = at / kPerRow, col = at % kPerRow * E;
+            const bool in = n0 + row < len && col < D;
+            const u32x4 zero = {0u, 0u, 0u, 0u};
+            *(u32x4 *)(lds + row * kStride + col) = in ? r[i] : zero;
+        }
+    }
+};
+
+template <typename T, int KD, int CT> struct LinShape {
+    static constexpr int TT = sizeof(T) == 2 ? 64 : 32;  // tokens of a chunk
+    static constexpr int VC = 64 * CT;                   // columns of a workgroup
+    using SK = Stage<T, TT, KD>;
+    using SV = Stage<T, TT, VC>;
+    static constexpr int E = 16 / (int)sizeof(T);
+    static constexpr int kScores = TT + E;               // stride of the scores
+    static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
+    static constexpr size_t bytes(bool out)
+    {
+        return sizeof(T) * ((out ? 2 : 1) * TT * SK::kStride + TT * SV::kStride +
+                            (out ? kParts * TT * kScores : 0));
+    }
+};
+
+// The token that stands in position m of 16 where an operand's slots are tokens: rows 4 apart are
+// read together by the transposing reads, which then meet no bank twice.
+__device__ __forceinline__ int token_of(int m) { return (m >> 2) + 4 * (m & 3); }
+
+// OUT: the walk, with outputs; else a segment's contribution to the state alone.
+template <typename T, int KD, int CT, bool OUT>
+__global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel(const LinArgs g)
+{
+    using Sh = LinShape<T, KD, CT>;
+    constexpr int TT = Sh::TT, VC = Sh::VC, IT = TT / 16, KS = TT / 32, KB = KD / 32;
+    constexpr int QS = Sh::SK::kStride, VS = Sh::SV::kStride, PS = Sh::kScores;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    T *vs = (T *)lds, *ks = vs + TT * VS, *qs = ks + TT * QS;
+    T *ps = qs + TT * QS;  // [parts][TT][PS]
+
+    const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, h4 = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const LinJob &J = g.job[blockIdx.y];
+    int id = blockIdx.x;
+    const int slice = id % g.slices;
+    id /= g.slices;
+    const int seg = id % g.nseg;
+    id /= g.nseg;
+    const int hd = id % g.H, b = id / g.H;
+    const int c0 = slice * VC;
+    if (c0 >= J.D2) return;
+    const int D1 = J.D1, D2 = J.D2 - c0 < VC ? J.D2 - c0 : VC;  // of this workgroup
+    const int64_t L = g.L;
+    int64_t len = g.lengths != nullptr ? g.lengths[b] : L;
+    len = len < 0 ? 0 : len < L ? len : L;
+    const bool back = J.back != 0;
+    const int late = J.late;
+    // log2 of the decay; below -1e30 it is 0 after one step, and 0 * -1e30 stays 0
+    float a2 = g.log_decay[hd];
+    a2 = (a2 < -1e30f ? -1e30f : a2) * kLog2e;
+
+    const T *q = (const T *)J.q + (int64_t)b * L * J.ldq + (int64_t)(hd / J.gq) * D1;
+    const T *k = (const T *)J.k + (int64_t)b * L * J.ldk + (int64_t)(hd / J.gk) * D1;
+    const T *v = (const T *)J.v + (int64_t)b * L * J.ldv + (int64_t)(hd / J.gv) * J.D2 + c0;
+
+    // this lane's columns of the state: 4 CT neighbouring lanes' tiles interleave, so that a
+    // lane's outputs of one token are 4 CT consecutive elements
+    auto column = [&](int ct) { return 16 * CT * w + 4 * CT * (m >> 2) + 4 * ct + (m & 3); };
+    // rows of the state: register r of tile 2 kb + a is row 32 kb + 8 h4 + 4 a + r
+    f32x4 S[CT][2 * KB];
+    {
+        const float *e = J.enter;
+        if (e != nullptr)
+            e += (int64_t)(b * g.H + hd) * J.enter_bh + (int64_t)seg * J.enter_seg;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int kt = 0; kt < 2 * KB; ++kt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * (kt & ~1) + 8 * h4 + 4 * (kt & 1) + r;
+                    const int col = column(ct);
+                    float s = 0.f;
+                    if (OUT && e != nullptr && row < D1 && col < D2)
+                        s = e[(int64_t)row * J.enter_r + (int64_t)(c0 + col) * J.enter_c];
+                    S[ct][kt][r] = s;
+                }
+    }
+    float lead[IT];  // of S^T q, for this lane's token of each tile
+    if constexpr (OUT) {
+#pragma unroll
+        for (int it = 0; it < IT; ++it) lead[it] = J.s_row * ex2(a2 * (float)(16 * it + m + late));
+    }
+
+    const int64_t first = (int64_t)seg * g.seg;
+    const int64_t end = first + g.seg < L ? first + g.seg : L;      // tokens of this segment
+    const int64_t stop = end < len ? end : len;                     // those that there are
+    typename Sh::SK rq, rk;
+    typename Sh::SV rv;
+    auto fetch = [&](int64_t n0) {
+        if constexpr (OUT) rq.fetch(q, J.ldq, n0, len, back, D1, tid);
+        rk.fetch(k, J.ldk, n0, len, back, D1, tid);
+        rv.fetch(v, J.ldv, n0, len, back, D2, tid);
+    };
+    if (first < stop) fetch(first);
+    for (int64_t n0 = first; n0 < stop; n0 += TT) {
+        __syncthreads();  // (the chunk before has been read)
+        if constexpr (OUT) rq.put(qs, n0, len, D1, tid);
+        rk.put(ks, n0, len, D1, tid);
+        rv.put(vs, n0, len, D2, tid);
+        if (n0 + TT < stop) fetch(n0 + TT);
+        __syncthreads();
+        const int there = stop - n0 < TT ? (int)(stop - n0) : TT;
+
+        if constexpr (OUT) {
+            // scores of 16 tokens i, transposed: positions of tokens j in a lane's registers
+            if (w < IT) {
+                Frag<T> fq[KB];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) fq[kb].row(qs + (16 * w + m) * QS + 32 * kb + 8 * h4);
+                const int i = 16 * w + m;
+                for (int jt = 0; jt < 2 * (w / 2) + 2; ++jt) {
+                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (jt <= w) {
+                        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int kb = 0; kb < KB; ++kb) {
+                            Frag<T> fk;
+                            fk.row(ks + (16 * jt + token_of(m)) * QS + 32 * kb + 8 * h4);
+                            acc = mma(fk, fq[kb], acc);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int gap = i - (16 * jt + h4 + 4 * r);
+                            const float p = acc[r] * (J.s_pair * ex2(a2 * (float)gap));
+                            s[r] = gap >= 0 ? p : 0.f;
+                        }
+                    }
+                    T *to = ps + i * PS + 32 * (jt / 2) + 8 * h4 + 4 * (jt & 1);
+                    if constexpr (sizeof(T) == 2) {
+                        float lo[4];
+                        uint32_t hi[2];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            lo[r] = s[r] - __uint_as_float(__float_as_uint(s[r]) & 0xffff0000u);
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+                            hi[r] = __builtin_amdgcn_perm(__float_as_uint(s[2 * r + 1]),
+                                                          __float_as_uint(s[2 * r]), 0x07060302u);
+                        __builtin_memcpy(__builtin_assume_aligned(to, 8), hi, 8);
+                        const Run<bf16, 4> l = round_run<bf16, 4>(lo);
+                        __builtin_memcpy(__builtin_assume_aligned(to + TT * PS, 8), l.w, 8);
+                    } else {
+                        *(f32x4 *)to = f32x4{s[0], s[1], s[2], s[3]};
+                    }
+                }
+            }
+            __syncthreads();
+        }
+
+        // values: this wave's columns, slots = tokens
+        Frag<T> fv[CT][KS];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                if constexpr (sizeof(T) == 2)
+                    fv[ct][s].cols(vs + (32 * s + h4 + 4 * (m >> 2)) * VS + 16 * CT * w +
+                                       4 * CT * (m & 3) + 4 * ct, VS);
+                else
+                    fv[ct][s].cols(vs + (32 * s + h4) * VS + column(ct), VS);
+            }
+
+        if constexpr (OUT) {
+            f32x4 o[IT][CT];
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) o[it][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                Parts<T, 2> st[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    float x[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) x[r] = S[ct][2 * kb + r / 4][r % 4];
+                    st[ct].set(x);
+                }
+#pragma unroll
+                for (int it = 0; it < IT; ++it) {
+                    Frag<T> fq;
+                    fq.row(qs + (16 * it + m) * QS + 32 * kb + 8 * h4);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) o[it][ct] = mma(st[ct], fq, o[it][ct]);
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < IT; ++it) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) o[it][ct] *= lead[it];
+#pragma unroll
+                for (int s = 0; s <= it / 2; ++s) {
+                    Parts<T, 2> fp;
+#pragma unroll
+                    for (int n = 0; n < Sh::kParts; ++n)
+                        fp.p[n].row(ps + n * TT * PS + (16 * it + m) * PS + 32 * s + 8 * h4);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) o[it][ct] = mma(fv[ct][s], fp, o[it][ct]);
+                }
+                const int64_t n = n0 + 16 * it + m;
+                if (n < stop) {
+                    const int64_t t = back ? len - 1 - n : n;
+                    const int col = 16 * CT * w + 4 * CT * h4;
+                    float x[4 * CT];
+#pragma unroll
+                    for (int i = 0; i < 4 * CT; ++i) x[i] = o[it][i / 4][i % 4];
+                    const int64_t at = ((int64_t)b * L + t) * J.ldo + (int64_t)hd * J.D2 + c0 + col;
+                    if (col < D2) {  // (D2 is a multiple of 8, and so is what a lane stores)
+                        if (sizeof(T) == 4 || J.out_f32) {
+#pragma unroll
+                            for (int i = 0; i < CT; ++i)
+                                *(f32x4 *)((float *)J.o + at + 4 * i) =
+                                    f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+                        } else {
+                            const Run<bf16, 4 * CT> run = round_run<bf16, 4 * CT>(x);
+                            __builtin_memcpy(__builtin_assume_aligned((bf16 *)J.o + at, 8 * CT),
+                                             run.w, 8 * CT);
+                        }
+                    }
+                }
+            }
+        }
+
+        // the state behind the chunk
+        const float fade = ex2(a2 * (float)there);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int kt = 0; kt < 2 * KB; ++kt) S[ct][kt] *= fade;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            Parts<T, 3> vd[CT];
+            float tok[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int left = there - late - (32 * s + h4 + 4 * j);
+                tok[j] = J.s_tok * ex2(a2 * (float)(left > 0 ? left : 0));
+            }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                float x[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = fv[ct][s].get(j) * tok[j];
+                vd[ct].set(x);
+            }
+#pragma unroll
+            for (int kt = 0; kt < 2 * KB; ++kt) {
+                Frag<T> fk;
+                if constexpr (sizeof(T) == 2)
+                    fk.cols(ks + (32 * s + h4 + 4 * (m >> 2)) * QS + 16 * (kt & ~1) + 8 * (m & 3) +
+                                4 * (kt & 1), QS);
+                else
+                    fk.cols(ks + (32 * s + h4) * QS + 16 * (kt & ~1) + 8 * (m >> 2) + 4 * (kt & 1) +
+                                (m & 3), QS);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) S[ct][kt] = mma(fk, vd[ct], S[ct][kt]);
+            }
+        }
+    }
+
+    if constexpr (OUT) {
+        // rows behind a sequence's last token
+        const int64_t z0 = first > len ? first : len;
+        if (z0 < end) {
+            const int per = D2 / 8;
+            for (int64_t i = tid; i < (end - z0) * per; i += kLinThreads) {
+                const int64_t t = z0 + i / per;
+                const int64_t at = ((int64_t)b * L + t) * J.ldo + (int64_t)hd * J.D2 + c0 +
+                                   i % per * 8;
+                const u32x4 zero = {0u, 0u, 0u, 0u};
+                if (sizeof(T) == 4 || J.out_f32) {
+                    ((u32x4 *)((float *)J.o + at))[0] = zero;
+                    ((u32x4 *)((float *)J.o + at))[1] = zero;
+                } else {
+                    *(u32x4 *)((bf16 *)J.o + at) = zero;
+                }
+            }
+        }
+    }
+    if (J.leave == nullptr || (OUT && seg != g.nseg - 1)) return;
+    float *e = J.leave + (int64_t)(b * g.H + hd) * J.leave_bh + (int64_t)seg * J.leave_seg;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+        for (int kt = 0; kt < 2 * KB; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * (kt & ~1) + 8 * h4 + 4 * (kt & 1) + r, col = column(ct);
+                if (row < D1 && col < D2)
+                    e[(int64_t)row * J.leave_r + (int64_t)(c0 + col) * J.leave_c] = S[ct][kt][r];
+            }
+}
+
+// Segments' contributions -> the states that enter them, in place: [B H][nseg][D1 D2].
+struct LinJoin {
+    float *seg[2];
+    const float *enter[2];   // the first state, or null
+    int enter_r[2], enter_c[2];
+    int cols[2];             // D2: elements of a row
+};
+__global__ __launch_bounds__(256) void linattn_join_kernel(const LinJoin j, const float *log_decay,
+                                                           const int32_t *lengths, int H, int n,
+                                                           int nseg, int seg, int64_t L)
+{
+    const int i = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y, q = blockIdx.z;
+    if (i >= n) return;
+    const int b = bh / H;
+    int64_t len = lengths != nullptr ? lengths[b] : L;
+    len = len < 0 ? 0 : len < L ? len : L;
+    float a2 = log_decay[bh % H];
+    a2 = (a2 < -1e30f ? -1e30f : a2) * kLog2e;
+    float x = 0.f;
+    if (j.enter[q] != nullptr)
+        x = j.enter[q][(int64_t)bh * n + (int64_t)(i / j.cols[q]) * j.enter_r[q] +
+                       (int64_t)(i % j.cols[q]) * j.enter_c[q]];
+    float *p = j.seg[q] + (int64_t)bh * nseg * n + i;
+    for (int s0 = 0; s0 < nseg; s0 += 8) {  // (eight at a time: loads ahead of the stores)
+        float own[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            own[i] = s0 + i < nseg - 1 ? p[(int64_t)(s0 + i) * n] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t left = len - (int64_t)(s0 + i) * seg;
+            const int64_t there = left < 0 ? 0 : left < seg ? left : seg;
+            if (s0 + i < nseg) p[(int64_t)(s0 + i) * n] = x;
+            x = x * ex2(a2 * (float)there) + own[i];
+        }
+    }
+}
+
+// Sums over the heads that share a key or a value: [tokens][Hk][group][D] -> [tokens][Hk][D].
+template <typename T>
+__global__ __launch_bounds__(256) void linattn_group_kernel(const float *x, T *out, int64_t n,
+                                                            int group, int D)
+{
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;  // of the output
+    if (i >= n) return;
+    const int64_t row = i / D;
+    const float *p = x + row * group * D + i % D;
+    f32x4 s = *(const f32x4 *)p;
+    for (int g = 1; g < group; ++g) s += *(const f32x4 *)(p + (int64_t)g * D);
+    const float f[4] = {s[0], s[1], s[2], s[3]};
+    round_run<T, 4>(f).store(out + i);
+}
+
+// --------------------------------------------------------------------- one token
+// A workgroup takes 32 columns of one head's state: 8 lanes of 4 columns, 32 rows at a time.
+template <typename T>
+__global__ __launch_bounds__(256) void linattn_step_kernel(int H, int group, int D1, int D2,
+                                                           const T *q, const T *k, const T *v,
+                                                           const float *log_decay, float scale,
+                                                           const float *state, float *state_out,
+                                                           T *o)
+{
+    __shared__ f32x4 part[4][8];
+    const int tid = threadIdx.x, c4 = tid & 7, r0 = tid >> 3;
+    const int hd = blockIdx.y % H, b = blockIdx.y / H, Hk = H / group;
+    const int col = blockIdx.x * 32 + 4 * c4;
+    const bool in = col < D2;
+    const int64_t bh = (int64_t)b * H + hd, kv = (int64_t)b * Hk + hd / group;
+    const float lam = ex2(log_decay[hd] * kLog2e);
+    f32x4 x = {0.f, 0.f, 0.f, 0.f}, acc = x;
+    const int64_t base = bh * D1 * D2 + col;
+    if (in) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = to_f(v[kv * D2 + col + i]);
+    }
+    f32x4 s[kLinMost / 32];
+    float kf[kLinMost / 32], qf[kLinMost / 32];
+#pragma unroll
+    for (int i = 0; i < kLinMost / 32; ++i) {
+        const int row = r0 + 32 * i;
+        if (in && row < D1) {
+            s[i] = *(const f32x4 *)(state + base + (int64_t)row * D2);
+            kf[i] = to_f(k[kv * D1 + row]);
+            qf[i] = to_f(q[bh * D1 + row]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kLinMost / 32; ++i) {
+        const int row = r0 + 32 * i;
+        if (in && row < D1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[i][e] = __builtin_fmaf(s[i][e], lam, kf[i] * x[e]);
+                acc[e] = __builtin_fmaf(qf[i], s[i][e], acc[e]);
+            }
+            *(f32x4 *)(state_out + base + (int64_t)row * D2) = s[i];
+        }
+    }
+    // over the rows: lanes 8, 16 and 32 apart, then the waves
+#pragma unroll
+    for (int d = 8; d < 64; d <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], d);
+    if ((tid & 63) < 8) part[tid >> 6][c4] = acc;
+    __syncthreads();
+    if (tid < 8 && in) {
+        const f32x4 y = ((part[0][c4] + part[1][c4]) + (part[2][c4] + part[3][c4])) * scale;
+        const float f[4] = {y[0], y[1], y[2], y[3]};
+        round_run<T, 4>(f).store(o + bh * D2 + col);
+    }
+}
+
+// ---------------------------------------------------------------------- host
+template <typename T, int KD, int CT, bool OUT>
+static hipError_t launch_walk(const LinArgs &g, int jobs, hipStream_t st)
+{
+    const int n = g.B * g.H * g.slices * g.nseg;
+    const size_t bytes = LinShape<T, KD, CT>::bytes(OUT);
+    const hipError_t e = hipFuncSetAttribute((const void *)linattn_kernel<T, KD, CT, OUT>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)bytes);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((linattn_kernel<T, KD, CT, OUT>), dim3(n, jobs), dim3(kLinThreads), bytes,
+                       st, g);
+    return hipGetLastError();
+}
+
+template <typename T, bool OUT>
+static hipError_t pick_walk(const LinArgs &g, int jobs, int rows, bool wide, hipStream_t st)
+{
+    if (rows <= 32 && !wide) return launch_walk<T, 32, 1, OUT>(g, jobs, st);
+    if (rows <= 64)
+        return wide ? launch_walk<T, 64, 2, OUT>(g, jobs, st) : launch_walk<T, 64, 1, OUT>(g, jobs, st);
+    if (rows <= 128)
+        return wide ? launch_walk<T, 128, 2, OUT>(g, jobs, st)
+                    : launch_walk<T, 128, 1, OUT>(g, jobs, st);
+    return wide ? launch_walk<T, 256, 2, OUT>(g, jobs, st) : launch_walk<T, 256, 1, OUT>(g, jobs, st);
+}
+
+struct LinPlan {
+    int rows, slices, nseg, seg;
+    bool wide;
+    size_t off_seg[2], off_dk, off_dv, bytes;
+};
+
+// How the sequence is cut: as many segments as bring two workgroups to each of 256 CUs, of 512
+// tokens at least (a segment's state is written, joined and read again: as many bytes as 190 of
+// its tokens with heads of 128).
+static LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                        bool bwd)
+{
+    LinPlan p{};
+    const int64_t most = dk > dv ? dk : dv, cols = bwd ? most : dv;
+    p.rows = (int)(bwd ? most : dk);
+    p.wide = cols > 64;
+    p.slices = (int)(p.wide ? (cols + 127) / 128 : 1);
+    const int64_t groups = B * H * p.slices * (bwd ? 3 : 1);
+    int64_t n = groups > 0 ? (512 + groups - 1) / groups : 1;
+    const int64_t longest = (L + 511) / 512;
+    n = n < longest ? n : longest;
+    n = n < 1 ? 1 : n;
+    int64_t seg = ((L + n - 1) / n + 63) / 64 * 64;
+    if (seg < 64) seg = 64;
+    p.seg = (int)(seg < ((int64_t)1 << 30) ? seg : (int64_t)1 << 30);
+    p.nseg = (int)((L + p.seg - 1) / p.seg);
+    if (p.nseg < 1) p.nseg = 1;
+    size_t at = 0;
+    if (p.nseg > 1)
+        for (int i = 0; i < (bwd ? 2 : 1); ++i) {
+            p.off_seg[i] = at;
+            at = align256(at + (size_t)(B * H * p.nseg) * (size_t)(dk * dv) * 4);
+        }
+    if (bwd && H > Hk) {
+        p.off_dk = at;
+        at = align256(at + (size_t)(B * L * H) * (size_t)dk * 4);
+        p.off_dv = at;
+        at = align256(at + (size_t)(B * L * H) * (size_t)dv * 4);
+    }
+    p.bytes = at;
+    return p;
+}
+
+static naju_status_t check_lin(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
+                               int32_t io, float scale)
+{
+    if (B < 0 || L < 0 || H < 0 || Hk < 0 || dk < 0 || dv < 0)
+        return fail(NAJU_EINVAL, "negative size (batch=%lld seqlen=%lld heads=%lld kv_heads=%lld "
+                                 "d_key=%lld d_value=%lld)",
+                    (long long)B, (long long)L, (long long)H, (long long)Hk, (long long)dk,
+                    (long long)dv);
+    if (io != NAJU_F32 && io != NAJU_BF16)
+        return fail(NAJU_EINVAL, "io dtype %d is neither NAJU_F32 nor NAJU_BF16", (int)io);
+    if (H > 0 && (Hk == 0 || H % Hk != 0))
+        return fail(NAJU_EINVAL, "heads %lld is no multiple of kv_heads %lld", (long long)H,
+                    (long long)Hk);
+    if (H > 0 && (dk < 8 || dv < 8 || dk % 8 || dv % 8 || dk > kLinMost || dv > kLinMost))
+        return fail(NAJU_EUNSUPPORTED, "d_key %lld and d_value %lld must be multiples of 8 up to %d",
+                    (long long)dk, (long long)dv, kLinMost);
+    if (B > (1 << 20) || H > 65535 || B * H > (1 << 20) || L > ((int64_t)1 << 30))
+        return fail(NAJU_EINVAL, "batch * heads (2^20 max), heads (65535 max) or seqlen (2^30 max) "
+                                 "too large");
+    if (!(scale >= -1e30f && scale <= 1e30f)) return fail(NAJU_EINVAL, "scale must be finite");
+    return NAJU_OK;
+}
+
+static naju_status_t check_ld(int64_t ld, int64_t least, size_t e, const char *name)
+{
+    if (ld < least || ld > ((int64_t)1 << 32) || ld * (int64_t)e % 16 != 0)
+        return fail(NAJU_EINVAL, "token stride of %s (%lld) must be at least %lld elements and a "
+                                 "multiple of 16 bytes",
+                    name, (long long)ld, (long long)least);
+    return NAJU_OK;
+}
+
+template <bool OUT>
+static hipError_t walk(const LinArgs &g, int jobs, const LinPlan &p, int32_t io, hipStream_t st)
+{
+    return io == NAJU_F32 ? pick_walk<float, OUT>(g, jobs, p.rows, p.wide, st)
+                          : pick_walk<bf16, OUT>(g, jobs, p.rows, p.wide, st);
+}
+
+// the entering states of all segments, for the first `jobs` of g's walks
+static hipError_t enter_segments(LinArgs g, int jobs, const LinPlan &p, char *ws, int n, int32_t io,
+                                 hipStream_t st)
+{
+    LinJoin j{};
+    for (int i = 0; i < jobs; ++i) {
+        LinJob &J = g.job[i];
+        j.seg[i] = (float *)(ws + p.off_seg[i]);
+        j.enter[i] = J.enter;
+        j.enter_r[i] = J.enter_r;
+        j.enter_c[i] = J.enter_c;
+        j.cols[i] = J.D2;
+        J.enter = nullptr;
+        J.leave = j.seg[i];
+        J.leave_bh = (int64_t)p.nseg * n;
+        J.leave_seg = n;
+        J.leave_r = J.D2;
+        J.leave_c = 1;
+    }
+    const hipError_t e = walk<false>(g, jobs, p, io, st);
+    if (e != hipSuccess) return e;
+    // (a launch holds whole batch rows, so that heads and lengths keep their places)
+    const int rows = 65535 / g.H * g.H;
+    for (int at = 0; at < g.B * g.H; at += rows) {
+        const int now = g.B * g.H - at < rows ? g.B * g.H - at : rows;
+        LinJoin part = j;
+        for (int i = 0; i < jobs; ++i) {
+            part.seg[i] += (int64_t)at * p.nseg * n;
+            if (part.enter[i] != nullptr) part.enter[i] += (int64_t)at * n;
+        }
+        hipLaunchKernelGGL(linattn_join_kernel, dim3((n + 255) / 256, now, jobs), dim3(256), 0, st,
+                           part, g.log_decay, g.lengths != nullptr ? g.lengths + at / g.H : nullptr,
+                           g.H, n, p.nseg, p.seg, g.L);
+        const hipError_t f = hipGetLastError();
+        if (f != hipSuccess) return f;
+    }
+    return hipSuccess;
+}
+
+}  // namespace naju
+
+using namespace naju;
+
+extern "C" {
+
+size_t naju_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
+                                        int64_t kv_heads, int64_t d_key, int64_t d_value)
+{
+    if (check_lin(batch, seqlen, heads, kv_heads, d_key, d_value, NAJU_F32, 1.f) != NAJU_OK)
+        return 0;
+    return lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, false).bytes;
+}
+
+naju_status_t naju_linattn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads,
+                               int64_t d_key, int64_t d_value, int32_t io, const void *q,
+                               int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                               const float *log_decay, const float *state, const int32_t *lengths,
+                               float scale, void *o, float *state_out, void *ws, size_t ws_bytes,
+                               void *stream)
+{
+    NAJU_TRY(check_lin(batch, seqlen, heads, kv_heads, d_key, d_value, io, scale));
+    if (batch == 0 || heads == 0) return NAJU_OK;
+    const size_t e = io == NAJU_F32 ? 4 : 2;
+    if (seqlen > 0) {
+        NAJU_TRY(check_ld(ldq, heads * d_key, e, "q"));
+        NAJU_TRY(check_ld(ldk, kv_heads * d_key, e, "k"));
+        NAJU_TRY(check_ld(ldv, kv_heads * d_value, e, "v"));
+        NAJU_TRY(need(q, "q", 16));
+        NAJU_TRY(need(k, "k", 16));
+        NAJU_TRY(need(v, "v", 16));
+        NAJU_TRY(need(o, "o", 16));
+    }
+    NAJU_TRY(need(log_decay, "log_decay", 4));
+    NAJU_TRY(opt(state, "state", 4));
+    NAJU_TRY(opt(state_out, "state_out", 4));
+    NAJU_TRY(opt(lengths, "lengths", 4));
+    const LinPlan p = lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, false);
+    if (p.bytes > 0) NAJU_TRY(need_ws(ws, ws_bytes, p.bytes));
+    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 23))
+        return fail(NAJU_EINVAL, "batch * heads too large for this sequence length");
+    const int n = (int)(d_key * d_value);
+    LinArgs g{};
+    g.log_decay = log_decay;
+    g.lengths = lengths;
+    g.B = (int)batch;
+    g.H = (int)heads;
+    g.L = seqlen;
+    g.slices = p.slices;
+    g.nseg = p.nseg;
+    g.seg = p.seg;
+    LinJob &J = g.job[0];
+    J.q = q;
+    J.k = k;
+    J.v = v;
+    J.o = o;
+    J.ldq = ldq;
+    J.ldk = ldk;
+    J.ldv = ldv;
+    J.ldo = heads * d_value;
+    J.enter = state;
+    J.enter_bh = n;
+    J.enter_r = (int)d_value;
+    J.enter_c = 1;
+    J.leave = state_out;
+    J.leave_bh = n;
+    J.leave_r = (int)d_value;
+    J.leave_c = 1;
+    J.D1 = (int)d_key;
+    J.D2 = (int)d_value;
+    J.gq = 1;
+    J.gk = J.gv = (int)(heads / kv_heads);
+    J.s_row = J.s_pair = scale;
+    J.s_tok = 1.f;
+    J.late = 1;
+    hipStream_t st = (hipStream_t)stream;
+    if (p.nseg > 1) {
+        NAJU_TRY(hip_status(enter_segments(g, 1, p, (char *)ws, n, io, st),
+                            "linear attention segments launch"));
+        J.enter = (const float *)((char *)ws + p.off_seg[0]);
+        J.enter_bh = (int64_t)p.nseg * n;
+        J.enter_seg = n;
+    }
+    return hip_status(walk<true>(g, 1, p, io, st), "linear attention launch");
+}
+
+size_t naju_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
+                                        int64_t kv_heads, int64_t d_key, int64_t d_value)
+{
+    if (check_lin(batch, seqlen, heads, kv_heads, d_key, d_value, NAJU_F32, 1.f) != NAJU_OK)
+        return 0;
+    return lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, true).bytes;
+}
+
+naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int64_t kv_heads,
+                               int64_t d_key, int64_t d_value, int32_t io, const void *q,
+                               int64_t ldq, const void *k, int64_t ldk, const void *v, int64_t ldv,
+                               const float *log_decay, const float *state, const int32_t *lengths,
+                               float scale, const void *dout, const float *dstate_out, void *dq,
+                               void *dk, void *dv, float *dstate, void *ws, size_t ws_bytes,
+                               void *stream)
+{
+    NAJU_TRY(check_lin(batch, seqlen, heads, kv_heads, d_key, d_value, io, scale));
+    if (batch == 0 || heads == 0) return NAJU_OK;
+    const size_t e = io == NAJU_F32 ? 4 : 2;
+    if (seqlen > 0) {
+        NAJU_TRY(check_ld(ldq, heads * d_key, e, "q"));
+        NAJU_TRY(check_ld(ldk, kv_heads * d_key, e, "k"));
+        NAJU_TRY(check_ld(ldv, kv_heads * d_value, e, "v"));
+        NAJU_TRY(need(q, "q", 16));
+        NAJU_TRY(need(k, "k", 16));
+        NAJU_TRY(need(v, "v", 16));
+        NAJU_TRY(need(dout, "dout", 16));
+        NAJU_TRY(need(dq, "dq", 16));
+        NAJU_TRY(need(dk, "dk", 16));
+        NAJU_TRY(need(dv, "dv", 16));
+    }
+    NAJU_TRY(need(log_decay, "log_decay", 4));
+    NAJU_TRY(opt(state, "state", 4));
+    NAJU_TRY(opt(dstate_out, "dstate_out", 4));
+    NAJU_TRY(opt(dstate, "dstate", 4));
+    NAJU_TRY(opt(lengths, "lengths", 4));
+    const LinPlan p = lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, true);
+    if (p.bytes > 0) NAJU_TRY(need_ws(ws, ws_bytes, p.bytes));
+    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 23))
+        return fail(NAJU_EINVAL, "batch * heads too large for this sequence length");
+    const int n = (int)(d_key * d_value), group = (int)(heads / kv_heads);
+    char *base = (char *)ws;
+    LinArgs g{};
+    g.log_decay = log_decay;
+    g.lengths = lengths;
+    g.B = (int)batch;
+    g.H = (int)heads;
+    g.L = seqlen;
+    g.slices = p.slices;
+    g.nseg = p.nseg;
+    g.seg = p.seg;
+    const int64_t ldg = heads * d_value;
+    // dq: the forward's state transposed, from dout, v and k
+    LinJob &A = g.job[0];
+    A.q = dout;
+    A.ldq = ldg;
+    A.gq = 1;
+    A.k = v;
+    A.ldk = ldv;
+    A.v = k;
+    A.ldv = ldk;
+    A.gk = A.gv = group;
+    A.o = dq;
+    A.ldo = heads * d_key;
+    A.D1 = (int)d_value;
+    A.D2 = (int)d_key;
+    A.enter = state;
+    A.enter_bh = n;
+    A.enter_r = 1;
+    A.enter_c = (int)d_value;
+    A.s_row = A.s_pair = scale;
+    A.s_tok = 1.f;
+    A.late = 1;
+    // dv, and the state's gradient: back in time from k, q and dout
+    LinJob &V = g.job[1];
+    V.q = k;
+    V.ldq = ldk;
+    V.gq = group;
+    V.k = q;
+    V.ldk = ldq;
+    V.v = dout;
+    V.ldv = ldg;
+    V.gk = V.gv = 1;
+    V.o = group > 1 ? (void *)(base + p.off_dv) : dv;
+    V.out_f32 = group > 1;
+    V.ldo = heads * d_value;
+    V.D1 = (int)d_key;
+    V.D2 = (int)d_value;
+    V.enter = dstate_out;
+    V.enter_bh = n;
+    V.enter_r = (int)d_value;
+    V.enter_c = 1;
+    V.leave = dstate;
+    V.leave_bh = n;
+    V.leave_r = (int)d_value;
+    V.leave_c = 1;
+    V.s_row = 1.f;
+    V.s_pair = V.s_tok = scale;
+    V.late = 0;
+    V.back = 1;
+    hipStream_t st = (hipStream_t)stream;
+    if (p.nseg > 1) {
+        NAJU_TRY(hip_status(enter_segments(g, 2, p, base, n, io, st),
+                            "linear attention segments launch"));
+        A.enter = (const float *)(base + p.off_seg[0]);
+        A.enter_r = (int)d_key;
+        A.enter_c = 1;
+        V.enter = (const float *)(base + p.off_seg[1]);
+        A.enter_bh = V.enter_bh = (int64_t)p.nseg * n;
+        A.enter_seg = V.enter_seg = n;
+    }
+    // dk: the same state as dv's, transposed, from v, dout and q
+    LinJob &K = g.job[2];
+    K = V;
+    K.q = v;
+    K.ldq = ldv;
+    K.k = dout;
+    K.ldk = ldg;
+    K.v = q;
+    K.ldv = ldq;
+    K.o = group > 1 ? (void *)(base + p.off_dk) : dk;
+    K.ldo = heads * d_key;
+    K.D1 = (int)d_value;
+    K.D2 = (int)d_key;
+    K.enter_r = 1;
+    K.enter_c = (int)d_value;
+    K.leave = nullptr;
+    NAJU_TRY(hip_status(walk<true>(g, 3, p, io, st), "linear attention gradient launch"));
+    if (group == 1 || seqlen == 0) return NAJU_OK;
+    for (int i = 0; i < 2; ++i) {
+        const int64_t D = i ? d_value : d_key, total = batch * seqlen * kv_heads * D;
+        const float *x = (const float *)(base + (i ? p.off_dv : p.off_dk));
+        void *out = i ? dv : dk;
+        const int64_t most = (int64_t)1 << 32;  // elements of a launch, a multiple of every D's row
+        for (int64_t at = 0; at < total;) {
+            const int64_t step = most / D * D, now = total - at < step ? total - at : step;
+            const dim3 grid((unsigned)((now + 1023) / 1024));
+            if (io == NAJU_F32)
+                hipLaunchKernelGGL(linattn_group_kernel<float>, grid, dim3(256), 0, st,
+                                   x + at * group, (float *)out + at, now, group, (int)D);
+            else
+                hipLaunchKernelGGL(linattn_group_kernel<bf16>, grid, dim3(256), 0, st,
+                                   x + at * group, (bf16 *)out + at, now, group, (int)D);
+            NAJU_TRY(hip_status(hipGetLastError(), "linear attention head sums launch"));
+            at += now;
+        }
+    }
+    return NAJU_OK;
+}
+
+naju_status_t naju_linattn_step(int64_t batch, int64_t heads, int64_t kv_heads, int64_t d_key,
+                                int64_t d_value, int32_t io, const void *q, const void *k,
+                                const void *v, const float *log_decay, const float *state,
+                                float scale, void *o, float *state_out, void *stream)
+{
+    NAJU_TRY(check_lin(batch, 1, heads, kv_heads, d_key, d_value, io, scale));
+    if (batch == 0 || heads == 0) return NAJU_OK;
+    const size_t e = io == NAJU_F32 ? 4 : 2;
+    NAJU_TRY(need(q, "q", e));
+    NAJU_TRY(need(k, "k", e));
+    NAJU_TRY(need(v, "v", e));
+    NAJU_TRY(need(o, "o", e));
+    NAJU_TRY(need(log_decay, "log_decay", 4));
+    NAJU_TRY(need(state, "state", 16));
+    NAJU_TRY(need(state_out, "state_out", 16));
+    const int64_t per = 65535 / heads;  // batch rows of a launch
+    const int group = (int)(heads / kv_heads);
+    for (int64_t b = 0; b < batch; b += per) {
+        const int64_t now = batch - b < per ? batch - b : per;
+        const dim3 grid((unsigned)((d_value + 31) / 32), (unsigned)(now * heads));
+        const int64_t s = b * heads * d_key * d_value;
+        const int64_t bq = b * heads * d_key, bo = b * heads * d_value;
+        const int64_t bk = b * kv_heads * d_key, bv = b * kv_heads * d_value;
+        if (io == NAJU_F32)
+            hipLaunchKernelGGL(linattn_step_kernel<float>, grid, dim3(256), 0, (hipStream_t)stream,
+                               (int)heads, group, (int)d_key, (int)d_value, (const float *)q + bq,
+                               (const float *)k + bk, (const float *)v + bv, log_decay, scale,
+                               state + s, state_out + s, (float *)o + bo);
+        else
+            hipLaunchKernelGGL(linattn_step_kernel<bf16>, grid, dim3(256), 0, (hipStream_t)stream,
+                               (int)heads, group, (int)d_key, (int)d_value, (const bf16 *)q + bq,
+                               (const bf16 *)k + bk, (const bf16 *)v + bv, log_decay, scale,
+                               state + s, state_out + s, (bf16 *)o + bo);
+        NAJU_TRY(hip_status(hipGetLastError(), "linear attention step launch"));
+    }
+    return NAJU_OK;
+}
+
+}  // extern "C"

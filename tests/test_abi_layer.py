@@ -158,3 +158,114 @@ def test_adamw_definition():
     vals = layer.e4m3_values()
     t = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
     assert np.array_equal(vals, t) and vals[-1] == 448
+
+
+def lin_args(B=2, L=100, H=4, Hk=2, dk=64, dv=32, io=nb.BF16, q=FAKE, ldq=256, k=FAKE, ldk=128,
+             v=FAKE, ldv=64, a=FAKE, state=None, lengths=None, scale=0.125):
+    return (B, L, H, Hk, dk, dv, io, q, ldq, k, ldk, v, ldv, a, state, lengths, scale)
+
+
+def test_linattn_refusals(lib):
+    def fwd(o=FAKE, so=FAKE, ws=FAKE, wsb=1 << 40, **kw):
+        return lib.naju_linattn_fwd(*lin_args(**kw), o, so, ws, wsb, None)
+
+    def bwd(do=FAKE, ds=None, dq=FAKE, dk_=FAKE, dv_=FAKE, dst=FAKE, ws=FAKE, wsb=1 << 40, **kw):
+        return lib.naju_linattn_bwd(*lin_args(**kw), do, ds, dq, dk_, dv_, dst, ws, wsb, None)
+    for call in (fwd, bwd):
+        expect(call(B=-1), nb.EINVAL, "negative size")
+        expect(call(L=-1), nb.EINVAL, "negative size")
+        expect(call(io=2), nb.EINVAL, "io dtype")
+        expect(call(Hk=3), nb.EINVAL, "no multiple")
+        expect(call(Hk=0), nb.EINVAL, "no multiple")
+        for d in (0, 4, 20, 264):
+            expect(call(dk=d), nb.EUNSUPPORTED, "multiples of 8")
+            expect(call(dv=d), nb.EUNSUPPORTED, "multiples of 8")
+        expect(call(L=2 ** 31), nb.EINVAL, "too large")
+        expect(call(B=2 ** 21), nb.EINVAL, "too large")
+        expect(call(scale=float("nan")), nb.EINVAL, "scale")
+        expect(call(ldq=248), nb.EINVAL, "token stride of q")
+        expect(call(ldk=132), nb.EINVAL, "token stride of k")
+        expect(call(ldv=56), nb.EINVAL, "token stride of v")
+        for name in ("q", "k", "v"):
+            expect(call(**{name: None}), nb.EINVAL, name + " is NULL")
+            expect(call(**{name: FAKE + 8}), nb.EINVAL, "aligned")
+        expect(call(a=None), nb.EINVAL, "log_decay is NULL")
+        expect(call(lengths=FAKE + 2), nb.EINVAL, "aligned")
+        expect(call(state=FAKE + 2), nb.EINVAL, "aligned")
+        assert call(B=0, q=None) == nb.OK
+        assert call(H=0, Hk=0, q=None) == nb.OK
+        # a long sequence of few heads is cut, and needs the workspace
+        expect(call(L=65536, ws=None), nb.EWORKSPACE, "workspace is NULL")
+        expect(call(L=65536, wsb=256), nb.EWORKSPACE, "needs")
+    expect(fwd(o=None), nb.EINVAL, "o is NULL")
+    expect(bwd(dq=None), nb.EINVAL, "dq is NULL")
+    expect(bwd(dv_=FAKE + 4), nb.EINVAL, "aligned")
+    expect(bwd(do=None), nb.EINVAL, "dout is NULL")
+    expect(bwd(wsb=64), nb.EWORKSPACE, "needs")  # (shared heads)
+    f, g = lib.naju_linattn_fwd_workspace_bytes, lib.naju_linattn_bwd_workspace_bytes
+    assert f(8, 64, 96, 96, 128, 128) == 0 and f(1, 65536, 16, 16, 128, 128) >= 16 * 65536
+    assert g(2, 100, 4, 2, 64, 32) >= 2 * 100 * 4 * (64 + 32) * 4
+    assert f(-1, 1, 1, 1, 8, 8) == 0 and g(1, 1, 1, 1, 9, 8) == 0
+
+
+def test_linattn_step_refusals(lib):
+    def call(B=2, H=4, Hk=2, dk=64, dv=32, io=nb.BF16, q=FAKE, k=FAKE, v=FAKE, a=FAKE, s=FAKE,
+             scale=1.0, o=FAKE, so=FAKE):
+        return lib.naju_linattn_step(B, H, Hk, dk, dv, io, q, k, v, a, s, scale, o, so, None)
+    expect(call(B=-1), nb.EINVAL, "negative size")
+    expect(call(dk=12), nb.EUNSUPPORTED, "multiples of 8")
+    expect(call(Hk=3), nb.EINVAL, "no multiple")
+    expect(call(s=None), nb.EINVAL, "state is NULL")
+    expect(call(s=FAKE + 8), nb.EINVAL, "aligned")
+    expect(call(so=None), nb.EINVAL, "state_out is NULL")
+    expect(call(o=FAKE + 1), nb.EINVAL, "aligned")
+    assert call(B=0, q=None, s=None) == nb.OK
+
+
+def test_linattn_binding_refusals(lib):
+    q, a = torch.zeros(2, 5, 4, 16), torch.zeros(4)
+    with pytest.raises(ValueError, match="GPU"):
+        nb.linattn_fwd(q, q, q, a)
+    with pytest.raises(ValueError, match="GPU"):
+        nb.linattn_bwd(q, q, q, a, q)
+    with pytest.raises(ValueError, match="GPU"):
+        nb.linattn_step(q[0], q[0], q[0], a, torch.zeros(5, 4, 16, 16))
+    # strides: parts of a joint projection pass, other orders do not
+    joint = torch.zeros(2, 5, 3, 4, 16)
+    assert nb._req_tokens(joint[:, :, 1], "q", (2, 5, 4, 16), q.dtype, q.device) == 192
+    assert nb._req_tokens(joint[:, :1, 1], "q", (2, 1, 4, 16), q.dtype, q.device) == 960
+    for bad in (q.transpose(1, 2).contiguous().transpose(1, 2), joint[:, ::2, 0],
+                joint[:, :, 0, :, ::2], q.expand(2, 5, 4, 16)[:, :, :1].expand(2, 5, 4, 16)):
+        with pytest.raises(ValueError):
+            nb._req_tokens(bad, "q", tuple(bad.shape), q.dtype, q.device)
+
+
+def test_linattn_definition():
+    """Without decay it is causal attention without softmax; with decay 0 only the token itself
+    counts; two halves with the state carried are the whole; gradients are differences."""
+    rng = np.random.default_rng(2)
+    q, k = rng.standard_normal((2, 2, 7, 2, 3))
+    v, do = rng.standard_normal((2, 2, 7, 2, 4))
+    o, s = layer.linattn_fwd(q, k, v, np.zeros(2), scale=0.5)
+    scores = np.einsum("bihd,bjhd->bhij", q, k) * np.tril(np.ones((7, 7)))
+    assert np.allclose(o, 0.5 * np.einsum("bhij,bjhe->bihe", scores, v))
+    assert np.allclose(s, np.einsum("bjhd,bjhe->bhde", k, v))
+    o, _ = layer.linattn_fwd(q, k, v, np.full(2, -np.inf))
+    assert np.allclose(o, (q * k).sum(-1, keepdims=True) * v)
+    a = np.array([-0.1, -1.0])
+    whole, end = layer.linattn_fwd(q, k, v, a)
+    o1, s1 = layer.linattn_fwd(q[:, :3], k[:, :3], v[:, :3], a)
+    o2, s2 = layer.linattn_fwd(q[:, 3:], k[:, 3:], v[:, 3:], a, state=s1)
+    assert np.allclose(np.concatenate([o1, o2], 1), whole) and np.allclose(s2, end)
+    s0, ds = rng.standard_normal((2, 2, 2, 3, 4))
+    n = np.array([7, 4])
+
+    def loss(q, k, v, s0):
+        o, s = layer.linattn_fwd(q, k, v, a, s0, n, 0.7)
+        return (o * do).sum() + (s * ds).sum()
+    g = layer.linattn_bwd(q, k, v, a, do, s0, ds, n, 0.7)
+    base = dict(q=q, k=k, v=v, s0=s0)
+    for name, key in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("s0", "dstate")):
+        way = rng.standard_normal(base[name].shape)
+        up, down = (loss(**{**base, name: base[name] + h * way}) for h in (1e-5, -1e-5))
+        assert abs((g[key] * way).sum() - (up - down) / 2e-5) < 1e-6
