@@ -43,9 +43,12 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kLinMost = 256;      // elements of a head's keys or values
 constexpr int kLinThreads = 256;
+constexpr int64_t kLinStride = (int64_t)1 << 20;  // elements from token to token: a chunk's tokens
+                                                  // span 2^28 bytes at most
 
 // One walk.  The names are the forward's: q reads, k and v are summed into the state.
 struct LinJob {
@@ -61,7 +64,6 @@ struct LinJob {
     float s_row, s_pair, s_tok;         // scales of S^T q, of the scores, of k v^T
     int late;
     int back;                // 1: from each row's last token to its first
-    int out_f32;             // o is fp32 whatever the io type
 };
 
 struct LinArgs {
@@ -69,19 +71,38 @@ struct LinArgs {
     const float *log_decay;
     const int32_t *lengths;
     int B, H, slices, nseg, seg;        // seg: tokens of a segment
+    int jobs, items;                    // walks, and workgroups of each
     int64_t L;
 };
 
 // ------------------------------------------------------- operands of the products
-// 8 elements of a row (or column) of an operand in a lane: the lane's row is l % 16, its slots
-// 8 (l / 16) .. + 7 of 32.  Both operands of a product take the same elements in the same slots.
+// An operand in a lane: row l % 16 of 16, and 8 of 32 elements, those in the slots 8 h .. 8 h + 7 of
+// its quarter h = l / 16.  Both operands of a product put the same elements into the same slots,
+// in any order: where elements are tokens, and in products with the state, slot 8 h + j holds
+// element slot_step(j) + 4 h, the order in which the matrix instruction leaves two tiles of 16
+// rows in a lane's registers.
+//
+// Rows of LDS tiles lie 32 bytes further in the 64 banks than the one before.  Measured with the
+// bank-conflict counter (cycles of an access of the wave, the least in brackets): 16-byte reads of
+// 16 rows 4 (4), and 8 with rows 16 bytes further; transposing reads of 16 neighbouring columns
+// 2 (2), of columns 16 bytes apart 4.
+__device__ __forceinline__ constexpr int slot_step(int j) { return 16 * (j >> 2) + (j & 3); }
+
 template <typename T> struct Frag;
 
 template <> struct Frag<bf16> {
     bf16x8 f;
-    __device__ __forceinline__ void row(const bf16 *p) { f = *(const bf16x8 *)p; }
-    // Transposed: element j of the lane is column `col` of the lane of row 4 (j % 4) + 16 (j / 4)
-    // behind its first.  ds_read_tr16_b64: lane i of 16 hands in row i / 4 (of four) and columns
+    // 8 neighbouring elements of the 32 from p on
+    __device__ __forceinline__ void row(const bf16 *p, int h) { f = *(const bf16x8 *)(p + 8 * h); }
+    __device__ __forceinline__ void scores(const bf16 *p, int h) { row(p, h); }
+    // those of slot_step
+    __device__ __forceinline__ void split_row(const bf16 *p, int h)
+    {
+        const bf16x4 a = *(const bf16x4 *)(p + 4 * h), b = *(const bf16x4 *)(p + 4 * h + 16);
+        f = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    // Transposed: element j of the lane is its column of row slot_step(j) behind the first.
+    // ds_read_tr16_b64: lane i of 16 hands in row i / 4 (of four) and columns
     // 4 (i % 4) .. + 3 of its choice, and receives column i of all four rows.
     __device__ __forceinline__ void cols(const bf16 *p, int stride)
     {
@@ -101,20 +122,22 @@ template <> struct Frag<bf16> {
 };
 template <> struct Frag<float> {
     float f[8];
-    __device__ __forceinline__ void row(const float *p)
+    __device__ __forceinline__ void split_row(const float *p, int h)
     {
-        const f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
+        const f32x4 a = *(const f32x4 *)(p + 4 * h), b = *(const f32x4 *)(p + 4 * h + 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             f[i] = a[i];
             f[4 + i] = b[i];
         }
     }
+    __device__ __forceinline__ void row(const float *p, int h) { split_row(p, h); }
+    __device__ __forceinline__ void scores(const float *p, int h) { split_row(p, h); }
     // (no transposing read for 32-bit elements: the lane reads its own column)
     __device__ __forceinline__ void cols(const float *p, int stride)
     {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = p[4 * j * stride];
+        for (int j = 0; j < 8; ++j) f[j] = p[slot_step(j) * stride];
     }
     __device__ __forceinline__ float get(int i) const { return f[i]; }
 };
@@ -186,39 +209,56 @@ __device__ __forceinline__ f32x4 mma(const Frag<T> &a, const Parts<T, P> &b, f32
     return c;
 }
 
-// A tile of rows on its way from HBM to LDS: 16 bytes at a time, zeros behind the sequence's
-// and the head's ends.
+// A raw buffer over [p, p + bytes): loads past the end read 0, stores past the end are dropped (the
+// check covers every dword's whole offset).
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rsrc(const void *p, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes,
+                                             0x00020000);
+}
+// An offset past every buffer here, also with a chunk's length taken off or added
+// (a chunk's rows span less than 2^29 bytes).
+constexpr uint32_t kPast = 0x80000000u;
+
+// A tile of rows on its way from HBM to LDS, 16 bytes at a time.  Rows are a chunk's tokens in the
+// order of the walk; a buffer over the chunk's tokens that there are gives zeros for the others.
 template <typename T, int ROWS, int COLS> struct Stage {
     static constexpr int E = 16 / (int)sizeof(T);
     static constexpr int kPerRow = COLS / E;
     static constexpr int N = ROWS * kPerRow / kLinThreads;  // accesses of a thread
     static_assert(ROWS * kPerRow % kLinThreads == 0, "whole accesses");
-    static constexpr int kStride = COLS + E;  // (rows lie 16 bytes further in the banks)
+    static constexpr int kStride = COLS + 2 * E;  // (32 bytes further in the banks)
+    static constexpr int kRows = kLinThreads / kPerRow;     // rows from one access to the next
     u32x4 r[N];
+    uint32_t off;   // of the first access, in a chunk of ROWS tokens
+    uint32_t step;  // to the next (negative where the walk goes back)
 
-    // tokens n0 .. of a row with `len` of them; D: elements of a row from column c0 on
-    __device__ __forceinline__ void fetch(const T *p, int64_t ld, int64_t n0, int64_t len,
-                                          bool back, int D, int tid)
+    __device__ __forceinline__ void init(int64_t ld, bool back, int D, int tid)
     {
+        const uint32_t row_bytes = (uint32_t)ld * (uint32_t)sizeof(T);
+        const int row = tid / kPerRow, col = tid % kPerRow * E;
+        off = (uint32_t)(back ? ROWS - 1 - row : row) * row_bytes + col * (uint32_t)sizeof(T);
+        if (col >= D) off = kPast;
+        step = (uint32_t)(back ? -kRows : kRows) * row_bytes;
+    }
+    // lo: the chunk's lowest token; there: its tokens; moved: offsets' change in a short chunk
+    __device__ __forceinline__ void fetch(const T *lo, int64_t ld, int there, uint32_t moved, int tid)
+    {
+        const rsrc_t b = make_rsrc(lo, (uint32_t)there * (uint32_t)ld * (uint32_t)sizeof(T));
+        const int row = tid / kPerRow;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int at = tid + i * kLinThreads, row = at / kPerRow, col = at % kPerRow * E;
-            int64_t n = n0 + row;
-            n = n < len ? n : len - 1;
-            const int64_t t = back ? len - 1 - n : n;
-            const int c = col < D ? col : 0;
-            r[i] = *(const u32x4 *)(p + t * ld + c);
+            uint32_t at = off + moved + i * step;
+            if (row + i * kRows >= there) at = kPast;  // (walking back it is below the buffer)
+            r[i] = __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, 0);
         }
     }
-    __device__ __forceinline__ void put(T *lds, int64_t n0, int64_t len, int D, int tid) const
+    __device__ __forceinline__ void put(T *lds, int tid) const
     {
+        T *to = lds + tid / kPerRow * kStride + tid % kPerRow * E;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = tid + i * kLinThreads, row = at / kPerRow, col = at % kPerRow * E;
-            const bool in = n0 + row < len && col < D;
-            const u32x4 zero = {0u, 0u, 0u, 0u};
-            *(u32x4 *)(lds + row * kStride + col) = in ? r[i] : zero;
-        }
+        for (int i = 0; i < N; ++i) *(u32x4 *)(to + i * kRows * kStride) = r[i];
     }
 };
 
@@ -228,7 +268,7 @@ template <typename T, int KD, int CT> struct LinShape {
     using SK = Stage<T, TT, KD>;
     using SV = Stage<T, TT, VC>;
     static constexpr int E = 16 / (int)sizeof(T);
-    static constexpr int kScores = TT + E;               // stride of the scores
+    static constexpr int kScores = TT + 2 * E;           // stride of the scores
     static constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
     static constexpr size_t bytes(bool out)
     {
@@ -237,15 +277,12 @@ template <typename T, int KD, int CT> struct LinShape {
     }
 };
 
-// The token that stands in position m of 16 where an operand's slots are tokens: rows 4 apart are
-// read together by the transposing reads, which then meet no bank twice.
-__device__ __forceinline__ int token_of(int m) { return (m >> 2) + 4 * (m & 3); }
-
-// OUT: the walk, with outputs; else a segment's contribution to the state alone.
-template <typename T, int KD, int CT, bool OUT>
+// OT: the outputs' type; void: none, a segment's contribution to the state alone.
+template <typename T, int KD, int CT, typename OT>
 __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel(const LinArgs g)
 {
     using Sh = LinShape<T, KD, CT>;
+    constexpr bool OUT = !__is_same(OT, void), wide_out = __is_same(OT, float);
     constexpr int TT = Sh::TT, VC = Sh::VC, IT = TT / 16, KS = TT / 32, KB = KD / 32;
     constexpr int QS = Sh::SK::kStride, VS = Sh::SV::kStride, PS = Sh::kScores;
     extern __shared__ __attribute__((aligned(16))) char lds[];
@@ -254,8 +291,13 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
 
     const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, h4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const LinJob &J = g.job[blockIdx.y];
+    // jobs of the same segment run on the same XCD (workgroups go round robin over 8 of them)
     int id = blockIdx.x;
+    const int jobs = g.jobs;
+    const int job = id / 8 % jobs;
+    id = id / (8 * jobs) * 8 + id % 8;
+    if (id >= g.items) return;
+    const LinJob &J = g.job[job];
     const int slice = id % g.slices;
     id /= g.slices;
     const int seg = id % g.nseg;
@@ -265,22 +307,28 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
     if (c0 >= J.D2) return;
     const int D1 = J.D1, D2 = J.D2 - c0 < VC ? J.D2 - c0 : VC;  // of this workgroup
     const int64_t L = g.L;
-    int64_t len = g.lengths != nullptr ? g.lengths[b] : L;
-    len = len < 0 ? 0 : len < L ? len : L;
+    int len_i = g.lengths != nullptr ? g.lengths[b] : (int)L;
+    len_i = len_i < 0 ? 0 : len_i < (int)L ? len_i : (int)L;
+    const int64_t len = __builtin_amdgcn_readfirstlane(len_i);
     const bool back = J.back != 0;
     const int late = J.late;
+    const float s_pair = J.s_pair, s_tok = J.s_tok;
     // log2 of the decay; below -1e30 it is 0 after one step, and 0 * -1e30 stays 0
     float a2 = g.log_decay[hd];
     a2 = (a2 < -1e30f ? -1e30f : a2) * kLog2e;
 
-    const T *q = (const T *)J.q + (int64_t)b * L * J.ldq + (int64_t)(hd / J.gq) * D1;
-    const T *k = (const T *)J.k + (int64_t)b * L * J.ldk + (int64_t)(hd / J.gk) * D1;
-    const T *v = (const T *)J.v + (int64_t)b * L * J.ldv + (int64_t)(hd / J.gv) * J.D2 + c0;
+    const int64_t ldq = J.ldq, ldk = J.ldk, ldv = J.ldv;
+    const T *q = (const T *)J.q + (int64_t)b * L * ldq + (int64_t)(hd / J.gq) * D1;
+    const T *k = (const T *)J.k + (int64_t)b * L * ldk + (int64_t)(hd / J.gk) * D1;
+    const T *v = (const T *)J.v + (int64_t)b * L * ldv + (int64_t)(hd / J.gv) * J.D2 + c0;
+    const uint32_t out_row = (uint32_t)J.ldo * (wide_out ? 4u : 2u);  // bytes
+    char *out = (char *)J.o + (int64_t)b * L * out_row +
+                ((int64_t)hd * J.D2 + c0) * (wide_out ? 4 : 2);
 
     // this lane's columns of the state: 4 CT neighbouring lanes' tiles interleave, so that a
     // lane's outputs of one token are 4 CT consecutive elements
     auto column = [&](int ct) { return 16 * CT * w + 4 * CT * (m >> 2) + 4 * ct + (m & 3); };
-    // rows of the state: register r of tile 2 kb + a is row 32 kb + 8 h4 + 4 a + r
+    // rows of the state: register r of tile kt is row 16 kt + 4 h4 + r
     f32x4 S[CT][2 * KB];
     {
         const float *e = J.enter;
@@ -292,7 +340,7 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
             for (int kt = 0; kt < 2 * KB; ++kt)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * (kt & ~1) + 8 * h4 + 4 * (kt & 1) + r;
+                    const int row = 16 * kt + 4 * h4 + r;
                     const int col = column(ct);
                     float s = 0.f;
                     if (OUT && e != nullptr && row < D1 && col < D2)
@@ -300,8 +348,33 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
                     S[ct][kt][r] = s;
                 }
     }
-    float lead[IT];  // of S^T q, for this lane's token of each tile
+    // Powers of the decay that every whole chunk takes.
+    float lead[IT];     // of S^T q, for this lane's token of each tile
+    // scores come in tiles of 16 tokens i by 16 tokens j <= i, dealt out to the waves; then the
+    // tiles above the diagonal that a product of 32 tokens takes in, which are zeros
+    constexpr int kTiles = IT * (IT + 1) / 2, kAll = kTiles + IT / 2, kOwn = (kAll + 3) / 4;
+    float pair[kOwn][4];  // of the scores: scale and power, 0 above the diagonal
+    auto tile = [&](int n, int &it, int &jt) {
+        const int t = w + 4 * n;
+        it = t < kTiles ? (t >= 1) + (t >= 3) + (t >= 6) : 2 * (t - kTiles);
+        jt = t < kTiles ? t - it * (it + 1) / 2 : it + 1;
+    };
+    float tok[8], tok0[KS];  // of k v^T: a product of two, neither exponent negative
+#pragma unroll
+    for (int j = 0; j < 8; ++j) tok[j] = ex2(a2 * (float)(19 - slot_step(j)));
+#pragma unroll
+    for (int s = 0; s < KS; ++s) tok0[s] = s_tok * ex2(a2 * (float)(TT - late - 32 * s - 4 * h4 - 19));
     if constexpr (OUT) {
+#pragma unroll
+        for (int n = 0; n < kOwn; ++n) {
+            int it, jt;
+            tile(n, it, jt);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int gap = 16 * (it - jt) + m - (4 * h4 + r);
+                pair[n][r] = gap >= 0 ? s_pair * ex2(a2 * (float)gap) : 0.f;
+            }
+        }
 #pragma unroll
         for (int it = 0; it < IT; ++it) lead[it] = J.s_row * ex2(a2 * (float)(16 * it + m + late));
     }
@@ -311,46 +384,64 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
     const int64_t stop = end < len ? end : len;                     // those that there are
     typename Sh::SK rq, rk;
     typename Sh::SV rv;
+    if constexpr (OUT) rq.init(ldq, back, D1, tid);
+    rk.init(ldk, back, D1, tid);
+    rv.init(ldv, back, D2, tid);
     auto fetch = [&](int64_t n0) {
-        if constexpr (OUT) rq.fetch(q, J.ldq, n0, len, back, D1, tid);
-        rk.fetch(k, J.ldk, n0, len, back, D1, tid);
-        rv.fetch(v, J.ldv, n0, len, back, D2, tid);
+        const int there = stop - n0 < TT ? (int)(stop - n0) : TT;
+        const int64_t lo = back ? len - n0 - there : n0;
+        const uint32_t moved = back ? (uint32_t)(there - TT) : 0u;
+        if constexpr (OUT) rq.fetch(q + lo * ldq, ldq, there, moved * (uint32_t)ldq * sizeof(T), tid);
+        rk.fetch(k + lo * ldk, ldk, there, moved * (uint32_t)ldk * sizeof(T), tid);
+        rv.fetch(v + lo * ldv, ldv, there, moved * (uint32_t)ldv * sizeof(T), tid);
     };
+    // where this lane's outputs go, in a chunk of TT tokens: 4 CT elements of tokens m, m + 16, ..
+    const int ocol = 16 * CT * w + 4 * CT * h4;
+    uint32_t ooff = (uint32_t)(back ? TT - 1 - m : m) * out_row + ocol * (wide_out ? 4 : 2);
+    if (ocol >= D2) ooff = kPast;
+    const uint32_t ostep = (back ? -16u : 16u) * out_row;
+
     if (first < stop) fetch(first);
     for (int64_t n0 = first; n0 < stop; n0 += TT) {
         __syncthreads();  // (the chunk before has been read)
-        if constexpr (OUT) rq.put(qs, n0, len, D1, tid);
-        rk.put(ks, n0, len, D1, tid);
-        rv.put(vs, n0, len, D2, tid);
+        if constexpr (OUT) rq.put(qs, tid);
+        rk.put(ks, tid);
+        rv.put(vs, tid);
         if (n0 + TT < stop) fetch(n0 + TT);
         __syncthreads();
         const int there = stop - n0 < TT ? (int)(stop - n0) : TT;
 
         if constexpr (OUT) {
-            // scores of 16 tokens i, transposed: positions of tokens j in a lane's registers
-            if (w < IT) {
-                Frag<T> fq[KB];
+            // (transposed: positions of tokens j in a lane's registers)
+            f32x4 acc[kOwn];
 #pragma unroll
-                for (int kb = 0; kb < KB; ++kb) fq[kb].row(qs + (16 * w + m) * QS + 32 * kb + 8 * h4);
-                const int i = 16 * w + m;
-                for (int jt = 0; jt < 2 * (w / 2) + 2; ++jt) {
-                    float s[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (jt <= w) {
-                        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (int n = 0; n < kOwn; ++n) {
+                acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+                int it, jt;
+                tile(n, it, jt);
+                if (w + 4 * n < kTiles) {
 #pragma unroll
-                        for (int kb = 0; kb < KB; ++kb) {
-                            Frag<T> fk;
-                            fk.row(ks + (16 * jt + token_of(m)) * QS + 32 * kb + 8 * h4);
-                            acc = mma(fk, fq[kb], acc);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int gap = i - (16 * jt + h4 + 4 * r);
-                            const float p = acc[r] * (J.s_pair * ex2(a2 * (float)gap));
-                            s[r] = gap >= 0 ? p : 0.f;
-                        }
+                    for (int kb = 0; kb < KB; ++kb) {
+                        Frag<T> fq, fk;
+                        fq.row(qs + (16 * it + m) * QS + 32 * kb, h4);
+                        fk.row(ks + (16 * jt + m) * QS + 32 * kb, h4);
+                        acc[n] = mma(fk, fq, acc[n]);
                     }
-                    T *to = ps + i * PS + 32 * (jt / 2) + 8 * h4 + 4 * (jt & 1);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < kOwn; ++n) {
+                int it, jt;
+                tile(n, it, jt);
+                if (w + 4 * n < kAll) {
+                    float s[4];
+                    const int i = 16 * it + m;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        s[r] = pair[n][r] != 0.f ? acc[n][r] * pair[n][r] : 0.f;
+                    // (bf16: in the order of the slots, to be read as one run)
+                    T *to = ps + i * PS + (sizeof(T) == 2 ? 32 * (jt / 2) + 8 * h4 + 4 * (jt & 1)
+                                                          : 16 * jt + 4 * h4);
                     if constexpr (sizeof(T) == 2) {
                         float lo[4];
                         uint32_t hi[2];
@@ -369,7 +460,6 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
                     }
                 }
             }
-            __syncthreads();
         }
 
         // values: this wave's columns, slots = tokens
@@ -379,13 +469,16 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 if constexpr (sizeof(T) == 2)
-                    fv[ct][s].cols(vs + (32 * s + h4 + 4 * (m >> 2)) * VS + 16 * CT * w +
+                    fv[ct][s].cols(vs + (32 * s + 4 * h4 + (m >> 2)) * VS + 16 * CT * w +
                                        4 * CT * (m & 3) + 4 * ct, VS);
                 else
-                    fv[ct][s].cols(vs + (32 * s + h4) * VS + column(ct), VS);
+                    fv[ct][s].cols(vs + (32 * s + 4 * h4) * VS + column(ct), VS);
             }
 
         if constexpr (OUT) {
+            const int64_t lo = back ? len - n0 - there : n0;
+            const rsrc_t ob = make_rsrc(out + lo * out_row, (uint32_t)there * out_row);
+            const uint32_t omoved = back ? (uint32_t)(there - TT) * out_row : 0u;
             f32x4 o[IT][CT];
 #pragma unroll
             for (int it = 0; it < IT; ++it)
@@ -404,11 +497,13 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
 #pragma unroll
                 for (int it = 0; it < IT; ++it) {
                     Frag<T> fq;
-                    fq.row(qs + (16 * it + m) * QS + 32 * kb + 8 * h4);
+                    fq.split_row(qs + (16 * it + m) * QS + 32 * kb, h4);
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) o[it][ct] = mma(st[ct], fq, o[it][ct]);
                 }
             }
+            // (the scores of the other waves: waited for behind the products that do without them)
+            __syncthreads();
 #pragma unroll
             for (int it = 0; it < IT; ++it) {
 #pragma unroll
@@ -418,30 +513,28 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
                     Parts<T, 2> fp;
 #pragma unroll
                     for (int n = 0; n < Sh::kParts; ++n)
-                        fp.p[n].row(ps + n * TT * PS + (16 * it + m) * PS + 32 * s + 8 * h4);
+                        fp.p[n].scores(ps + n * TT * PS + (16 * it + m) * PS + 32 * s, h4);
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct) o[it][ct] = mma(fv[ct][s], fp, o[it][ct]);
                 }
-                const int64_t n = n0 + 16 * it + m;
-                if (n < stop) {
-                    const int64_t t = back ? len - 1 - n : n;
-                    const int col = 16 * CT * w + 4 * CT * h4;
+                // (tokens that there are none of lie past the buffer's end)
+                const uint32_t at = 16 * it + m < there ? ooff + it * ostep + omoved : kPast;
+                if constexpr (wide_out) {
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            __builtin_bit_cast(u32x4, o[it][ct]), ob, (int)(at + 16 * ct), 0, 0);
+                } else {
                     float x[4 * CT];
 #pragma unroll
                     for (int i = 0; i < 4 * CT; ++i) x[i] = o[it][i / 4][i % 4];
-                    const int64_t at = ((int64_t)b * L + t) * J.ldo + (int64_t)hd * J.D2 + c0 + col;
-                    if (col < D2) {  // (D2 is a multiple of 8, and so is what a lane stores)
-                        if (sizeof(T) == 4 || J.out_f32) {
-#pragma unroll
-                            for (int i = 0; i < CT; ++i)
-                                *(f32x4 *)((float *)J.o + at + 4 * i) =
-                                    f32x4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
-                        } else {
-                            const Run<bf16, 4 * CT> run = round_run<bf16, 4 * CT>(x);
-                            __builtin_memcpy(__builtin_assume_aligned((bf16 *)J.o + at, 8 * CT),
-                                             run.w, 8 * CT);
-                        }
-                    }
+                    const Run<bf16, 4 * CT> run = round_run<bf16, 4 * CT>(x);
+                    if constexpr (CT == 2)
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            u32x4{run.w[0], run.w[1], run.w[2], run.w[3]}, ob, (int)at, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b64(
+                            u32x2{run.w[0], run.w[1]}, ob, (int)at, 0, 0);
                 }
             }
         }
@@ -455,28 +548,30 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             Parts<T, 3> vd[CT];
-            float tok[8];
+            float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int left = there - late - (32 * s + h4 + 4 * j);
-                tok[j] = J.s_tok * ex2(a2 * (float)(left > 0 ? left : 0));
+            for (int j = 0; j < 8; ++j) f[j] = tok0[s] * tok[j];
+            if (there < TT) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int left = there - late - (32 * s + 4 * h4 + slot_step(j));
+                    f[j] = s_tok * ex2(a2 * (float)(left > 0 ? left : 0));
+                }
             }
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 float x[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] = fv[ct][s].get(j) * tok[j];
+                for (int j = 0; j < 8; ++j) x[j] = fv[ct][s].get(j) * f[j];
                 vd[ct].set(x);
             }
 #pragma unroll
             for (int kt = 0; kt < 2 * KB; ++kt) {
                 Frag<T> fk;
                 if constexpr (sizeof(T) == 2)
-                    fk.cols(ks + (32 * s + h4 + 4 * (m >> 2)) * QS + 16 * (kt & ~1) + 8 * (m & 3) +
-                                4 * (kt & 1), QS);
+                    fk.cols(ks + (32 * s + 4 * h4 + (m >> 2)) * QS + 16 * kt + 4 * (m & 3), QS);
                 else
-                    fk.cols(ks + (32 * s + h4) * QS + 16 * (kt & ~1) + 8 * (m >> 2) + 4 * (kt & 1) +
-                                (m & 3), QS);
+                    fk.cols(ks + (32 * s + 4 * h4) * QS + 16 * kt + m, QS);
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) S[ct][kt] = mma(fk, vd[ct], S[ct][kt]);
             }
@@ -490,15 +585,10 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
             const int per = D2 / 8;
             for (int64_t i = tid; i < (end - z0) * per; i += kLinThreads) {
                 const int64_t t = z0 + i / per;
-                const int64_t at = ((int64_t)b * L + t) * J.ldo + (int64_t)hd * J.D2 + c0 +
-                                   i % per * 8;
+                u32x4 *at = (u32x4 *)(out + t * out_row + i % per * (wide_out ? 32 : 16));
                 const u32x4 zero = {0u, 0u, 0u, 0u};
-                if (sizeof(T) == 4 || J.out_f32) {
-                    ((u32x4 *)((float *)J.o + at))[0] = zero;
-                    ((u32x4 *)((float *)J.o + at))[1] = zero;
-                } else {
-                    *(u32x4 *)((bf16 *)J.o + at) = zero;
-                }
+                at[0] = zero;
+                if (wide_out) at[1] = zero;
             }
         }
     }
@@ -510,7 +600,7 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
         for (int kt = 0; kt < 2 * KB; ++kt)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = 16 * (kt & ~1) + 8 * h4 + 4 * (kt & 1) + r, col = column(ct);
+                const int row = 16 * kt + 4 * h4 + r, col = column(ct);
                 if (row < D1 && col < D2)
                     e[(int64_t)row * J.leave_r + (int64_t)(c0 + col) * J.leave_c] = S[ct][kt][r];
             }
@@ -527,29 +617,34 @@ __global__ __launch_bounds__(256) void linattn_join_kernel(const LinJoin j, cons
                                                            const int32_t *lengths, int H, int n,
                                                            int nseg, int seg, int64_t L)
 {
-    const int i = blockIdx.x * 256 + threadIdx.x, bh = blockIdx.y, q = blockIdx.z;
+    const int i = (blockIdx.x * 256 + threadIdx.x) * 4, bh = blockIdx.y, q = blockIdx.z;
     if (i >= n) return;
     const int b = bh / H;
     int64_t len = lengths != nullptr ? lengths[b] : L;
     len = len < 0 ? 0 : len < L ? len : L;
     float a2 = log_decay[bh % H];
     a2 = (a2 < -1e30f ? -1e30f : a2) * kLog2e;
-    float x = 0.f;
-    if (j.enter[q] != nullptr)
-        x = j.enter[q][(int64_t)bh * n + (int64_t)(i / j.cols[q]) * j.enter_r[q] +
-                       (int64_t)(i % j.cols[q]) * j.enter_c[q]];
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    if (j.enter[q] != nullptr) {
+        const float *e = j.enter[q] + (int64_t)bh * n + (int64_t)(i / j.cols[q]) * j.enter_r[q] +
+                         (int64_t)(i % j.cols[q]) * j.enter_c[q];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = e[r * j.enter_c[q]];
+    }
     float *p = j.seg[q] + (int64_t)bh * nseg * n + i;
     for (int s0 = 0; s0 < nseg; s0 += 8) {  // (eight at a time: loads ahead of the stores)
-        float own[8];
+        f32x4 own[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            own[i] = s0 + i < nseg - 1 ? p[(int64_t)(s0 + i) * n] : 0.f;
+        for (int r = 0; r < 8; ++r) {
+            own[r] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (s0 + r < nseg - 1) own[r] = *(const f32x4 *)(p + (int64_t)(s0 + r) * n);
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int64_t left = len - (int64_t)(s0 + i) * seg;
+        for (int r = 0; r < 8; ++r) {
+            const int64_t left = len - (int64_t)(s0 + r) * seg;
             const int64_t there = left < 0 ? 0 : left < seg ? left : seg;
-            if (s0 + i < nseg) p[(int64_t)(s0 + i) * n] = x;
-            x = x * ex2(a2 * (float)there) + own[i];
+            if (s0 + r < nseg) *(f32x4 *)(p + (int64_t)(s0 + r) * n) = x;
+            x = x * ex2(a2 * (float)there) + own[r];
         }
     }
 }
@@ -629,30 +724,30 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(int H, int group, int
 }
 
 // ---------------------------------------------------------------------- host
-template <typename T, int KD, int CT, bool OUT>
-static hipError_t launch_walk(const LinArgs &g, int jobs, hipStream_t st)
+template <typename T, int KD, int CT, typename OT>
+static hipError_t launch_walk(LinArgs &g, hipStream_t st)
 {
-    const int n = g.B * g.H * g.slices * g.nseg;
-    const size_t bytes = LinShape<T, KD, CT>::bytes(OUT);
-    const hipError_t e = hipFuncSetAttribute((const void *)linattn_kernel<T, KD, CT, OUT>,
+    g.items = g.B * g.H * g.slices * g.nseg;
+    const int n = (g.items + 7) / 8 * 8 * g.jobs;
+    const size_t bytes = LinShape<T, KD, CT>::bytes(!__is_same(OT, void));
+    const hipError_t e = hipFuncSetAttribute((const void *)linattn_kernel<T, KD, CT, OT>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)bytes);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((linattn_kernel<T, KD, CT, OUT>), dim3(n, jobs), dim3(kLinThreads), bytes,
+    hipLaunchKernelGGL((linattn_kernel<T, KD, CT, OT>), dim3(n), dim3(kLinThreads), bytes,
                        st, g);
     return hipGetLastError();
 }
 
-template <typename T, bool OUT>
-static hipError_t pick_walk(const LinArgs &g, int jobs, int rows, bool wide, hipStream_t st)
+template <typename T, typename OT>
+static hipError_t pick_walk(LinArgs &g, int rows, bool wide, hipStream_t st)
 {
-    if (rows <= 32 && !wide) return launch_walk<T, 32, 1, OUT>(g, jobs, st);
+    if (rows <= 32 && !wide) return launch_walk<T, 32, 1, OT>(g, st);
     if (rows <= 64)
-        return wide ? launch_walk<T, 64, 2, OUT>(g, jobs, st) : launch_walk<T, 64, 1, OUT>(g, jobs, st);
+        return wide ? launch_walk<T, 64, 2, OT>(g, st) : launch_walk<T, 64, 1, OT>(g, st);
     if (rows <= 128)
-        return wide ? launch_walk<T, 128, 2, OUT>(g, jobs, st)
-                    : launch_walk<T, 128, 1, OUT>(g, jobs, st);
-    return wide ? launch_walk<T, 256, 2, OUT>(g, jobs, st) : launch_walk<T, 256, 1, OUT>(g, jobs, st);
+        return wide ? launch_walk<T, 128, 2, OT>(g, st) : launch_walk<T, 128, 1, OT>(g, st);
+    return wide ? launch_walk<T, 256, 2, OT>(g, st) : launch_walk<T, 256, 1, OT>(g, st);
 }
 
 struct LinPlan {
@@ -661,9 +756,40 @@ struct LinPlan {
     size_t off_seg[2], off_dk, off_dv, bytes;
 };
 
-// How the sequence is cut: as many segments as bring two workgroups to each of 256 CUs, of 512
-// tokens at least (a segment's state is written, joined and read again: as many bytes as 190 of
-// its tokens with heads of 128).
+// How the sequence is cut into segments: the count that costs least, in chunks of 64 tokens that a
+// workgroup walks (4.9 us with heads of 128 in bf16).  A workgroup alone on its CU takes 1 for a
+// chunk, two on each CU 1.8 each, about 1 more for the state that it starts and ends with; what a
+// segment adds to the state costs half of that; the launches and the joining 3, and 0.05 a
+// segment.  Measured against other counts (us; the rule's in brackets): forward, 12 heads x 8 rows
+// x 2048 tokens 1: 156, 2: 129, [4: 108], 5: 102, 8: 124; 64 heads x 4 rows x 2048 [1: 173], 2: 199;
+// 16 heads x 65536 tokens 16: 461, [32: 407], 48: 505; gradient, 12 x 8 x 2048 [1: 225], 2: 243,
+// 3: 215, 4: 235.
+static double lin_rounds(int64_t groups)
+{
+    const int64_t full = groups / 512, left = groups % 512;
+    return 1.8 * (double)full + (left == 0 ? 0. : left <= 256 ? 1. : 1. + 0.8 * (left - 256) / 256.);
+}
+static int64_t lin_segments(int64_t heads, int64_t adds, int64_t L)
+{
+    static const int kCounts[] = {1,  2,  3,  4,  5,  6,  7,  8,   10,  12,  14,  16, 20,
+                                  24, 28, 32, 40, 48, 64, 80, 96, 128, 192, 256, 384, 512};
+    const int64_t chunks = (L + 63) / 64;
+    int64_t best = 1;
+    double least = (double)(chunks + 1) * lin_rounds(heads);
+    for (int n : kCounts) {
+        if (n == 1) continue;
+        if (n > chunks || heads > ((int64_t)1 << 20)) break;
+        const int64_t per = (chunks + n - 1) / n;
+        const double t = (double)(per + 1) * lin_rounds(heads * n) +
+                         0.53 * (double)(per + 1) * lin_rounds(adds * (n - 1)) + 3. + 0.05 * n;
+        if (t < least) {
+            least = t;
+            best = n;
+        }
+    }
+    return best;
+}
+
 static LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk, int64_t dv,
                         bool bwd)
 {
@@ -672,11 +798,8 @@ static LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk,
     p.rows = (int)(bwd ? most : dk);
     p.wide = cols > 64;
     p.slices = (int)(p.wide ? (cols + 127) / 128 : 1);
-    const int64_t groups = B * H * p.slices * (bwd ? 3 : 1);
-    int64_t n = groups > 0 ? (512 + groups - 1) / groups : 1;
-    const int64_t longest = (L + 511) / 512;
-    n = n < longest ? n : longest;
-    n = n < 1 ? 1 : n;
+    const int64_t groups = B * H * p.slices;
+    const int64_t n = lin_segments(groups * (bwd ? 3 : 1), groups * (bwd ? 2 : 1), L);
     int64_t seg = ((L + n - 1) / n + 63) / 64 * 64;
     if (seg < 64) seg = 64;
     p.seg = (int)(seg < ((int64_t)1 << 30) ? seg : (int64_t)1 << 30);
@@ -717,24 +840,30 @@ static naju_status_t check_lin(int64_t B, int64_t L, int64_t H, int64_t Hk, int6
     if (B > (1 << 20) || H > 65535 || B * H > (1 << 20) || L > ((int64_t)1 << 30))
         return fail(NAJU_EINVAL, "batch * heads (2^20 max), heads (65535 max) or seqlen (2^30 max) "
                                  "too large");
+    if (H * dk > kLinStride || H * dv > kLinStride)
+        return fail(NAJU_EINVAL, "heads * d_key or heads * d_value (2^20 max) too large");
     if (!(scale >= -1e30f && scale <= 1e30f)) return fail(NAJU_EINVAL, "scale must be finite");
     return NAJU_OK;
 }
 
 static naju_status_t check_ld(int64_t ld, int64_t least, size_t e, const char *name)
 {
-    if (ld < least || ld > ((int64_t)1 << 32) || ld * (int64_t)e % 16 != 0)
-        return fail(NAJU_EINVAL, "token stride of %s (%lld) must be at least %lld elements and a "
+    if (ld < least || ld > kLinStride || ld * (int64_t)e % 16 != 0)
+        return fail(NAJU_EINVAL, "token stride of %s (%lld) must be from %lld to %lld elements and a "
                                  "multiple of 16 bytes",
-                    name, (long long)ld, (long long)least);
+                    name, (long long)ld, (long long)least, (long long)kLinStride);
     return NAJU_OK;
 }
 
-template <bool OUT>
-static hipError_t walk(const LinArgs &g, int jobs, const LinPlan &p, int32_t io, hipStream_t st)
+// the walks g.job[from] .. g.job[to - 1]
+static hipError_t walk(LinArgs g, int from, int to, const LinPlan &p, int32_t io, bool wide_out,
+                       hipStream_t st)
 {
-    return io == NAJU_F32 ? pick_walk<float, OUT>(g, jobs, p.rows, p.wide, st)
-                          : pick_walk<bf16, OUT>(g, jobs, p.rows, p.wide, st);
+    for (int i = from; i < to; ++i) g.job[i - from] = g.job[i];
+    g.jobs = to - from;
+    return io == NAJU_F32 ? pick_walk<float, float>(g, p.rows, p.wide, st)
+           : wide_out     ? pick_walk<bf16, float>(g, p.rows, p.wide, st)
+                          : pick_walk<bf16, bf16>(g, p.rows, p.wide, st);
 }
 
 // the entering states of all segments, for the first `jobs` of g's walks
@@ -756,7 +885,11 @@ static hipError_t enter_segments(LinArgs g, int jobs, const LinPlan &p, char *ws
         J.leave_r = J.D2;
         J.leave_c = 1;
     }
-    const hipError_t e = walk<false>(g, jobs, p, io, st);
+    LinArgs w = g;
+    w.jobs = jobs;
+    w.nseg -= 1;  // (what the last segment adds enters none)
+    const hipError_t e = io == NAJU_F32 ? pick_walk<float, void>(w, p.rows, p.wide, st)
+                                        : pick_walk<bf16, void>(w, p.rows, p.wide, st);
     if (e != hipSuccess) return e;
     // (a launch holds whole batch rows, so that heads and lengths keep their places)
     const int rows = 65535 / g.H * g.H;
@@ -767,7 +900,7 @@ static hipError_t enter_segments(LinArgs g, int jobs, const LinPlan &p, char *ws
             part.seg[i] += (int64_t)at * p.nseg * n;
             if (part.enter[i] != nullptr) part.enter[i] += (int64_t)at * n;
         }
-        hipLaunchKernelGGL(linattn_join_kernel, dim3((n + 255) / 256, now, jobs), dim3(256), 0, st,
+        hipLaunchKernelGGL(linattn_join_kernel, dim3((n + 1023) / 1024, now, jobs), dim3(256), 0, st,
                            part, g.log_decay, g.lengths != nullptr ? g.lengths + at / g.H : nullptr,
                            g.H, n, p.nseg, p.seg, g.L);
         const hipError_t f = hipGetLastError();
@@ -815,7 +948,7 @@ naju_status_t naju_linattn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int
     NAJU_TRY(opt(lengths, "lengths", 4));
     const LinPlan p = lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, false);
     if (p.bytes > 0) NAJU_TRY(need_ws(ws, ws_bytes, p.bytes));
-    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 23))
+    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 21))
         return fail(NAJU_EINVAL, "batch * heads too large for this sequence length");
     const int n = (int)(d_key * d_value);
     LinArgs g{};
@@ -859,7 +992,7 @@ naju_status_t naju_linattn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int
         J.enter_bh = (int64_t)p.nseg * n;
         J.enter_seg = n;
     }
-    return hip_status(walk<true>(g, 1, p, io, st), "linear attention launch");
+    return hip_status(walk(g, 0, 1, p, io, false, st), "linear attention launch");
 }
 
 size_t naju_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
@@ -900,7 +1033,7 @@ naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int
     NAJU_TRY(opt(lengths, "lengths", 4));
     const LinPlan p = lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, true);
     if (p.bytes > 0) NAJU_TRY(need_ws(ws, ws_bytes, p.bytes));
-    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 23))
+    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 21))
         return fail(NAJU_EINVAL, "batch * heads too large for this sequence length");
     const int n = (int)(d_key * d_value), group = (int)(heads / kv_heads);
     char *base = (char *)ws;
@@ -946,7 +1079,6 @@ naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int
     V.ldv = ldg;
     V.gk = V.gv = 1;
     V.o = group > 1 ? (void *)(base + p.off_dv) : dv;
-    V.out_f32 = group > 1;
     V.ldo = heads * d_value;
     V.D1 = (int)d_key;
     V.D2 = (int)d_value;
@@ -989,7 +1121,12 @@ naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int
     K.enter_r = 1;
     K.enter_c = (int)d_value;
     K.leave = nullptr;
-    NAJU_TRY(hip_status(walk<true>(g, 3, p, io, st), "linear attention gradient launch"));
+    if (group == 1 || io == NAJU_F32) {
+        NAJU_TRY(hip_status(walk(g, 0, 3, p, io, false, st), "linear attention gradient launch"));
+    } else {  // (those of shared heads are summed before they are rounded)
+        NAJU_TRY(hip_status(walk(g, 0, 1, p, io, false, st), "linear attention gradient launch"));
+        NAJU_TRY(hip_status(walk(g, 1, 3, p, io, true, st), "linear attention gradient launch"));
+    }
     if (group == 1 || seqlen == 0) return NAJU_OK;
     for (int i = 0; i < 2; ++i) {
         const int64_t D = i ? d_value : d_key, total = batch * seqlen * kv_heads * D;
