@@ -497,7 +497,7 @@ naju_status_t naju_w4_quantize(int64_t d_in, int64_t d_out, int64_t group, int32
  *   scale, w_post, w_pre  [d_model] fp32, each may be NULL (w_pre: no xn)
  *   x_new     [tokens][d_model] x_io (written)
  *   xn        [tokens][d_model] io (written), or NULL with w_pre
- * io BF16 with x_io BF16 or F32, or both F32.  d_model 4 to 16384.  eps >= 0.
+ * io BF16 with x_io BF16 or F32, or both F32.  d_model 4 to 8192.  eps >= 0.
  * Squares are summed as they are: a row whose sum of squares leaves fp32 (values
  * of 1e17 and more) has the norm 0, a row that holds NaN or infinity has NaN.
  */

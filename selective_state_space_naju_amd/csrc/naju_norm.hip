@@ -14,10 +14,16 @@
 //
 // Bound by bytes: every tensor is read or written once, the row's means are
 // taken from registers.  A row belongs to one wave (up to 1024 channels), or to
-// a workgroup of 4 or 16 waves; workgroups walk over rows with the per-channel
+// a workgroup of 4, 8 or 16 waves; workgroups walk over rows with the per-channel
 // vectors, and the gradient's per-channel sums, in registers, and the next row's
 // loads in flight while one is worked on.  Statistics and sums are fp32; each
 // output is rounded once.
+//
+// 16384 x 768, all of it: forward in bf16 with an fp32 stream 35.8 us (4.9 TB/s, a large
+// copy's rate), gradient with an fp32 stream gradient 60 us (4.6 TB/s); 65536 x 2048,
+// gradient 388 us (4.8 TB/s).  Rows that do not fill a wave's or a workgroup's threads
+// waste them (300 channels 3.7 TB/s, 64 channels 1.5), and the gradient beyond 4096
+// channels is bound by its registers (2.2 to 3.6 TB/s).
 #include <math.h>
 
 #include "naju_device.h"
@@ -27,8 +33,7 @@
 
 namespace naju {
 
-constexpr int kNormMost = 16384;   // channels of a row
-constexpr int kNormGroups = 512;   // workgroups of the gradient: rows of partial sums
+constexpr int kNormMost = 8192;  // channels of a row
 
 struct NormArgs {
     int64_t R;
@@ -105,6 +110,18 @@ __device__ __forceinline__ void load_runs(Run<IO, 4> (&r)[K], const void *p, int
     const IO *base = (const IO *)p + row * d;
 #pragma unroll
     for (int k = 0; k < K; ++k) r[k].load_at(base, (uint32_t)at.at[k] * (uint32_t)sizeof(IO));
+}
+
+template <typename IO, int T, int K>
+__device__ __forceinline__ void load_or_zero(Run<IO, 4> (&r)[K], bool given, const void *p,
+                                             int64_t row, int d, const Runs<T, K> &at)
+{
+    if (given) {
+        load_runs<IO, T, K>(r, p, row, d, at);
+    } else {
+#pragma unroll
+        for (int k = 0; k < K; ++k) r[k].zero();
+    }
 }
 
 // (channels that two runs share get the same bits from both)
@@ -221,7 +238,10 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_fwd_kernel(const N
 }
 
 // ------------------------------------------------------------------ backward
-template <typename IO, typename XIO, typename GIO, int W, int K>
+// AHEAD: the next row's loads are in flight while a row is worked on.  Beyond 4096 channels that
+// does not fit the registers; a row then stays packed, unpacked once for the sums and again for the
+// outputs (4882 x 8192: bf16 225 us, fp32 351; with 16 waves and the next row ahead 297 and 480).
+template <typename IO, typename XIO, typename GIO, int W, int K, bool AHEAD>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_bwd_kernel(const NormArgs g)
 {
     constexpr int T = 64 * W, kRows = W == 1 ? 4 : 1;
@@ -245,88 +265,105 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_bwd_kernel(const N
 #pragma unroll
         for (int i = 0; i < 4; ++i) a_pre[k][i] = a_post[k][i] = a_scale[k][i] = 0.f;
 
+    // (what is not given is zero, not left from the row before: nothing lives on)
     Run<XIO, 4> xr[K];
     Run<GIO, 4> er[K], dr[K];
     Run<IO, 4> yr[K], zr[K];
     auto fetch = [&](int64_t r) {
-        if (pre) load_runs<XIO, T, K>(xr, g.x, r, d, at);
-        if (pre) load_runs<GIO, T, K>(er, g.dxn, r, d, at);
-        if (has_dx) load_runs<GIO, T, K>(dr, g.dx_new, r, d, at);
-        if (has_y) load_runs<IO, T, K>(yr, g.y, r, d, at);
-        if (has_z) load_runs<IO, T, K>(zr, g.z, r, d, at);
+        load_or_zero<XIO, T, K>(xr, pre, g.x, r, d, at);
+        load_or_zero<GIO, T, K>(er, pre, g.dxn, r, d, at);
+        load_or_zero<GIO, T, K>(dr, has_dx, g.dx_new, r, d, at);
+        load_or_zero<IO, T, K>(yr, has_y, g.y, r, d, at);
+        load_or_zero<IO, T, K>(zr, has_z, g.z, r, d, at);
     };
-    if (row < g.R) fetch(row);
+    if (AHEAD && row < g.R) fetch(row);
     int slot = 0;
     for (; row < g.R; row += step) {
-        float dx[K][4], y[K][4], z[K][4], e[K][4], x[K][4];
+        if (!AHEAD) fetch(row);
+        Run<XIO, 4> xc[K];
+        Run<GIO, 4> ec[K], dc[K];
+        Run<IO, 4> yc[K], zc[K];
         float sum[3] = {0.f, 0.f, 0.f};  // x'^2, dxn w_pre x', y^2
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            xc[k] = xr[k];
+            ec[k] = er[k];
+            dc[k] = dr[k];
+            yc[k] = yr[k];
+            zc[k] = zr[k];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                dx[k][i] = has_dx ? dr[k].get(i) : 0.f;
-                y[k][i] = has_y ? yr[k].get(i) : 0.f;
-                z[k][i] = has_z ? zr[k].get(i) : 0.f;
-                e[k][i] = pre ? er[k].get(i) : 0.f;
-                x[k][i] = pre ? xr[k].get(i) : 0.f;
-                if (at.counts(k, i)) {
-                    sum[0] = __builtin_fmaf(x[k][i], x[k][i], sum[0]);
-                    sum[1] = __builtin_fmaf(e[k][i] * wi[k][i], x[k][i], sum[1]);
-                    sum[2] = __builtin_fmaf(y[k][i], y[k][i], sum[2]);
+                if (!at.counts(k, i)) continue;
+                if (pre) {
+                    const float x = xc[k].get(i);
+                    sum[0] = __builtin_fmaf(x, x, sum[0]);
+                    sum[1] = __builtin_fmaf(ec[k].get(i) * wi[k][i], x, sum[1]);
                 }
+                if (post) sum[2] = __builtin_fmaf(yc[k].get(i), yc[k].get(i), sum[2]);
             }
+        }
         const int64_t next = row + step;
-        if (next < g.R) fetch(next);
+        if (AHEAD && next < g.R) fetch(next);
         if (pre || post) {
             row_sums<W, 3>(sum, red, slot, w, lane);
             slot ^= 1;
         }
-        if (pre) {
-            const float r = rsqrtf(sum[0] * g.inv_d + g.eps);
-            const float mean = sum[1] * r * g.inv_d;  // of e xh
+        float dx[K][4];
+        const float r = pre ? rsqrtf(sum[0] * g.inv_d + g.eps) : 0.f;
+        const float mean = sum[1] * r * g.inv_d;  // of e xh
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            if (!AHEAD) xc[k].repack();
+            if (!AHEAD) ec[k].repack();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float xh = x[k][i] * r;
-                    a_pre[k][i] = __builtin_fmaf(e[k][i], xh, a_pre[k][i]);
-                    dx[k][i] += r * (e[k][i] * wi[k][i] - xh * mean);
+            for (int i = 0; i < 4; ++i) {
+                dx[k][i] = has_dx ? dc[k].get(i) : 0.f;
+                if (pre) {
+                    const float xh = xc[k].get(i) * r, e = ec[k].get(i);
+                    a_pre[k][i] = __builtin_fmaf(e, xh, a_pre[k][i]);
+                    dx[k][i] += r * (e * wi[k][i] - xh * mean);
                 }
+            }
         }
         store_runs<GIO, T, K>(dx, g.dx, row, d, at);
         if (!has_y) continue;
         const float ry = post ? rsqrtf(sum[2] * g.inv_d + g.eps) : 1.f;
         float dot[1] = {0.f};  // of f w_post and y
-        float dz[K][4];
 #pragma unroll
-        for (int k = 0; k < K; ++k)
+        for (int k = 0; k < K; ++k) {
+            float dz[4];
+            if (!AHEAD) yc[k].repack();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float gate = 1.f, slope = 0.f;
                 if (has_z) {
-                    const float sig = sigm(z[k][i]);
-                    gate = z[k][i] * sig;
-                    slope = sig * __builtin_fmaf(z[k][i], 1.f - sig, 1.f);
+                    const float z = zc[k].get(i), sig = sigm(z);
+                    gate = z * sig;
+                    slope = sig * __builtin_fmaf(z, 1.f - sig, 1.f);
                 }
-                const float yh = y[k][i] * ry, n = yh * wo[k][i];
+                const float yh = yc[k].get(i) * ry, n = yh * wo[k][i];
                 const float t = dx[k][i] * s[k][i];
                 a_scale[k][i] = __builtin_fmaf(dx[k][i] * gate, n, a_scale[k][i]);
-                dz[k][i] = t * n * slope;
+                dz[i] = t * n * slope;
                 const float f = t * gate;
                 a_post[k][i] = __builtin_fmaf(f, yh, a_post[k][i]);
                 dx[k][i] = f * wo[k][i];
-                y[k][i] = yh;
                 if (at.counts(k, i)) dot[0] = __builtin_fmaf(dx[k][i], yh, dot[0]);
             }
-        if (has_z) store_runs<IO, T, K>(dz, g.dz, row, d, at);
+            if (has_z && at.skip[k] < 4)
+                round_run<IO, 4>(dz).store_at((IO *)g.dz + row * d,
+                                              (uint32_t)at.at[k] * (uint32_t)sizeof(IO));
+        }
         if (post) {
             row_sums<W, 1>(dot, red, slot, w, lane);
             slot ^= 1;
-            const float mean = dot[0] * g.inv_d;
+            const float m = dot[0] * g.inv_d;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
+            for (int k = 0; k < K; ++k) {
+                if (!AHEAD) yc[k].repack();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) dx[k][i] = ry * (dx[k][i] - y[k][i] * mean);
+                for (int i = 0; i < 4; ++i) dx[k][i] = ry * (dx[k][i] - yc[k].get(i) * ry * m);
+            }
         }
         store_runs<IO, T, K>(dx, g.dy, row, d, at);
     }
@@ -407,20 +444,21 @@ template <typename IO, typename XIO> static hipError_t pick_fwd(const NormArgs &
     if (g.d <= 1024) return launch_fwd<IO, XIO, 1, 4>(g, st);
     if (g.d <= 2048) return launch_fwd<IO, XIO, 4, 2>(g, st);
     if (g.d <= 4096) return launch_fwd<IO, XIO, 4, 4>(g, st);
-    if (g.d <= 8192) return launch_fwd<IO, XIO, 16, 2>(g, st);
-    return launch_fwd<IO, XIO, 16, 4>(g, st);
+    return launch_fwd<IO, XIO, 16, 2>(g, st);
 }
 
+// Workgroups of the gradient, each with a row of partial sums: as many as are resident.
 static int bwd_groups(int64_t R, int64_t d)
 {
     const int64_t blocks = d <= 1024 ? (R + 3) / 4 : R;
-    return (int)(blocks < kNormGroups ? blocks : kNormGroups);
+    const int64_t most = d <= 256 ? 1536 : d <= 2048 ? 512 : 256;
+    return (int)(blocks < most ? blocks : most);
 }
 
 template <typename IO, typename XIO, typename GIO, int W, int K>
 static hipError_t launch_bwd(const NormArgs &g, hipStream_t st)
 {
-    hipLaunchKernelGGL((norm_bwd_kernel<IO, XIO, GIO, W, K>), dim3(bwd_groups(g.R, g.d)),
+    hipLaunchKernelGGL((norm_bwd_kernel<IO, XIO, GIO, W, K, (W * K < 32)>), dim3(bwd_groups(g.R, g.d)),
                        dim3(W == 1 ? 256 : 64 * W), 0, st, g);
     return hipGetLastError();
 }
@@ -433,9 +471,8 @@ static hipError_t pick_bwd(const NormArgs &g, hipStream_t st)
     if (g.d <= 768) return launch_bwd<IO, XIO, GIO, 1, 3>(g, st);
     if (g.d <= 1024) return launch_bwd<IO, XIO, GIO, 1, 4>(g, st);
     if (g.d <= 2048) return launch_bwd<IO, XIO, GIO, 4, 2>(g, st);
-    if (g.d <= 4096) return launch_bwd<IO, XIO, GIO, 4, 4>(g, st);
-    if (g.d <= 8192) return launch_bwd<IO, XIO, GIO, 16, 2>(g, st);
-    return launch_bwd<IO, XIO, GIO, 16, 4>(g, st);
+    if (g.d <= 4096) return launch_bwd<IO, XIO, GIO, 8, 2>(g, st);
+    return launch_bwd<IO, XIO, GIO, 8, 4>(g, st);
 }
 
 static naju_status_t check_norm(int64_t R, int64_t d, int32_t io, int32_t x_io, int32_t g_io,

@@ -34,7 +34,7 @@ def test_res_norm_fwd_refusals(lib):
     expect(call(io=3), nb.EINVAL, "io dtype")
     expect(call(xio=7), nb.EINVAL, "io dtype")
     expect(call(io=nb.F32, xio=nb.BF16), nb.EUNSUPPORTED, "fp32")
-    for d in (1, 3, 16385):
+    for d in (1, 3, 8193):
         expect(call(d=d), nb.EUNSUPPORTED, "d_model")
     for eps in (-1.0, float("nan"), float("inf")):
         expect(call(eps=eps), nb.EINVAL, "eps")
