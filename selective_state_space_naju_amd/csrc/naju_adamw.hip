@@ -17,6 +17,9 @@
 // table in device memory, which would have to be kept in step with gradients that
 // move, and nothing to copy before the launch.  A workgroup finds its tensor by
 // bisection over the first units of each.
+//
+// 138 M parameters with bf16 gradients and copies 738 us (28 bytes each, 5.2 TB/s, a large
+// copy's rate); 200 M with 8-bit states and fp32 gradients 646 us (16 bytes, 5.0 TB/s).
 #include <math.h>
 #include <stdlib.h>
 

@@ -29,6 +29,17 @@
 // bf16: v_mfma_f32_16x16x32_bf16 with fp32 sums; scores and state enter products as
 // bf16 hi + lo (2^-16), the decayed values of the state's sum in three bf16 parts
 // (fp32's precision: the state is an fp32 output).  fp32: v_mfma_f32_16x16x4_f32.
+//
+// Bound by a chunk's length in time: its loads, two barriers and three rounds of
+// products follow one another, and registers leave room for two workgroups a CU to
+// cover that.  8 x 2048 x 64 heads x 128 (a full chip) forward 282 us, 3.8 TB/s of its
+// inputs and outputs; few heads are cut into segments, which read k and v twice: 65536
+// x 16 x 128 forward 418 us (2.6 TB/s), 8 x 2048 x 12 x 128 gradient 219 us (its three
+// walks and their segments read 9 tensors where 4 are needed); fp32 3 x 333 x 5 heads of 40
+// and 72 forward 24 us.  Not faster in the same place: eight waves of 16 columns (330 us, one
+// workgroup a CU), LDS reads a step ahead of the products (345, one workgroup a CU; two
+// spill), splitting values by hand between the products (334), loads that bypass the
+// caches (332 to 341).
 #include <math.h>
 
 #include "naju_device.h"
@@ -82,10 +93,11 @@ struct LinArgs {
 // element slot_step(j) + 4 h, the order in which the matrix instruction leaves two tiles of 16
 // rows in a lane's registers.
 //
-// Rows of LDS tiles lie 32 bytes further in the 64 banks than the one before.  Measured with the
-// bank-conflict counter (cycles of an access of the wave, the least in brackets): 16-byte reads of
-// 16 rows 4 (4), and 8 with rows 16 bytes further; transposing reads of 16 neighbouring columns
-// 2 (2), of columns 16 bytes apart 4.
+// Rows of LDS tiles lie 32 bytes further in the 64 banks than the one before.  Cycles of one
+// wave's access with eight waves at it: transposing reads 7 whichever columns the lanes take,
+// 16-byte reads of 16 rows 8; two 8-byte reads of 16 rows (slot_step's order) 32, and 16 where rows
+// lie 16 bytes further.  Those read q alone; rows 16 bytes further, or 16-byte reads of a second
+// order of k, made the walk slower all the same (362 to 390 us against 366).
 __device__ __forceinline__ constexpr int slot_step(int j) { return 16 * (j >> 2) + (j & 3); }
 
 template <typename T> struct Frag;

@@ -21,9 +21,9 @@
 //
 // 16384 x 768, all of it: forward in bf16 with an fp32 stream 35.8 us (4.9 TB/s, a large
 // copy's rate), gradient with an fp32 stream gradient 60 us (4.6 TB/s); 65536 x 2048,
-// gradient 388 us (4.8 TB/s).  Rows that do not fill a wave's or a workgroup's threads
+// gradient 342 us (5.5 TB/s).  Rows that do not fill a wave's or a workgroup's threads
 // waste them (300 channels 3.7 TB/s, 64 channels 1.5), and the gradient beyond 4096
-// channels is bound by its registers (2.2 to 3.6 TB/s).
+// channels is bound by its registers (8192 channels, below).
 #include <math.h>
 
 #include "naju_device.h"
