@@ -225,6 +225,8 @@ def _on_its_device(fn):
     @functools.wraps(fn)
     def call(*args, **kw):
         t = args[0] if args else kw.get(first)
+        if t is None:  # (a gradient that is not given: the next tensor's device)
+            t = next((a for a in (*args, *kw.values()) if isinstance(a, torch.Tensor)), None)
         device = t.get_device() if t is not None else -1  # (-1 in host memory)
         if device < 0 or device == _current_device():
             return fn(*args, **kw)
@@ -890,9 +892,9 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
     n = len(params)
     if n == 0:
         return
-    dev = params[0].device
-    if dev.index is not None and dev.index != _current_device():
-        with torch.cuda.device(dev):
+    index, dev = params[0].get_device(), params[0].device
+    if index >= 0 and index != _current_device():
+        with torch.cuda.device(index):
             return adamw_step(params, grads, m, v, step, lr, beta1, beta2, eps, weight_decay,
                               m_scale=m_scale, v_scale=v_scale, grad_scale=grad_scale,
                               copies=copies, out=out)
@@ -931,12 +933,18 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
         every += ts
         types += [dt] * n
         counts += blocks if of_blocks else sizes
-    fits = (list(map(_dtype_of, every)) == types and set(map(T.get_device, every)) == {dev.index}
-            and all(map(T.is_contiguous, every)) and list(map(T.numel, every)) == counts
-            and list(map(_shape_of, grads)) == list(map(_shape_of, params)))
+    try:
+        fits = (list(map(_dtype_of, every)) == types
+                and set(map(T.get_device, every)) == {index}
+                and all(map(T.is_contiguous, every)) and list(map(T.numel, every)) == counts
+                and list(map(_shape_of, grads)) == list(map(_shape_of, params)))
+    except TypeError:  # something that is no tensor: a gradient that is None, say
+        fits = False
     if not fits:  # which one, and what is wrong with it
         for _, k, ts, dt, of_blocks in lists:
             for i, t in enumerate(ts):
+                if not isinstance(t, T):
+                    raise ValueError("%s[%d] is required" % (k, i))
                 shape = (blocks[i],) if of_blocks else params[i].shape if k == "g" else t.shape
                 _req(t, "%s[%d]" % (k, i), shape, dt, dev)
                 if t.numel() != (blocks if of_blocks else sizes)[i]:
