@@ -930,7 +930,8 @@ extern "C" {
 size_t naju_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
                                         int64_t kv_heads, int64_t d_key, int64_t d_value)
 {
-    if (check_lin(batch, seqlen, heads, kv_heads, d_key, d_value, NAJU_F32, 1.f) != NAJU_OK)
+    if (check_lin(batch, seqlen, heads, kv_heads, d_key, d_value, NAJU_F32, 1.f) != NAJU_OK ||
+        batch == 0 || heads == 0)  // (without heads the other sizes are not looked at)
         return 0;
     return lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, false).bytes;
 }
@@ -1010,7 +1011,8 @@ naju_status_t naju_linattn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int
 size_t naju_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
                                         int64_t kv_heads, int64_t d_key, int64_t d_value)
 {
-    if (check_lin(batch, seqlen, heads, kv_heads, d_key, d_value, NAJU_F32, 1.f) != NAJU_OK)
+    if (check_lin(batch, seqlen, heads, kv_heads, d_key, d_value, NAJU_F32, 1.f) != NAJU_OK ||
+        batch == 0 || heads == 0)  // (without heads the other sizes are not looked at)
         return 0;
     return lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, true).bytes;
 }
