@@ -813,11 +813,15 @@ def _norm_args(x, y, z, scale, w_post, w_pre, like):
     st = _stream(dev)
     if y is None and (z is not None or scale is not None or w_post is not None):
         raise ValueError("z, scale and w_post need y")
-    io_dt = y.dtype if y is not None else like
-    for nm, t in (("y", y), ("z", z)):
-        _opt(t, nm, x.shape, io_dt, dev)
+    io_dt = like
+    if y is not None:
+        io_dt = y.dtype
+        _req(y, "y", x.shape, io_dt, dev)
+        if z is not None:
+            _req(z, "z", x.shape, io_dt, dev)
     for nm, t in (("scale", scale), ("w_post", w_post), ("w_pre", w_pre)):
-        _opt(t, nm, (d,), torch.float32, dev)
+        if t is not None:
+            _req(t, nm, (d,), torch.float32, dev)
     return (x.numel() // d if d else 0), d, dev, st, io_dt
 
 
@@ -835,8 +839,11 @@ def res_norm_fwd(x, y=None, z=None, *, scale=None, w_post=None, w_pre=None, eps=
     io, x_io = _code(io_dt), _io_of(x)
     if y is None and w_pre is None:
         raise ValueError("neither y nor w_pre is given: nothing to compute")
+    # (empty_like: 1.2 us a call where empty takes 2.3)
     x_new = torch.empty_like(x) if y is not None else None
-    xn = torch.empty(x.shape, dtype=io_dt, device=dev) if w_pre is not None else None
+    xn = None
+    if w_pre is not None:
+        xn = torch.empty_like(y) if y is not None else torch.empty_like(x, dtype=io_dt)
     check(lib().naju_res_norm_fwd(T, d, io, x_io, _p(x), _p(y), _p(z), _p(scale), _p(w_post),
                                   _p(w_pre), float(eps), _p(x_new), _p(xn), st))
     return (x if y is None else x_new), xn
@@ -1073,7 +1080,7 @@ def linattn_step(q, k, v, log_decay, state, scale=None, *, state_out=None):
     _req(log_decay, "log_decay", (H,), torch.float32, dev)
     _req(state, "state", (B, H, dk, dv), torch.float32, dev)
     _opt(state_out, "state_out", (B, H, dk, dv), torch.float32, dev)
-    o = torch.empty((B, H, dv), dtype=dt, device=dev)
+    o = torch.empty_like(v) if Hk == H else torch.empty((B, H, dv), dtype=dt, device=dev)
     check(lib().naju_linattn_step(B, H, Hk, dk, dv, io, _p(q), _p(k), _p(v), _p(log_decay),
                                   _p(state), dk ** -0.5 if scale is None else float(scale), _p(o),
                                   _p(state if state_out is None else state_out), st))
