@@ -974,6 +974,9 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
 def _req_tokens(t, name, shape, dtype, device) -> int:
     """A tensor [batch, tokens, heads, d] whose tokens' heads are contiguous and whose tokens lie
     any one distance apart (a part of a joint projection); returns that distance."""
+    if (t is not None and t.shape == shape and t.dtype == dtype and t.device == device
+            and t.is_contiguous()):
+        return shape[2] * shape[3]
     if t is None:
         raise ValueError("%s is required" % name)
     if tuple(t.shape) != shape:
@@ -983,8 +986,6 @@ def _req_tokens(t, name, shape, dtype, device) -> int:
     if t.device != device:
         raise ValueError("%s must be on %s" % (name, device))
     B, L, H, d = shape
-    if t.is_contiguous():
-        return H * d
     sb, sl, sh, sd = t.stride()
     if L == 1:
         sl = sb if B > 1 else H * d
@@ -1031,9 +1032,12 @@ def linattn_fwd(q, k, v, log_decay, state=None, lengths=None, scale=None, *, sta
     itself among them."""
     (B, L, H, Hk, dk, dv), dt, dev, st, args = _linattn_args(q, k, v, log_decay, state, lengths,
                                                               scale)
-    o = torch.empty((B, L, H, dv), dtype=dt, device=dev)
+    # (empty_like: 1.2 us a call where empty takes 2.3)
+    o = (torch.empty_like(v) if Hk == H and v.is_contiguous() else
+         torch.empty((B, L, H, dv), dtype=dt, device=dev))
     if state_out is None:
-        state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+        state_out = (torch.empty_like(state) if state is not None else
+                     torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev))
     else:
         _req(state_out, "state_out", (B, H, dk, dv), torch.float32, dev)
     nbytes = lib().naju_linattn_fwd_workspace_bytes(B, L, H, Hk, dk, dv) if ws is None else 0

@@ -36,7 +36,7 @@
 // inputs and outputs; few heads are cut into segments, which read k and v twice: 65536
 // x 16 x 128 forward 418 us (2.6 TB/s), 8 x 2048 x 12 x 128 gradient 219 us (its three
 // walks and their segments read 9 tensors where 4 are needed); fp32 3 x 333 x 5 heads of 40
-// and 72 forward 24 us.  Not faster in the same place: eight waves of 16 columns (330 us, one
+// and 72 forward 17 us in a graph.  Not faster in the same place: eight waves of 16 columns (330 us, one
 // workgroup a CU), LDS reads a step ahead of the products (345, one workgroup a CU; two
 // spill), splitting values by hand between the products (334), loads that bypass the
 // caches (332 to 341).
@@ -741,11 +741,13 @@ static hipError_t launch_walk(LinArgs &g, hipStream_t st)
 {
     g.items = g.B * g.H * g.slices * g.nseg;
     const int n = (g.items + 7) / 8 * 8 * g.jobs;
-    const size_t bytes = LinShape<T, KD, CT>::bytes(!__is_same(OT, void));
-    const hipError_t e = hipFuncSetAttribute((const void *)linattn_kernel<T, KD, CT, OT>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)bytes);
-    if (e != hipSuccess) return e;
+    constexpr size_t bytes = LinShape<T, KD, CT>::bytes(!__is_same(OT, void));
+    if constexpr (bytes > 65536) {  // (more than a kernel may take unasked)
+        const hipError_t e = hipFuncSetAttribute((const void *)linattn_kernel<T, KD, CT, OT>,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (int)bytes);
+        if (e != hipSuccess) return e;
+    }
     hipLaunchKernelGGL((linattn_kernel<T, KD, CT, OT>), dim3(n), dim3(kLinThreads), bytes,
                        st, g);
     return hipGetLastError();
@@ -768,36 +770,49 @@ struct LinPlan {
     size_t off_seg[2], off_dk, off_dv, bytes;
 };
 
-// How the sequence is cut into segments: the count that costs least, in chunks of 64 tokens that a
-// workgroup walks (4.9 us with heads of 128 in bf16).  A workgroup alone on its CU takes 1 for a
-// chunk, two on each CU 1.8 each, about 1 more for the state that it starts and ends with; what a
-// segment adds to the state costs half of that; the launches and the joining 3, and 0.05 a
-// segment.  Measured against other counts (us; the rule's in brackets): forward, 12 heads x 8 rows
-// x 2048 tokens 1: 156, 2: 129, [4: 108], 5: 102, 8: 124; 64 heads x 4 rows x 2048 [1: 173], 2: 199;
-// 16 heads x 65536 tokens 16: 461, [32: 407], 48: 505; gradient, 12 x 8 x 2048 [1: 225], 2: 243,
-// 3: 215, 4: 235.
-static double lin_rounds(int64_t groups)
+// How wide a workgroup's part of the state is, 128 or 64 columns, and how the sequence is cut into
+// segments: what costs least, in chunks of 64 tokens that a workgroup of 128 columns walks alone on
+// its CU (4.9 us with heads of 128 in bf16).  With 64 columns a chunk takes 0.7; two workgroups on
+// each CU 1.8 each, 1.05 with 64 columns (with keys beyond 128 a CU holds one).  1 more for the state
+// that it starts and ends with, 2 with keys beyond 128; what a segment adds to the state costs 0.53
+// of a walk, 0.45 with 64 columns; the launches and the joining 1, 1.5 with keys up to 64, whose
+// chunks are shorter, and 0.1 a segment.  Measured against other choices, the rule's in brackets (us,
+// columns x segments).  Forward, heads of 128: 8 rows x 2048 tokens x 12 heads 128x1: 150, [128x4:
+// 110], 128x5: 106, 64x1: 122, 64x4: 122; 4 x 2048 x 64 [128x1: 177], 64x1: 182, 128x2: 206; 65536 x
+// 16 128x16: 496, [128x32: 451], 64x32: 532; 2 x 4096 x 32 64x4: 134, [128x8: 123], 128x1: 292; 2048
+// x 4 128x16: 37, 64x8: 36, [64x16: 30]; heads of 256, 4 x 1024 x 16 [64x1: 104], 128x1: 144; heads
+// of 64, 2 x 4096 x 8 1: 135, 8: 39, [16: 30], 24: 31; fp32, 3 x 333 x 5 heads of 40 and 72 128x6: 22,
+// [64x6: 17], 64x1: 30.  Gradient: 8 x 2048 x 12 [128x1: 228], 128x3: 222, 64x1: 270; 2 x 4096 x 32
+// 128x1: 298, 128x4: 269, [64x1: 309]; 1000 x 12 128x6: 44, [64x6: 38], 64x1: 60; heads of 256, 4 x
+// 1024 x 16 [128x1: 263], 64x1: 294, 128x2: 351.
+static double lin_rounds(int64_t groups, bool wide, int rows)
 {
+    const double lone = wide ? 1. : 0.7, two = rows > 128 ? 2. * lone : wide ? 1.8 : 1.05;
     const int64_t full = groups / 512, left = groups % 512;
-    return 1.8 * (double)full + (left == 0 ? 0. : left <= 256 ? 1. : 1. + 0.8 * (left - 256) / 256.);
+    const double part = rows > 128 ? (left > 256 ? 1. : 0.) : (left - 256) / 256.;
+    return two * (double)full +
+           (left == 0 ? 0. : left <= 256 ? lone : lone + (two - lone) * part);
 }
-static int64_t lin_segments(int64_t heads, int64_t adds, int64_t L)
+struct LinCut {
+    int64_t n;
+    double cost;
+};
+// heads: walks of the call, adds: those whose segments add to the state first
+static LinCut lin_segments(int64_t heads, int64_t adds, int64_t L, bool wide, int rows)
 {
-    static const int kCounts[] = {1,  2,  3,  4,  5,  6,  7,  8,   10,  12,  14,  16, 20,
-                                  24, 28, 32, 40, 48, 64, 80, 96, 128, 192, 256, 384, 512};
+    static const int kCounts[] = {2,  3,  4,  5,  6,  7,  8,  10, 12,  14,  16,  20, 24,
+                                  28, 32, 40, 48, 64, 80, 96, 128, 192, 256, 384, 512};
     const int64_t chunks = (L + 63) / 64;
-    int64_t best = 1;
-    double least = (double)(chunks + 1) * lin_rounds(heads);
+    const int64_t ends = rows > 128 ? 2 : 1;
+    LinCut best{1, (double)(chunks + ends) * lin_rounds(heads, wide, rows)};
     for (int n : kCounts) {
-        if (n == 1) continue;
         if (n > chunks || heads > ((int64_t)1 << 20)) break;
         const int64_t per = (chunks + n - 1) / n;
-        const double t = (double)(per + 1) * lin_rounds(heads * n) +
-                         0.53 * (double)(per + 1) * lin_rounds(adds * (n - 1)) + 3. + 0.05 * n;
-        if (t < least) {
-            least = t;
-            best = n;
-        }
+        const double t = (double)(per + ends) * (lin_rounds(heads * n, wide, rows) +
+                                                 (wide ? 0.53 : 0.45) *
+                                                     lin_rounds(adds * (n - 1), wide, rows)) +
+                         (rows > 64 ? 1. : 1.5) + 0.1 * n;
+        if (t < best.cost) best = {n, t};
     }
     return best;
 }
@@ -808,10 +823,19 @@ static LinPlan lin_plan(int64_t B, int64_t L, int64_t H, int64_t Hk, int64_t dk,
     LinPlan p{};
     const int64_t most = dk > dv ? dk : dv, cols = bwd ? most : dv;
     p.rows = (int)(bwd ? most : dk);
-    p.wide = cols > 64;
-    p.slices = (int)(p.wide ? (cols + 127) / 128 : 1);
-    const int64_t groups = B * H * p.slices;
-    const int64_t n = lin_segments(groups * (bwd ? 3 : 1), groups * (bwd ? 2 : 1), L);
+    int64_t n = 0;
+    double least = 0.;
+    for (const bool wide : {false, true}) {
+        if (wide && cols <= 64) break;
+        const int64_t slices = wide ? (cols + 127) / 128 : (cols + 63) / 64, groups = B * H * slices;
+        const LinCut cut = lin_segments(groups * (bwd ? 3 : 1), groups * (bwd ? 2 : 1), L, wide,
+                                        p.rows);
+        if (n > 0 && cut.cost > least) break;
+        n = cut.n;
+        least = cut.cost;
+        p.wide = wide;
+        p.slices = (int)slices;
+    }
     int64_t seg = ((L + n - 1) / n + 63) / 64 * 64;
     if (seg < 64) seg = 64;
     p.seg = (int)(seg < ((int64_t)1 << 30) ? seg : (int64_t)1 << 30);
@@ -961,7 +985,7 @@ naju_status_t naju_linattn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int
     NAJU_TRY(opt(lengths, "lengths", 4));
     const LinPlan p = lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, false);
     if (p.bytes > 0) NAJU_TRY(need_ws(ws, ws_bytes, p.bytes));
-    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 21))
+    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 22))
         return fail(NAJU_EINVAL, "batch * heads too large for this sequence length");
     const int n = (int)(d_key * d_value);
     LinArgs g{};
@@ -1047,7 +1071,7 @@ naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int
     NAJU_TRY(opt(lengths, "lengths", 4));
     const LinPlan p = lin_plan(batch, seqlen, heads, kv_heads, d_key, d_value, true);
     if (p.bytes > 0) NAJU_TRY(need_ws(ws, ws_bytes, p.bytes));
-    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 21))
+    if (batch * heads * p.slices * p.nseg > ((int64_t)1 << 22))
         return fail(NAJU_EINVAL, "batch * heads too large for this sequence length");
     const int n = (int)(d_key * d_value), group = (int)(heads / kv_heads);
     char *base = (char *)ws;
