@@ -9,7 +9,6 @@ fallback path.
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import functools
 import inspect
@@ -140,8 +139,7 @@ def lib() -> ctypes.CDLL:
                                         [sz, vp])
         L.naju_res_norm_bwd.restype = st
         f64 = ctypes.c_double
-        L.naju_adamw_step.argtypes = ([i64, ctypes.POINTER(AdamwTensor), i32, i32] + [f64] * 5 +
-                                      [i64, vp, vp, vp, vp])
+        L.naju_adamw_step.argtypes = [i64, vp, i32, i32] + [f64] * 5 + [i64, vp, vp, vp, vp]
         L.naju_adamw_step.restype = st
         for name in ("naju_linattn_fwd_workspace_bytes", "naju_linattn_bwd_workspace_bytes"):
             getattr(L, name).argtypes = [i64] * 6
@@ -878,7 +876,17 @@ def res_norm_bwd(dxn, dx_new, x_new, y=None, z=None, *, scale=None, w_post=None,
     return out
 
 
-_dtype_of, _shape_of = torch.Tensor.dtype.__get__, torch.Tensor.shape.__get__
+_table = None
+
+
+def _load_table():
+    global _table
+    try:
+        from . import _tensors
+    except ImportError as e:
+        raise ImportError("_tensors.so cannot be loaded (%s); build it with "
+                          "`python -m selective_state_space_naju_amd.build`" % e)
+    _table = _tensors.table
 
 
 def _one_value(t, name, dtype, dev):
@@ -915,58 +923,45 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
     g_dt = grads[0].dtype if len(grads) else torch.float32
     io = _code(g_dt)
     f32 = torch.float32
-    # the fields that are given: place in the table, name, tensors, type, whether of a scale's shape
-    lists = [(1, "p", params, f32, False), (2, "g", grads, g_dt, False), (3, "m", m, s_dt, False),
-             (4, "v", v, s_dt, False)]
+    # the fields that are given: place in the table, name, tensors, type, and what has to agree with
+    # the parameters: the number of elements (0), the shape (1), the number of blocks (2)
+    lists = [(1, "p", params, f32, 0), (2, "g", grads, g_dt, 1), (3, "m", m, s_dt, 0),
+             (4, "v", v, s_dt, 0)]
     if eight:
-        lists += [(5, "m_scale", m_scale, f32, True), (6, "v_scale", v_scale, f32, True)]
+        lists += [(5, "m_scale", m_scale, f32, 2), (6, "v_scale", v_scale, f32, 2)]
     if out is not None:
         names = ("p", "m", "v", "m_scale", "v_scale")[:5 if eight else 3]
         if set(out) != set(names):
             raise ValueError("out: expected the lists %s" % ", ".join(names))
-        lists += [(7 + i, k + "_out", out[k], (f32, s_dt, s_dt, f32, f32)[i], i > 2)
+        lists += [(7 + i, k + "_out", out[k], (f32, s_dt, s_dt, f32, f32)[i], 2 if i > 2 else 0)
                   for i, k in enumerate(names)]
     if copies is not None:
-        lists.append((12, "copy", copies, torch.bfloat16, False))
-    # Checks over all tensors at once, property by property: 0.2 us a tensor, where checking
-    # tensor by tensor takes a microsecond.
-    T = torch.Tensor
-    sizes = list(map(T.numel, params))
-    blocks = [(k + 255) // 256 for k in sizes] if eight else None
-    every, types, counts = [], [], []
-    for _, k, ts, dt, of_blocks in lists:
+        lists.append((12, "copy", copies, torch.bfloat16, 0))
+    for _, k, ts, dt, _ in lists:
         if len(ts) != n:
             raise ValueError("%s: expected %d tensors, got %d" % (k, n, len(ts)))
-        every += ts
-        types += [dt] * n
-        counts += blocks if of_blocks else sizes
-    try:
-        fits = (list(map(_dtype_of, every)) == types
-                and set(map(T.get_device, every)) == {index}
-                and all(map(T.is_contiguous, every)) and list(map(T.numel, every)) == counts
-                and list(map(_shape_of, grads)) == list(map(_shape_of, params)))
-    except TypeError:  # something that is no tensor: a gradient that is None, say
-        fits = False
-    if not fits:  # which one, and what is wrong with it
-        for _, k, ts, dt, of_blocks in lists:
+    if _table is None:
+        _load_table()
+    # one pass over all tensors outside Python (there a property of a tensor takes 40 ns)
+    table = _table(13, index, 256, tuple(
+        (at, ts if isinstance(ts, (list, tuple)) else list(ts), dt, kind)
+        for at, _, ts, dt, kind in lists))
+    if table is None:  # which one, and what is wrong with it
+        for _, k, ts, dt, kind in lists:
             for i, t in enumerate(ts):
-                if not isinstance(t, T):
+                if not isinstance(t, torch.Tensor):
                     raise ValueError("%s[%d] is required" % (k, i))
-                shape = (blocks[i],) if of_blocks else params[i].shape if k == "g" else t.shape
+                count = -(-params[i].numel() // 256) if kind == 2 else params[i].numel()
+                shape = (count,) if kind == 2 else params[i].shape if kind == 1 else t.shape
                 _req(t, "%s[%d]" % (k, i), shape, dt, dev)
-                if t.numel() != (blocks if of_blocks else sizes)[i]:
+                if t.numel() != count:
                     raise ValueError("%s[%d]: expected %d elements, got %d" %
-                                     (k, i, sizes[i], t.numel()))
-    addresses = array.array("Q", map(T.data_ptr, every))
-    table = array.array("Q", bytes(8 * 13 * n))
-    table[0::13] = array.array("Q", sizes)
-    for j, field in enumerate(lists):
-        table[field[0]::13] = addresses[j * n:(j + 1) * n]
-    table = ctypes.cast(table.buffer_info()[0], ctypes.POINTER(AdamwTensor)), table
+                                     (k, i, count, t.numel()))
+        raise ValueError("tensors must be strided, on %s" % dev)
     step_dev = _one_value(step, "step", torch.int32, dev) if torch.is_tensor(step) else None
     lr_dev = _one_value(lr, "lr", f32, dev) if torch.is_tensor(lr) else None
     gs = _one_value(grad_scale, "grad_scale", f32, dev) if grad_scale is not None else None
-    check(lib().naju_adamw_step(n, table[0], io, 8 if eight else 32, 0.0 if lr_dev else float(lr),
+    check(lib().naju_adamw_step(n, table, io, 8 if eight else 32, 0.0 if lr_dev else float(lr),
                                 beta1, beta2, eps, weight_decay, 0 if step_dev else int(step),
                                 step_dev, lr_dev, gs, st))
 

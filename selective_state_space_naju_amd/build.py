@@ -1,4 +1,4 @@
-"""Builds libnaju.so (hipcc, gfx950) in-tree.
+"""Builds libnaju.so (hipcc, gfx950) and the binding's _tensors.so (g++) in-tree.
 
     python -m selective_state_space_naju_amd.build [--verbose]
 
@@ -11,12 +11,14 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnaju.so")
+TENSORS = os.path.join(HERE, "_tensors.so")
 SOURCES = ["naju_api.hip", "naju_fwd.hip", "naju_fwd_mfma.hip", "naju_fwd_mfma64.hip", "naju_bwd.hip",
            "naju_bwd_mfma.hip",
            "naju_step.hip", "naju_mixer.hip", "naju_embed.hip",
@@ -52,10 +54,31 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_tensors() -> None:
+    """The binding's helper for lists of tensors: host code on torch's headers."""
+    import torch
+    from torch.utils import cpp_extension
+    tmp = TENSORS + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
+    cmd += ["-I" + d for d in cpp_extension.include_paths()]
+    cmd += ["-I" + sysconfig.get_paths()["include"], os.path.join(CSRC, "naju_tensors.cpp"),
+            "-o", tmp]
+    cmd += ["-L" + d for d in cpp_extension.library_paths()]
+    r = subprocess.run(cmd + ["-ltorch_python", "-ltorch_cpu", "-lc10"], capture_output=True,
+                       text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for naju_tensors.cpp:\n%s" % r.stderr)
+    os.replace(tmp, TENSORS)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link libnaju.so.  Returns the library path."""
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    """Compile every HIP source, link libnaju.so, and compile _tensors.so.  Returns the path of
+    libnaju.so."""
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        tensors = ex.submit(_compile_tensors)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        tensors.result()
     tmp = LIB + ".tmp%d" % os.getpid()
     # (hipBLASLt runs the mixer layer's projections)
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs + [
