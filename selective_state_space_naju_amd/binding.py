@@ -864,7 +864,7 @@ def res_norm_bwd(dxn, dx_new, x_new, y=None, z=None, *, scale=None, w_post=None,
     g_dt = (dxn if dxn is not None else dx_new).dtype
     _opt(dxn, "dxn", x_new.shape, g_dt, dev)
     _opt(dx_new, "dx_new", x_new.shape, g_dt, dev)
-    out = {"dx": torch.empty(x_new.shape, dtype=g_dt, device=dev)}
+    out = {"dx": torch.empty_like(dxn if dxn is not None else dx_new)}
     for nm, t in (("dy", y), ("dz", z), ("dscale", scale), ("dw_post", w_post), ("dw_pre", w_pre)):
         out[nm] = torch.empty_like(t) if t is not None else None
     nbytes = lib().naju_res_norm_bwd_workspace_bytes(T, d) if ws is None else ws.nbytes
@@ -1051,10 +1051,12 @@ def linattn_bwd(q, k, v, log_decay, do, state=None, dstate=None, lengths=None, s
                                                               scale)
     _req(do, "do", (B, L, H, dv), dt, dev)
     _opt(dstate, "dstate", (B, H, dk, dv), torch.float32, dev)
-    out = {"dq": torch.empty((B, L, H, dk), dtype=dt, device=dev),
-           "dk": torch.empty((B, L, Hk, dk), dtype=dt, device=dev),
-           "dv": torch.empty((B, L, Hk, dv), dtype=dt, device=dev),
-           "dstate": torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)}
+    out = {name: torch.empty_like(t) if t.is_contiguous() else
+           torch.empty(t.shape, dtype=dt, device=dev)
+           for name, t in (("dq", q), ("dk", k), ("dv", v))}
+    like = state if state is not None else dstate
+    out["dstate"] = (torch.empty_like(like) if like is not None else
+                     torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev))
     nbytes = lib().naju_linattn_bwd_workspace_bytes(B, L, H, Hk, dk, dv) if ws is None else 0
     p, nbytes, keep = _linattn_scratch(nbytes, ws, dev)
     check(lib().naju_linattn_bwd(*args, _p(do), _p(dstate), _p(out["dq"]), _p(out["dk"]),

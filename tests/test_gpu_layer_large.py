@@ -88,3 +88,25 @@ def test_single_tokens_of_many_rows():
     first = torch.zeros(3, H, d, d, device=dev())
     fo = nb.linattn_step(q[:3].clone(), k[:3].clone(), v[:3].clone(), a, first)
     assert torch.equal(o[:3], fo) and torch.equal(state[:3], first)
+
+
+@pytest.mark.parametrize("dv", [8, 136, 256])
+def test_most_heads(dv):
+    """2^20 heads in all, in one, two or three parts of the columns each: the last rows give what
+    they give alone (one chunk, so whatever its cut the sums are the same)."""
+    B, L, H, dk, n = 1 << 16, 2, 16, 8, 3
+    print("heads", B * H, dv, flush=True)
+    q, k = (torch.randn(B, L, H, dk, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    v, do = (torch.randn(B, L, H, dv, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    a = torch.linspace(-0.5, 0.0, H, device=dev())
+    o, s = nb.linattn_fwd(q, k, v, a)
+    g = nb.linattn_bwd(q, k, v, a, do)
+    few = [t[-n:].clone() for t in (q, k, v)]
+    fo, fs = nb.linattn_fwd(*few, a)
+    f = nb.linattn_bwd(*few, a, do[-n:].clone())
+    assert torch.equal(o[-n:], fo) and torch.equal(s[-n:], fs)
+    for name in f:
+        assert torch.equal(g[name][-n:], f[name]), name
+    with pytest.raises(nb.NajuError, match="too large"):
+        nb.linattn_fwd(q[:, :, :1].expand(B, L, 17, dk).contiguous(), k[:, :, :1].contiguous(),
+                       v[:, :, :1].contiguous(), torch.zeros(17, device=dev()))
