@@ -603,8 +603,9 @@ naju_status_t naju_linattn_step(int64_t batch, int64_t heads, int64_t kv_heads, 
  * 8-bit floats (e4m3: 4 exponent bits of bias 7, 3 mantissa bits, no infinities),
  * each times the fp32 scale of its 256 consecutive elements (the tensor's last block
  * may be shorter).  A scale is its block's largest magnitude / 448 (0 below 2^-120,
- * and the block then holds zeros); values are rounded to nearest even; p is formed
- * from the unrounded m and v.  Zeros (codes and scales) are the states of a first
+ * and the block then holds zeros); values are rounded to nearest even, but a root that
+ * would be 0 beside a first moment that is not is stored as the smallest code (2^-9 of
+ * its scale); p is formed from the unrounded m and v.  Zeros (codes and scales) are the states of a first
  * step.  A NaN gradient makes its element NaN, one that is infinite or has an infinite
  * square its block's states.
  *   tensors   host array, read during the call only

@@ -7,8 +7,13 @@
 // 8-bit states hold m and sqrt(v) as e4m3 numbers (3 mantissa bits, 2^-9 to 448)
 // times one fp32 scale for every 256 elements, the block's largest magnitude over
 // 448: the root's range is half as many powers of two as v's, which that type
-// holds, and rounding it moves a step's size by at most 2^-4.  The step itself uses
-// the unrounded m and v.
+// holds.  Rounding moves a value by at most 2^-4 of itself down to 2^-6 of the scale
+// (1 / 28672 of the block's largest), and by 2^-10 of the scale below that.  The step
+// itself uses the unrounded m and v.  m may be small against its block where the root
+// is smaller still: a root lost beside a first moment that is kept would leave the next
+// step eps alone to divide by, so there it is stored as the smallest code, 2^-9 of its
+// scale (gradients of 1 beside sparse ones of 1e-5 move the latter by 3 lr at most, in
+// place of 900).
 //
 // Bound by bytes: 28 an element with fp32 gradients and 32-bit states, 16 with
 // 8-bit ones.  A wave takes 256 consecutive elements at a time, 4 a lane, so a
@@ -99,6 +104,14 @@ __device__ __forceinline__ uint32_t encode(const float (&x)[4], float &scale)
     return to_e4m3x4(f);
 }
 
+// the codes of roots with the smallest one in place of each 0 beside a first moment that is not 0
+__device__ __forceinline__ uint32_t keep_roots(uint32_t v, uint32_t m)
+{
+    const uint32_t low = 0x7f7f7f7fu;  // (bits below the sign: a sum past them says not 0)
+    const uint32_t has_m = (m & low) + low, has_v = (v & low) + low;
+    return v | (has_m & ~has_v & ~low) >> 7;
+}
+
 struct AdamCoef {
     float b1, c1, b2, c2, lr, shrink, eps, inv1, bc2, gs;
 };
@@ -187,6 +200,7 @@ template <typename GIO, bool S8> struct Elements {
             float sm, sv;
             cm = encode(mf, sm);
             cv = encode(vf, sv);
+            if (sv > 0.f && sv < INFINITY) cv = keep_roots(cv, cm);
             if (lane == 0) {
                 t.ms_out[b / kBlock8] = sm;
                 t.vs_out[b / kBlock8] = sv;
