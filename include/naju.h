@@ -83,6 +83,9 @@ typedef enum {
 
 typedef enum { NAJU_F32 = 0, NAJU_BF16 = 1 } naju_dtype_t;
 
+/* Added to naju_adamw_step()'s state_bits 8. */
+enum { NAJU_STOCHASTIC = 256 };
+
 typedef enum {
     NAJU_OP_SCAN_FWD = 0,
     NAJU_OP_SCAN_BWD = 1,
@@ -603,10 +606,19 @@ naju_status_t naju_linattn_step(int64_t batch, int64_t heads, int64_t kv_heads, 
  * 8-bit floats (e4m3: 4 exponent bits of bias 7, 3 mantissa bits, no infinities),
  * each times the fp32 scale of its 256 consecutive elements (the tensor's last block
  * may be shorter).  A scale is its block's largest magnitude / 448 (0 below 2^-120,
- * and the block then holds zeros); values are rounded to nearest even, but a root that
- * would be 0 beside a first moment that is not is stored as the smallest code (2^-9 of
- * its scale); p is formed from the unrounded m and v.  Zeros (codes and scales) are the states of a first
- * step.  A NaN gradient makes its element NaN, one that is infinite or has an infinite
+ * and the block then holds zeros); a root that would be 0 beside a first moment that is
+ * not is stored as the smallest code (2^-9 of its scale); p is formed from the unrounded m
+ * and v.  Zeros (codes and scales) are the states of a first step.
+ *   state_bits 8  rounds values to nearest even: each step's states are as near as 8 bits
+ *             come, but a change of less than half a code (3 to 6 %) is lost at every step
+ *             anew.  With beta2 = 0.999 a root falls by 0.05 % a step at most, so only
+ *             its block's largest follows gradients that become smaller.
+ *   state_bits 8 + NAJU_STOCHASTIC  rounds to one of the two neighbouring codes, with
+ *             probabilities that make the stored value right in the mean, so that states
+ *             follow their formulas over the steps: what training is to use.  The random
+ *             numbers are functions of the step's number and the element's index: equal
+ *             calls give equal bits.
+ * A NaN gradient makes its element NaN, one that is infinite or has an infinite
  * square its block's states.
  *   tensors   host array, read during the call only
  *   step      number of this step, from 1; or step_dev, a device int32 that holds it

@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(HERE, "libnaju.so")
 
 OK, EINVAL, EUNSUPPORTED, EWORKSPACE, EHIP = range(5)
 F32, BF16 = 0, 1
+STOCHASTIC = 256  # (with 8-bit optimizer states)
 OP_SCAN_FWD, OP_SCAN_BWD, OP_BLOCK_FWD, OP_BLOCK_BWD = range(4)
 D_CONV = 4
 
@@ -897,13 +898,16 @@ def _one_value(t, name, dtype, dev):
 
 def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
                weight_decay=0.01, *, m_scale=None, v_scale=None, grad_scale=None, copies=None,
-               out=None):
+               out=None, stochastic=False):
     """naju_adamw_step over lists of tensors, all on one device: params fp32; grads of their
     shapes, all fp32 or all bf16; states m, v fp32, or float8_e4m3fn with m_scale, v_scale (fp32
     [ceil(n / 256)]; v then holds the root of the second moment).  Updated in place, or with out
     (a dict of lists p, m, v and, for 8-bit states, m_scale, v_scale) written there.  step: its
     number from 1, or an int32 tensor that holds it; lr: a number or an fp32 tensor; grad_scale:
-    an fp32 tensor or None; copies: bf16 tensors that receive the new parameters, or None."""
+    an fp32 tensor or None; copies: bf16 tensors that receive the new parameters, or None.
+    stochastic: 8-bit states are rounded to one of the two codes around them, right in the mean,
+    as a training over many steps needs; without it to the nearest, where a state that each step
+    changes by less than half a code does not move."""
     n = len(params)
     if n == 0:
         return
@@ -912,7 +916,7 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
         with torch.cuda.device(index):
             return adamw_step(params, grads, m, v, step, lr, beta1, beta2, eps, weight_decay,
                               m_scale=m_scale, v_scale=v_scale, grad_scale=grad_scale,
-                              copies=copies, out=out)
+                              copies=copies, out=out, stochastic=stochastic)
     st = _stream(dev)
     s_dt = m[0].dtype if len(m) else torch.float32
     if s_dt not in (torch.float32, torch.float8_e4m3fn):
@@ -920,6 +924,8 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
     eight = s_dt == torch.float8_e4m3fn
     if eight != (m_scale is not None) or eight != (v_scale is not None):
         raise ValueError("m_scale and v_scale go with 8-bit states")
+    if stochastic and not eight:
+        raise ValueError("stochastic goes with 8-bit states")
     g_dt = grads[0].dtype if len(grads) else torch.float32
     io = _code(g_dt)
     f32 = torch.float32
@@ -961,7 +967,8 @@ def adamw_step(params, grads, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
     step_dev = _one_value(step, "step", torch.int32, dev) if torch.is_tensor(step) else None
     lr_dev = _one_value(lr, "lr", f32, dev) if torch.is_tensor(lr) else None
     gs = _one_value(grad_scale, "grad_scale", f32, dev) if grad_scale is not None else None
-    check(lib().naju_adamw_step(n, table, io, 8 if eight else 32, 0.0 if lr_dev else float(lr),
+    bits = 8 + STOCHASTIC if stochastic else 8 if eight else 32
+    check(lib().naju_adamw_step(n, table, io, bits, 0.0 if lr_dev else float(lr),
                                 beta1, beta2, eps, weight_decay, 0 if step_dev else int(step),
                                 step_dev, lr_dev, gs, st))
 

@@ -15,6 +15,15 @@
 // scale (gradients of 1 beside sparse ones of 1e-5 move the latter by 3 lr at most, in
 // place of 900).
 //
+// Rounded to nearest, a state that a step changes by less than half a code stays where it
+// was, however many steps: a root at b2 = 0.999 cannot fall (gradients that fall to a tenth
+// beside others that do not: 5.4 times its value 4000 steps later, in the median).  The
+// stochastic form rounds up with the probability of the value's distance from the code
+// below, so the mean of what is stored is the value: 1.00 times, eight of ten roots within
+// 25 %.  Its random number is the step's, mixed, plus the element's place in the sequence
+// of the golden ratio's multiples: independent from step to step for each element, and
+// spread evenly over a step's elements, for one addition an element.
+//
 // Bound by bytes: 28 an element with fp32 gradients and 32-bit states, 16 with
 // 8-bit ones.  A wave takes 256 consecutive elements at a time, 4 a lane, so a
 // block of the 8-bit states is one wave's and its maximum a reduction inside the
@@ -24,7 +33,9 @@
 // bisection over the first units of each.
 //
 // 138 M parameters with bf16 gradients and copies 738 us (28 bytes each, 5.2 TB/s, a large
-// copy's rate); 200 M with 8-bit states and fp32 gradients 646 us (16 bytes, 5.0 TB/s).
+// copy's rate); 200 M with 8-bit states and fp32 gradients 642 us (16 bytes, 5.0 TB/s), with
+// stochastic rounding 734 us (4.4 TB/s: 20 instructions an element more, and vector instructions
+// take as long as the loads).
 #include <math.h>
 #include <stdlib.h>
 
@@ -49,8 +60,11 @@ struct AdamTensor {
     float *ms_out, *vs_out;
     bf16 *copy;
     int64_t n;
+    uint32_t at;                          // first element's index in its tensor, low bits
 };
-constexpr int kTensors = 32;              // of a launch: 3.4 KB of the 4 KB of arguments
+constexpr int kTensors = 32;              // of a launch: 3.5 KB of the 4 KB of arguments
+
+enum Store { kF32, kNearest, kStochastic };  // the states' type, and how they are rounded
 
 struct AdamArgs {
     AdamTensor t[kTensors];
@@ -61,8 +75,24 @@ struct AdamArgs {
     float bc1, bc2;                       // 1 - b^t, where the step is the host's
     float ln1, ln2;                       // log of the betas
     const int32_t *step;                  // or null
+    uint32_t step_host;
     const float *lr_dev, *grad_scale;     // or null
 };
+
+// Multiples of the golden ratio's fraction lie evenly in [0, 1), the first n for every n.
+constexpr uint32_t kGolden = 0x9E3779B9u;
+
+// A step's random number, one for each of its two states.  (Products with the fractions of
+// the golden ratio, of sqrt 2 and of sqrt 3; their upper halves folded down in between.)
+__device__ __forceinline__ uint32_t step_noise(uint32_t step, uint32_t which)
+{
+    uint32_t x = (2u * step + which + 1u) * kGolden;
+    x ^= x >> 16;
+    x *= 0x6A09E667u;
+    x ^= x >> 15;
+    x *= 0xBB67AE85u;
+    return x ^ x >> 16;
+}
 
 // v_cvt_*_fp8 converts e4m3 on gfx950, to nearest even
 __device__ __forceinline__ uint32_t to_e4m3x4(const float (&f)[4])
@@ -86,8 +116,19 @@ __device__ __forceinline__ float wave_most(float v)
     return v;
 }
 
-// 4 of a block's values as codes of 8 bits; the scale is the block's
-__device__ __forceinline__ uint32_t encode(const float (&x)[4], float &scale)
+// f, at most kE4m3Most, as one of the two codes' values around it: 20 bits of noise are added to
+// the bits that a code does not hold, which are then cut off.  Below 2^-6 codes lie 2^-9 apart, as
+// they do from 2^-6 on: values are moved up there and back.
+__device__ __forceinline__ float spread(float f, uint32_t noise)
+{
+    const float a = fabsf(f), up = a < 0x1p-6f ? 0x1p-6f : 0.f;
+    const float r = __uint_as_float((__float_as_uint(a + up) + (noise >> 12)) & 0xfff00000u) - up;
+    return f == f ? copysignf(r, f) : f;
+}
+
+// 4 of a block's values as codes of 8 bits; the scale is the block's.  noise: the first one's
+template <bool STOCHASTIC>
+__device__ __forceinline__ uint32_t encode(const float (&x)[4], float &scale, uint32_t noise)
 {
     float most = 0.f;
 #pragma unroll
@@ -100,6 +141,7 @@ __device__ __forceinline__ uint32_t encode(const float (&x)[4], float &scale)
     for (int i = 0; i < 4; ++i) {
         f[i] = x[i] * inv;  // (selects, so that NaN stays)
         f[i] = f[i] > kE4m3Most ? kE4m3Most : f[i] < -kE4m3Most ? -kE4m3Most : f[i];
+        if constexpr (STOCHASTIC) f[i] = spread(f[i], noise + (uint32_t)i * kGolden);
     }
     return to_e4m3x4(f);
 }
@@ -114,6 +156,7 @@ __device__ __forceinline__ uint32_t keep_roots(uint32_t v, uint32_t m)
 
 struct AdamCoef {
     float b1, c1, b2, c2, lr, shrink, eps, inv1, bc2, gs;
+    uint32_t noise_m, noise_v;
 };
 
 __device__ __forceinline__ void adam_element(const AdamCoef &c, float g, float &p, float &m,
@@ -126,7 +169,8 @@ __device__ __forceinline__ void adam_element(const AdamCoef &c, float g, float &
 }
 
 // a lane's 4 elements of a wave's block of 256 from b on; FULL: the tensor has them all
-template <typename GIO, bool S8> struct Elements {
+template <typename GIO, Store ST> struct Elements {
+    static constexpr bool S8 = ST != kF32;
     Run<float, 4> p, m, v;
     Run<GIO, 4> g;
     uint32_t m8, v8;
@@ -198,8 +242,9 @@ template <typename GIO, bool S8> struct Elements {
         uint32_t cm = 0, cv = 0;
         if constexpr (S8) {
             float sm, sv;
-            cm = encode(mf, sm);
-            cv = encode(vf, sv);
+            const uint32_t place = (t.at + (uint32_t)e) * kGolden;
+            cm = encode<ST == kStochastic>(mf, sm, c.noise_m + place);
+            cv = encode<ST == kStochastic>(vf, sv, c.noise_v + place);
             if (sv > 0.f && sv < INFINITY) cv = keep_roots(cv, cm);
             if (lane == 0) {
                 t.ms_out[b / kBlock8] = sm;
@@ -234,7 +279,7 @@ template <typename GIO, bool S8> struct Elements {
     }
 };
 
-template <typename GIO, bool S8>
+template <typename GIO, Store ST>
 __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a)
 {
     // the tensor that holds this workgroup's unit
@@ -249,7 +294,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t e0 = (int64_t)(blockIdx.x - a.first[lo]) * kUnit + wave * 256;
 
-    AdamCoef c{a.b1, a.c1, a.b2, a.c2, a.lr, 0.f, a.eps, 0.f, a.bc2, 1.f};
+    AdamCoef c{a.b1, a.c1, a.b2, a.c2, a.lr, 0.f, a.eps, 0.f, a.bc2, 1.f, 0u, 0u};
     float bc1 = a.bc1;
     if (a.lr_dev != nullptr) c.lr = *a.lr_dev;
     if (a.grad_scale != nullptr) c.gs = *a.grad_scale;
@@ -258,12 +303,17 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a)
         bc1 = -expm1f(s * a.ln1);
         c.bc2 = -expm1f(s * a.ln2);
     }
+    if constexpr (ST == kStochastic) {
+        const uint32_t n = a.step != nullptr ? (uint32_t)*a.step : a.step_host;
+        c.noise_m = step_noise(n, 0);
+        c.noise_v = step_noise(n, 1);
+    }
     c.inv1 = 1.f / bc1;
     c.shrink = 1.f - c.lr * a.wd;
 
     constexpr int J = kUnit / 1024;  // blocks of 256 elements of a wave
     if (e0 - wave * 256 + kUnit <= t.n) {
-        Elements<GIO, S8> x[J];
+        Elements<GIO, ST> x[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) x[j].template load<true>(t, e0 + j * 1024, lane);
 #pragma unroll
@@ -274,7 +324,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a)
     for (int j = 0; j < J; ++j) {
         const int64_t b = e0 + j * 1024;
         if (b >= t.n) break;
-        Elements<GIO, S8> x;
+        Elements<GIO, ST> x;
         if (b + 256 <= t.n) {
             x.template load<true>(t, b, lane);
             x.template step<true>(t, b, lane, c);
@@ -286,6 +336,14 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a)
 }
 
 // ---------------------------------------------------------------------- host
+template <typename GIO> static void launch(const AdamArgs &a, unsigned units, Store st, hipStream_t s)
+{
+    if (st == kF32) hipLaunchKernelGGL((adamw_kernel<GIO, kF32>), dim3(units), dim3(256), 0, s, a);
+    else if (st == kNearest)
+        hipLaunchKernelGGL((adamw_kernel<GIO, kNearest>), dim3(units), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((adamw_kernel<GIO, kStochastic>), dim3(units), dim3(256), 0, s, a);
+}
+
 static int by_address(const void *a, const void *b)
 {
     const naju_adamw_tensor_t *x = *(naju_adamw_tensor_t *const *)a;
@@ -309,8 +367,9 @@ extern "C" naju_status_t naju_adamw_step(int64_t n_tensors, const naju_adamw_ten
     if (n_tensors > (1 << 24)) return fail(NAJU_EINVAL, "n_tensors (2^24 max) too large");
     if (g_io != NAJU_F32 && g_io != NAJU_BF16)
         return fail(NAJU_EINVAL, "io dtype %d is neither NAJU_F32 nor NAJU_BF16", (int)g_io);
-    if (state_bits != 32 && state_bits != 8)
-        return fail(NAJU_EUNSUPPORTED, "state_bits %d is neither 32 nor 8", (int)state_bits);
+    if (state_bits != 32 && state_bits != 8 && state_bits != 8 + NAJU_STOCHASTIC)
+        return fail(NAJU_EUNSUPPORTED, "state_bits %d is neither 32 nor 8 nor 8 + NAJU_STOCHASTIC",
+                    (int)state_bits);
     if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1))
         return fail(NAJU_EINVAL, "beta1 and beta2 must lie in [0, 1)");
     if (!(eps >= 0) || eps > 1e30) return fail(NAJU_EINVAL, "eps must be finite and not negative");
@@ -323,7 +382,8 @@ extern "C" naju_status_t naju_adamw_step(int64_t n_tensors, const naju_adamw_ten
     NAJU_TRY(opt(grad_scale, "grad_scale", 4));
     if (n_tensors == 0) return NAJU_OK;
     NAJU_TRY(need(tensors, "tensors", 8));
-    const bool s8 = state_bits == 8;
+    const Store store = state_bits == 32 ? kF32 : state_bits == 8 ? kNearest : kStochastic;
+    const bool s8 = store != kF32;
     const size_t eg = g_io == NAJU_F32 ? 4 : 2, es = s8 ? 1 : 4;
     for (int64_t i = 0; i < n_tensors; ++i) {
         const naju_adamw_tensor_t &t = tensors[i];
@@ -381,6 +441,7 @@ extern "C" naju_status_t naju_adamw_step(int64_t n_tensors, const naju_adamw_ten
         a.bc2 = (float)-expm1((double)step * log(beta2));
     }
     a.step = step_dev;
+    a.step_host = (uint32_t)step;
     a.lr_dev = lr_dev;
     a.grad_scale = grad_scale;
     hipStream_t st = (hipStream_t)stream;
@@ -398,6 +459,7 @@ extern "C" naju_status_t naju_adamw_step(int64_t n_tensors, const naju_adamw_ten
                 const int64_t end = (done + now) * kUnit;
                 AdamTensor &o = a.t[a.count];
                 o.n = (end < t.n ? end : t.n) - e;
+                o.at = (uint32_t)e;
                 o.p = t.p + e;
                 o.g = (const char *)t.g + e * (int64_t)eg;
                 o.m = (const char *)t.m + e * (int64_t)es;
@@ -423,17 +485,8 @@ extern "C" naju_status_t naju_adamw_step(int64_t n_tensors, const naju_adamw_ten
             }
         }
         if (units == 0) break;
-        if (g_io == NAJU_F32) {
-            if (s8) hipLaunchKernelGGL((adamw_kernel<float, true>), dim3((unsigned)units), dim3(256),
-                                       0, st, a);
-            else hipLaunchKernelGGL((adamw_kernel<float, false>), dim3((unsigned)units), dim3(256),
-                                    0, st, a);
-        } else {
-            if (s8) hipLaunchKernelGGL((adamw_kernel<bf16, true>), dim3((unsigned)units), dim3(256),
-                                       0, st, a);
-            else hipLaunchKernelGGL((adamw_kernel<bf16, false>), dim3((unsigned)units), dim3(256),
-                                    0, st, a);
-        }
+        if (g_io == NAJU_F32) launch<float>(a, (unsigned)units, store, st);
+        else launch<bf16>(a, (unsigned)units, store, st);
         NAJU_TRY(hip_status(hipGetLastError(), "AdamW launch"));
     }
     return NAJU_OK;
