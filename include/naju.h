@@ -538,8 +538,10 @@ naju_status_t naju_res_norm_bwd(int64_t tokens, int64_t d_model, int32_t io, int
  *     S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
  *   q         [batch][seqlen][heads][d_key] io, k [..][kv_heads][d_key], v
  *             [..][kv_heads][d_value]; ldq, ldk, ldv: elements from one token to
- *             the next (parts of a joint projection), a multiple of 16 bytes; heads
- *             h of q read the key and value of head h / (heads / kv_heads)
+ *             the next (parts of a joint projection), a multiple of 16 bytes, 2^20 at
+ *             most; rows of the batch lie seqlen times as far apart (seqlen 1: up to
+ *             2^40, the last token of longer rows).  Heads h of q read the key and
+ *             value of head h / (heads / kv_heads)
  *   log_decay [heads] fp32, at most 0 (-inf: only the token itself); a constant of
  *             the head, to which there is no gradient
  *   state     [batch][heads][d_key][d_value] fp32 before the first token, or NULL

@@ -68,6 +68,7 @@ struct LinJob {
     const float *enter;      // states entering the segments, or the first; null: zeros
     float *leave;            // segments' contributions, or the last state; may be null
     int64_t ldq, ldk, ldv, ldo;         // elements from token to token
+    int64_t bq, bk, bv;                 // from batch row to batch row
     int64_t enter_bh, enter_seg, leave_bh, leave_seg;
     int enter_r, enter_c, leave_r, leave_c;  // element (row, column) of a state
     int D1, D2;              // rows (q's and k's elements) and columns (v's) of the state
@@ -330,9 +331,9 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
     a2 = (a2 < -1e30f ? -1e30f : a2) * kLog2e;
 
     const int64_t ldq = J.ldq, ldk = J.ldk, ldv = J.ldv;
-    const T *q = (const T *)J.q + (int64_t)b * L * ldq + (int64_t)(hd / J.gq) * D1;
-    const T *k = (const T *)J.k + (int64_t)b * L * ldk + (int64_t)(hd / J.gk) * D1;
-    const T *v = (const T *)J.v + (int64_t)b * L * ldv + (int64_t)(hd / J.gv) * J.D2 + c0;
+    const T *q = (const T *)J.q + (int64_t)b * J.bq + (int64_t)(hd / J.gq) * D1;
+    const T *k = (const T *)J.k + (int64_t)b * J.bk + (int64_t)(hd / J.gk) * D1;
+    const T *v = (const T *)J.v + (int64_t)b * J.bv + (int64_t)(hd / J.gv) * J.D2 + c0;
     const uint32_t out_row = (uint32_t)J.ldo * (wide_out ? 4u : 2u);  // bytes
     char *out = (char *)J.o + (int64_t)b * L * out_row +
                 ((int64_t)hd * J.D2 + c0) * (wide_out ? 4 : 2);
@@ -882,14 +883,20 @@ static naju_status_t check_lin(int64_t B, int64_t L, int64_t H, int64_t Hk, int6
     return NAJU_OK;
 }
 
-static naju_status_t check_ld(int64_t ld, int64_t least, size_t e, const char *name)
+// (one token a row: the rows' distance, which no chunk spans)
+static naju_status_t check_ld(int64_t ld, int64_t least, int64_t L, size_t e, const char *name)
 {
-    if (ld < least || ld > kLinStride || ld * (int64_t)e % 16 != 0)
+    const int64_t most = L == 1 ? (int64_t)1 << 40 : kLinStride;
+    if (ld < least || ld > most || ld * (int64_t)e % 16 != 0)
         return fail(NAJU_EINVAL, "token stride of %s (%lld) must be from %lld to %lld elements and a "
                                  "multiple of 16 bytes",
-                    name, (long long)ld, (long long)least, (long long)kLinStride);
+                    name, (long long)ld, (long long)least, (long long)most);
     return NAJU_OK;
 }
+
+// The kernel's tokens lie in chunks, and its rows where J.bq, .. say: with one token a row the
+// distance from token to token is that of a contiguous one.
+static int64_t token_ld(int64_t ld, int64_t least, int64_t L) { return L == 1 ? least : ld; }
 
 // the walks g.job[from] .. g.job[to - 1]
 static hipError_t walk(LinArgs g, int from, int to, const LinPlan &p, int32_t io, bool wide_out,
@@ -971,9 +978,9 @@ naju_status_t naju_linattn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int
     if (batch == 0 || heads == 0) return NAJU_OK;
     const size_t e = io == NAJU_F32 ? 4 : 2;
     if (seqlen > 0) {
-        NAJU_TRY(check_ld(ldq, heads * d_key, e, "q"));
-        NAJU_TRY(check_ld(ldk, kv_heads * d_key, e, "k"));
-        NAJU_TRY(check_ld(ldv, kv_heads * d_value, e, "v"));
+        NAJU_TRY(check_ld(ldq, heads * d_key, seqlen, e, "q"));
+        NAJU_TRY(check_ld(ldk, kv_heads * d_key, seqlen, e, "k"));
+        NAJU_TRY(check_ld(ldv, kv_heads * d_value, seqlen, e, "v"));
         NAJU_TRY(need(q, "q", 16));
         NAJU_TRY(need(k, "k", 16));
         NAJU_TRY(need(v, "v", 16));
@@ -1002,10 +1009,13 @@ naju_status_t naju_linattn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int
     J.k = k;
     J.v = v;
     J.o = o;
-    J.ldq = ldq;
-    J.ldk = ldk;
-    J.ldv = ldv;
+    J.ldq = token_ld(ldq, heads * d_key, seqlen);
+    J.ldk = token_ld(ldk, kv_heads * d_key, seqlen);
+    J.ldv = token_ld(ldv, kv_heads * d_value, seqlen);
     J.ldo = heads * d_value;
+    J.bq = seqlen * ldq;
+    J.bk = seqlen * ldk;
+    J.bv = seqlen * ldv;
     J.enter = state;
     J.enter_bh = n;
     J.enter_r = (int)d_value;
@@ -1053,9 +1063,9 @@ naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int
     if (batch == 0 || heads == 0) return NAJU_OK;
     const size_t e = io == NAJU_F32 ? 4 : 2;
     if (seqlen > 0) {
-        NAJU_TRY(check_ld(ldq, heads * d_key, e, "q"));
-        NAJU_TRY(check_ld(ldk, kv_heads * d_key, e, "k"));
-        NAJU_TRY(check_ld(ldv, kv_heads * d_value, e, "v"));
+        NAJU_TRY(check_ld(ldq, heads * d_key, seqlen, e, "q"));
+        NAJU_TRY(check_ld(ldk, kv_heads * d_key, seqlen, e, "k"));
+        NAJU_TRY(check_ld(ldv, kv_heads * d_value, seqlen, e, "v"));
         NAJU_TRY(need(q, "q", 16));
         NAJU_TRY(need(k, "k", 16));
         NAJU_TRY(need(v, "v", 16));
@@ -1084,16 +1094,23 @@ naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int
     g.slices = p.slices;
     g.nseg = p.nseg;
     g.seg = p.seg;
-    const int64_t ldg = heads * d_value;
+    const int64_t ldg = heads * d_value, bg = seqlen * ldg;
+    const int64_t bq = seqlen * ldq, bk = seqlen * ldk, bv = seqlen * ldv;
+    ldq = token_ld(ldq, heads * d_key, seqlen);
+    ldk = token_ld(ldk, kv_heads * d_key, seqlen);
+    ldv = token_ld(ldv, kv_heads * d_value, seqlen);
     // dq: the forward's state transposed, from dout, v and k
     LinJob &A = g.job[0];
     A.q = dout;
     A.ldq = ldg;
+    A.bq = bg;
     A.gq = 1;
     A.k = v;
     A.ldk = ldv;
+    A.bk = bv;
     A.v = k;
     A.ldv = ldk;
+    A.bv = bk;
     A.gk = A.gv = group;
     A.o = dq;
     A.ldo = heads * d_key;
@@ -1110,11 +1127,14 @@ naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int
     LinJob &V = g.job[1];
     V.q = k;
     V.ldq = ldk;
+    V.bq = bk;
     V.gq = group;
     V.k = q;
     V.ldk = ldq;
+    V.bk = bq;
     V.v = dout;
     V.ldv = ldg;
+    V.bv = bg;
     V.gk = V.gv = 1;
     V.o = group > 1 ? (void *)(base + p.off_dv) : dv;
     V.ldo = heads * d_value;
@@ -1148,10 +1168,13 @@ naju_status_t naju_linattn_bwd(int64_t batch, int64_t seqlen, int64_t heads, int
     K = V;
     K.q = v;
     K.ldq = ldv;
+    K.bq = bv;
     K.k = dout;
     K.ldk = ldg;
+    K.bk = bg;
     K.v = q;
     K.ldv = ldq;
+    K.bv = bq;
     K.o = group > 1 ? (void *)(base + p.off_dk) : dk;
     K.ldo = heads * d_key;
     K.D1 = (int)d_value;
