@@ -74,21 +74,21 @@ def _compile_tensors() -> None:
 
 def build(verbose: bool = False) -> str:
     """Compile every HIP source, link libnaju.so, and compile _tensors.so.  Returns the path of
-    libnaju.so."""
+    libnaju.so, which is there also where _tensors.so fails (that error is raised behind it)."""
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         tensors = ex.submit(_compile_tensors)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        tmp = LIB + ".tmp%d" % os.getpid()
+        # (hipBLASLt runs the mixer layer's projections)
+        cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs + [
+            "-L/opt/rocm/lib", "-lhipblaslt", "-Wl,-rpath,/opt/rocm/lib"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError("link failed:\n%s" % r.stderr)
+        os.replace(tmp, LIB)
+        for o in objs:
+            os.remove(o)
         tensors.result()
-    tmp = LIB + ".tmp%d" % os.getpid()
-    # (hipBLASLt runs the mixer layer's projections)
-    cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs + [
-        "-L/opt/rocm/lib", "-lhipblaslt", "-Wl,-rpath,/opt/rocm/lib"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s" % r.stderr)
-    os.replace(tmp, LIB)
-    for o in objs:
-        os.remove(o)
     return LIB
 
 
