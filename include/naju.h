@@ -552,8 +552,9 @@ naju_status_t naju_res_norm_bwd(int64_t tokens, int64_t d_model, int32_t io, int
  *   ws        naju_linattn_fwd_workspace_bytes() bytes, 256-byte aligned (no initial
  *             contents needed; 0 bytes: may be NULL)
  * d_key, d_value multiples of 8 from 8 to 256; q, k, v, o (and the gradients) 16-byte
- * aligned.  Sums and states are fp32.  A NaN or infinite input reaches o from up to 63
- * tokens before it on, in its own row and the heads that read it.
+ * aligned.  Sums and states are fp32; bf16 products with a state and with the scores of a
+ * chunk's tokens take 16 bits of these (two bf16 parts).  A NaN or infinite input reaches
+ * what the formula says, an infinity also as NaN.
  */
 size_t naju_linattn_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
                                         int64_t kv_heads, int64_t d_key, int64_t d_value);
@@ -573,8 +574,7 @@ naju_status_t naju_linattn_fwd(int64_t batch, int64_t seqlen, int64_t heads, int
  *             its readers)
  *   dstate    [batch][heads][d_key][d_value] fp32 (written), or NULL
  *   ws        naju_linattn_bwd_workspace_bytes() bytes, as for the forward
- * A NaN or infinite input reaches dq from up to 63 tokens before it on, dk and dv from
- * up to 63 tokens behind it back, in its own row and the heads that share it.
+ * A NaN or infinite input reaches what the formulas say, an infinity also as NaN.
  */
 size_t naju_linattn_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
                                         int64_t kv_heads, int64_t d_key, int64_t d_value);

@@ -61,6 +61,13 @@ constexpr int kLinThreads = 256;
 constexpr int64_t kLinStride = (int64_t)1 << 20;  // elements from token to token: a chunk's tokens
                                                   // span 2^28 bytes at most
 
+// A number as if it were new: what was formed from it before is not kept in registers for later.
+__device__ __forceinline__ int anew(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // One walk.  The names are the forward's: q reads, k and v are summed into the state.
 struct LinJob {
     const void *q, *k, *v;
@@ -267,6 +274,23 @@ template <typename T, int ROWS, int COLS> struct Stage {
             r[i] = __builtin_amdgcn_raw_buffer_load_b128(b, (int)at, 0, 0);
         }
     }
+    // zeros in place of what is neither a number nor finite; from[c]: the first row where column c
+    // had it, and what was there before if that is less
+    __device__ __forceinline__ void clean(int *from, int tid)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int at = e * (int)sizeof(T) / 4;
+                const uint32_t own = sizeof(T) == 4 ? ~0u : e % 2 ? 0xffff0000u : 0xffffu;
+                const uint32_t exponent = 0x7f807f80u & own & (sizeof(T) == 4 ? 0x7f800000u : ~0u);
+                if ((r[i][at] & exponent) == exponent) {
+                    r[i][at] &= ~own;
+                    atomicMin(from + tid % kPerRow * E + e, tid / kPerRow + i * kRows);
+                }
+            }
+    }
     __device__ __forceinline__ void put(T *lds, int tid) const
     {
         T *to = lds + tid / kPerRow * kStride + tid % kPerRow * E;
@@ -286,30 +310,42 @@ template <typename T, int KD, int CT> struct LinShape {
     static constexpr size_t bytes(bool out)
     {
         return sizeof(T) * ((out ? 2 : 1) * TT * SK::kStride + TT * SV::kStride +
-                            (out ? kParts * TT * kScores : 0));
+                            (out ? kParts * TT * kScores : 0)) +
+               (out ? sizeof(int) * VC : 0);
     }
 };
 
-// OT: the outputs' type; void: none, a segment's contribution to the state alone.
+// One workgroup's walk.  OT: the outputs' type; void: none, a segment's contribution to the state
+// alone.  Returns whether it has to be done again with care.
+//
+// A score of 0 times a value that is not finite is NaN, which so reaches the tokens before it in
+// its chunk.  In the state such a value leaves its whole column not finite for good: one look at it
+// behind the walk tells, and then the walk is done again: with care, each chunk's bad values are
+// taken as 0, and the outputs of their columns from the first of them on are NaN, as is the
+// column's last state.  (The loop has nothing of it but one branch behind a barrier, where few
+// registers hold anything: 3 % slower to 5 % faster than without it, by what the scheduler makes of
+// each form.  Looked for in each chunk's products, or in a second form of the walk in the same
+// kernel, it made heads of 128 15 to 25 % slower, in registers that spill.)
 template <typename T, int KD, int CT, typename OT>
-__global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel(const LinArgs g)
+__device__ __forceinline__ bool linattn_walk(const LinArgs &g, char *lds, const bool care)
 {
     using Sh = LinShape<T, KD, CT>;
     constexpr bool OUT = !__is_same(OT, void), wide_out = __is_same(OT, float);
     constexpr int TT = Sh::TT, VC = Sh::VC, IT = TT / 16, KS = TT / 32, KB = KD / 32;
     constexpr int QS = Sh::SK::kStride, VS = Sh::SV::kStride, PS = Sh::kScores;
-    extern __shared__ __attribute__((aligned(16))) char lds[];
     T *vs = (T *)lds, *ks = vs + TT * VS, *qs = ks + TT * QS;
     T *ps = qs + TT * QS;  // [parts][TT][PS]
+    int *from = (int *)(ps + Sh::kParts * TT * PS);  // [VC] first token whose value is bad
 
-    const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, h4 = lane >> 4;
+    const int tid = anew(threadIdx.x);
+    const int lane = tid & 63, m = lane & 15, h4 = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // jobs of the same segment run on the same XCD (workgroups go round robin over 8 of them)
     int id = blockIdx.x;
     const int jobs = g.jobs;
     const int job = id / 8 % jobs;
     id = id / (8 * jobs) * 8 + id % 8;
-    if (id >= g.items) return;
+    if (id >= g.items) return false;
     const LinJob &J = g.job[job];
     const int slice = id % g.slices;
     id /= g.slices;
@@ -317,7 +353,7 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
     id /= g.nseg;
     const int hd = id % g.H, b = id / g.H;
     const int c0 = slice * VC;
-    if (c0 >= J.D2) return;
+    if (c0 >= J.D2) return false;
     const int D1 = J.D1, D2 = J.D2 - c0 < VC ? J.D2 - c0 : VC;  // of this workgroup
     const int64_t L = g.L;
     int len_i = g.lengths != nullptr ? g.lengths[b] : (int)L;
@@ -340,10 +376,13 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
 
     // this lane's columns of the state: 4 CT neighbouring lanes' tiles interleave, so that a
     // lane's outputs of one token are 4 CT consecutive elements
-    auto column = [&](int ct) { return 16 * CT * w + 4 * CT * (m >> 2) + 4 * ct + (m & 3); };
+    auto column = [&](int m, int ct) {
+        return 16 * CT * w + 4 * CT * (m >> 2) + 4 * ct + (m & 3);
+    };
     // rows of the state: register r of tile kt is row 16 kt + 4 h4 + r
     f32x4 S[CT][2 * KB];
     {
+        const int ln = anew(lane), m = ln & 15, h4 = ln >> 4;
         const float *e = J.enter;
         if (e != nullptr)
             e += (int64_t)(b * g.H + hd) * J.enter_bh + (int64_t)seg * J.enter_seg;
@@ -354,7 +393,7 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = 16 * kt + 4 * h4 + r;
-                    const int col = column(ct);
+                    const int col = column(m, ct);
                     float s = 0.f;
                     if (OUT && e != nullptr && row < D1 && col < D2)
                         s = e[(int64_t)row * J.enter_r + (int64_t)(c0 + col) * J.enter_c];
@@ -414,9 +453,31 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
     if (ocol >= D2) ooff = kPast;
     const uint32_t ostep = (back ? -16u : 16u) * out_row;
 
+    // with care: the bad outputs of the chunk at n0 (by the lane that stored them)
+    auto patch = [&](int64_t n0) {
+        const int there = stop - n0 < TT ? (int)(stop - n0) : TT;
+        const int ln = anew(lane), from_c = 16 * CT * w + 4 * CT * (ln >> 4);
+#pragma unroll 1
+        for (int c = from_c; c < from_c + 4 * CT && c < D2; ++c)
+#pragma unroll 1
+            for (int i = ln & 15; i < there; i += 16) {
+                if (i < from[c]) continue;
+                const int64_t t = back ? len - 1 - n0 - i : n0 + i;
+                if constexpr (wide_out) *(float *)(out + t * out_row + c * 4) = NAN;
+                else *(bf16 *)(out + t * out_row + c * 2) = (bf16)0x7fc0;
+            }
+    };
     if (first < stop) fetch(first);
     for (int64_t n0 = first; n0 < stop; n0 += TT) {
         __syncthreads();  // (the chunk before has been read)
+        if (OUT && __builtin_expect(care, 0)) {
+            if (n0 > first) patch(n0 - TT);
+            __syncthreads();
+            const int c = anew(tid);
+            if (c < VC) from[c] = n0 > first && from[c] < TT ? 0 : TT;
+            __syncthreads();
+            rv.clean(from, c);
+        }
         if constexpr (OUT) rq.put(qs, tid);
         rk.put(ks, tid);
         rv.put(vs, tid);
@@ -485,7 +546,7 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
                     fv[ct][s].cols(vs + (32 * s + 4 * h4 + (m >> 2)) * VS + 16 * CT * w +
                                        4 * CT * (m & 3) + 4 * ct, VS);
                 else
-                    fv[ct][s].cols(vs + (32 * s + 4 * h4) * VS + column(ct), VS);
+                    fv[ct][s].cols(vs + (32 * s + 4 * h4) * VS + column(m, ct), VS);
             }
 
         if constexpr (OUT) {
@@ -592,6 +653,19 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
     }
 
     if constexpr (OUT) {
+        if (care) {
+            if (first < stop) patch(first + (stop - 1 - first) / TT * TT);
+        } else if (first < stop) {
+            // (one row of the state says it for all: no key makes a bad value good)
+            float sum = 0.f;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) sum = __builtin_fmaf(S[ct][0][0], 0.f, sum);
+            const bool bad = __builtin_amdgcn_ballot_w64(sum != 0.f) != 0;
+            if (lane == 0) from[w] = bad;
+            __syncthreads();
+            const int again = from[0] | from[1] | from[2] | from[3];
+            if (__builtin_expect(__builtin_amdgcn_readfirstlane(again) != 0, 0)) return true;
+        }
         // rows behind a sequence's last token
         const int64_t z0 = first > len ? first : len;
         if (z0 < end) {
@@ -605,7 +679,8 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
             }
         }
     }
-    if (J.leave == nullptr || (OUT && seg != g.nseg - 1)) return;
+    if (J.leave == nullptr || (OUT && seg != g.nseg - 1)) return false;
+    const int ln = anew(lane);
     float *e = J.leave + (int64_t)(b * g.H + hd) * J.leave_bh + (int64_t)seg * J.leave_seg;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct)
@@ -613,10 +688,20 @@ __global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel
         for (int kt = 0; kt < 2 * KB; ++kt)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = 16 * kt + 4 * h4 + r, col = column(ct);
+                const int row = 16 * kt + 4 * (ln >> 4) + r, col = column(ln & 15, ct);
                 if (row < D1 && col < D2)
-                    e[(int64_t)row * J.leave_r + (int64_t)(c0 + col) * J.leave_c] = S[ct][kt][r];
+                    e[(int64_t)row * J.leave_r + (int64_t)(c0 + col) * J.leave_c] =
+                        OUT && care && from[col] < TT ? NAN : S[ct][kt][r];
             }
+    return false;
+}
+
+template <typename T, int KD, int CT, typename OT>
+__global__ __launch_bounds__(kLinThreads, KD <= 128 ? 2 : 1) void linattn_kernel(const LinArgs g)
+{
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    bool care = false;
+    while (linattn_walk<T, KD, CT, OT>(g, lds, care)) care = true;  // (twice at most)
 }
 
 // Segments' contributions -> the states that enter them, in place: [B H][nseg][D1 D2].
