@@ -502,7 +502,8 @@ naju_status_t naju_w4_quantize(int64_t d_in, int64_t d_out, int64_t group, int32
  *   xn        [tokens][d_model] io (written), or NULL with w_pre
  * io BF16 with x_io BF16 or F32, or both F32.  d_model 4 to 8192.  eps >= 0.
  * Squares are summed as they are: a row whose sum of squares leaves fp32 (values
- * of 1e17 and more) has the norm 0, a row that holds NaN or infinity has NaN.
+ * of 1e17 and more) has the norm 0, a row that holds NaN or infinity has NaN.  With
+ * eps 0 a row of zeros has NaN, one whose squares vanish (values below 1e-22) infinities.
  */
 naju_status_t naju_res_norm_fwd(int64_t tokens, int64_t d_model, int32_t io, int32_t x_io,
                                 const void *x, const void *y, const void *z, const float *scale,

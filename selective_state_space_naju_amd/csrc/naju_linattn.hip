@@ -32,11 +32,12 @@
 //
 // Bound by a chunk's length in time: its loads, two barriers and three rounds of
 // products follow one another, and registers leave room for two workgroups a CU to
-// cover that.  8 x 2048 x 64 heads x 128 (a full chip) forward 282 us, 3.8 TB/s of its
-// inputs and outputs; few heads are cut into segments, which read k and v twice: 65536
-// x 16 x 128 forward 418 us (2.6 TB/s), 8 x 2048 x 12 x 128 gradient 219 us (its three
-// walks and their segments read 9 tensors where 4 are needed); fp32 3 x 333 x 5 heads of 40
-// and 72 forward 17 us in a graph.  Not faster in the same place: eight waves of 16 columns (330 us, one
+// cover that.  8 x 2048 x 64 heads x 128 (a full chip) forward 290 us, 3.7 TB/s of its
+// inputs and outputs; few heads are cut into segments, which read k and v twice (both
+// times from beyond L2, by counter): 65536 x 16 x 128 forward 422 us (2.5 TB/s), 8 x 2048 x
+// 12 x 128 gradient 224 us (its three walks read 348 MB from beyond L2, the four tensors
+// once are 201); fp32 3 x 333 x 5 heads of 40 and 72 forward 17 us in a graph.  Not faster in
+// the same place (the base there 282 us, or as given): eight waves of 16 columns (330 us, one
 // workgroup a CU), LDS reads a step ahead of the products (345, one workgroup a CU; two
 // spill), splitting values by hand between the products (334), loads that bypass the
 // caches (332 to 341).
@@ -864,13 +865,14 @@ struct LinPlan {
 // of a walk, 0.45 with 64 columns; the launches and the joining 1, 1.5 with keys up to 64, whose
 // chunks are shorter, and 0.1 a segment.  Measured against other choices, the rule's in brackets (us,
 // columns x segments).  Forward, heads of 128: 8 rows x 2048 tokens x 12 heads 128x1: 150, [128x4:
-// 110], 128x5: 106, 64x1: 122, 64x4: 122; 4 x 2048 x 64 [128x1: 177], 64x1: 182, 128x2: 206; 65536 x
-// 16 128x16: 496, [128x32: 451], 64x32: 532; 2 x 4096 x 32 64x4: 134, [128x8: 123], 128x1: 292; 2048
-// x 4 128x16: 37, 64x8: 36, [64x16: 30]; heads of 256, 4 x 1024 x 16 [64x1: 104], 128x1: 144; heads
-// of 64, 2 x 4096 x 8 1: 135, 8: 39, [16: 30], 24: 31; fp32, 3 x 333 x 5 heads of 40 and 72 128x6: 22,
-// [64x6: 17], 64x1: 30.  Gradient: 8 x 2048 x 12 [128x1: 228], 128x3: 222, 64x1: 270; 2 x 4096 x 32
-// 128x1: 298, 128x4: 269, [64x1: 309]; 1000 x 12 128x6: 44, [64x6: 38], 64x1: 60; heads of 256, 4 x
-// 1024 x 16 [128x1: 263], 64x1: 294, 128x2: 351.
+// 112], 128x5: 102, 64x1: 111, 64x4: 115; 4 x 2048 x 64 [128x1: 165], 64x1: 179, 128x2: 195; 65536 x
+// 16 128x16: 449, [128x32: 421], 64x32: 514; 2 x 4096 x 32 64x4: 133, [128x8: 121], 128x1: 286; 2048
+// x 4 128x16: 37, 64x8: 35, [64x16: 29]; heads of 256, 4 x 1024 x 16 [64x1: 105], 128x1: 134; heads
+// of 64, 2 x 4096 x 8 1: 138, 8: 39, [16: 30], 24: 32; fp32, 3 x 333 x 5 heads of 40 and 72 128x6: 22,
+// [64x6: 17], 64x1: 29.  Gradient: 8 x 2048 x 12 [128x1: 214], 128x3: 208, 64x1: 251; 2 x 4096 x 32
+// 128x1: 297, 128x4: 257, [64x1: 308]; 1000 x 12 128x6: 44, [64x6: 39], 64x1: 58; heads of 256, 4 x
+// 1024 x 16 [128x1: 252], 64x1: 296, 128x2: 308.  So it misses by up to a fifth: it averages over the
+// CUs where the fullest one ends the call, and takes a chunk of fp32 for one of bf16.
 static double lin_rounds(int64_t groups, bool wide, int rows)
 {
     const double lone = wide ? 1. : 0.7, two = rows > 128 ? 2. * lone : wide ? 1.8 : 1.05;
