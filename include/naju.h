@@ -620,7 +620,7 @@ naju_status_t naju_linattn_step(int64_t batch, int64_t heads, int64_t kv_heads, 
  *             probabilities that make the stored value right in the mean, so that states
  *             follow their formulas over the steps: what training is to use.  The random
  *             numbers are functions of the step's number and the element's index: equal
- *             calls give equal bits.
+ *             calls give equal bits (so replays of a captured call need step_dev).
  * A NaN gradient makes its element NaN, one that is infinite or has an infinite
  * square its block's states.
  *   tensors   host array, read during the call only
