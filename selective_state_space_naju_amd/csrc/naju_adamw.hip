@@ -34,8 +34,8 @@
 //
 // 138 M parameters with bf16 gradients and copies 738 us (28 bytes each, 5.2 TB/s, a large
 // copy's rate); 200 M with 8-bit states and fp32 gradients 642 us (16 bytes, 5.0 TB/s), with
-// stochastic rounding 734 us (4.4 TB/s: 20 instructions an element more, and vector instructions
-// take as long as the loads).
+// stochastic rounding 734 us (4.4 TB/s: 23 vector instructions an element on top of 118, four cycles
+// of a SIMD each, which then take longer than the loads).
 #include <math.h>
 #include <stdlib.h>
 
